@@ -1,4 +1,10 @@
-"""A differentiable KDA chunked forward for PyTorch training code.
+"""Differentiable KDA operators for PyTorch training code.
+
+``kda_chunk`` is the chunked forward; ``kda_glr`` the gated linear recurrence,
+``kda_short_conv`` the short causal convolution and ``kda_qk_norm_rope`` the
+norm and rotation of queries and keys.  Each allocates its outputs and
+workspaces with PyTorch and calls the library's entry points for both
+directions; without a gradient to compute they are the inference calls too.
 
 ``kda_chunk`` allocates the outputs and workspaces with PyTorch and calls the
 library's ``kda_fwd`` in the forward and ``kda_bwd`` in the backward; it adds
@@ -10,10 +16,13 @@ from __future__ import annotations
 
 import torch
 
-from . import (FLAG_KEEP_RECORDS, FLAG_REUSE_RECORDS, kda_bwd_ex, kda_bwd_workspace_size, kda_fwd_ex,
-               kda_workspace_size)
+from . import (FLAG_COMPLEMENT, FLAG_GATE_GIVEN, FLAG_INTERLEAVED, FLAG_KEEP_RECORDS, FLAG_NO_QK_NORM,
+               FLAG_REUSE_RECORDS, FLAG_RMS_NORM, FLAG_SILU, FLAG_ZERO_REST, kda_bwd_ex, kda_bwd_workspace_size, kda_conv_bwd,
+               kda_conv_bwd_workspace_size, kda_conv_fwd, kda_fwd_ex, kda_glr_bwd, kda_glr_bwd_workspace_size,
+               kda_glr_fwd, kda_glr_states_size, kda_glr_workspace_size, kda_qk_rope_bwd,
+               kda_qk_rope_bwd_workspace_size, kda_qk_rope_fwd, kda_workspace_size)
 
-__all__ = ["kda_chunk"]
+__all__ = ["kda_chunk", "kda_glr", "kda_short_conv", "kda_qk_norm_rope"]
 
 
 def _sizes(q, v, cu_seqlens):
@@ -83,3 +92,154 @@ def kda_chunk(q, k, v, raw_gate, raw_beta, A_log, dt_bias, *, scale=None, lower_
         scale = q.shape[-1] ** -0.5
     return _KdaChunk.apply(q, k, v, raw_gate, raw_beta, A_log, dt_bias, initial_state, float(scale),
                            float(lower_bound), cu_seqlens, bool(reuse_records))
+
+
+def _scratch(size, like):
+    return torch.empty(max(size, 1), dtype=torch.uint8, device=like.device)
+
+
+def _grad(g, like):
+    """A gradient as the library takes it: the output's type, contiguous, zeros where there is none."""
+    return torch.zeros_like(like, memory_format=torch.contiguous_format) if g is None else g.to(like.dtype).contiguous()
+
+
+def _count(x, cu_seqlens):
+    return x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+
+
+class _Glr(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens, flags, train):
+        B, T, H, K = x.shape
+        out = torch.empty_like(x)
+        final = torch.empty(_count(x, cu_seqlens), H, K, dtype=torch.float32, device=x.device)
+        states = _scratch(kda_glr_states_size(B * T, H, K), x) if train else None
+        kda_glr_fwd(x, raw_gate, out, _scratch(kda_glr_workspace_size(B * T, H, K), x), A_log, dt_bias, lower_bound,
+                    initial_state, final, states, cu_seqlens, flags)
+        if train:
+            ctx.save_for_backward(x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens)
+            ctx.states, ctx.lower_bound, ctx.flags = states, lower_bound, flags
+            ctx.set_materialize_grads(False)
+        return out, final
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_final):
+        x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
+        B, T, H, K = x.shape
+        d_out = _grad(d_out, x)
+        d_final = None if d_final is None else d_final.to(torch.float32).contiguous()
+        dx, dg = torch.empty_like(x), torch.empty_like(raw_gate)
+        dA, dd = (None if t is None else torch.empty_like(t) for t in (A_log, dt_bias))
+        di = None if initial_state is None else torch.empty_like(initial_state)
+        kda_glr_bwd(x, raw_gate, ctx.states, d_out, dx, dg, dA, dd,
+                    _scratch(kda_glr_bwd_workspace_size(B * T, H, K), x), A_log, dt_bias, ctx.lower_bound,
+                    initial_state, d_final, di, cu_seqlens, ctx.flags)
+        return dx, dg, dA, dd, di, None, None, None, None
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def kda_glr(x, raw_gate, A_log=None, dt_bias=None, *, lower_bound=-5.0, initial_state=None, cu_seqlens=None,
+            gate_given=False, complement=False):
+    """Differentiable gated linear recurrence h_t = a_t h_{t-1} + b_t x_t; returns (h of x's type
+    [B,T,H,K], final_state fp32 [N,H,K]).
+
+    a_t = exp(g_t) with g_t = lower_bound sigmoid(exp(A_log) (raw_gate_t + dt_bias)), or raw_gate_t
+    itself with ``gate_given`` (A_log and dt_bias must then be None); b_t = 1, or 1 - a_t with ``complement``.  x and
+    raw_gate bf16 or fp32 [B,T,H,K]; A_log fp32 [H]; dt_bias fp32 [H,K]; initial_state fp32
+    [N,H,K] or None; cu_seqlens int32 [N+1] (with B = 1) or None; rows behind the last sequence
+    come back as zeros.  All tensors contiguous, on one GPU, and unchanged until the backward.
+    """
+    if gate_given and (A_log is not None or dt_bias is not None):
+        raise ValueError("with gate_given there is no A_log and no dt_bias")
+    flags = (FLAG_GATE_GIVEN if gate_given else 0) | (FLAG_COMPLEMENT if complement else 0) | FLAG_ZERO_REST
+    return _Glr.apply(x, raw_gate, A_log, dt_bias, initial_state, float(lower_bound), cu_seqlens, flags,
+                      _wants_grad(x, raw_gate, A_log, dt_bias, initial_state))
+
+
+class _Conv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state, cu_seqlens, flags):
+        N, W = _count(x, cu_seqlens), weight.shape[1]
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        final = torch.empty(N, W - 1, x.shape[2], dtype=x.dtype, device=x.device)
+        kda_conv_fwd(x, weight, out, bias, initial_state, final, cu_seqlens, flags)
+        ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
+        ctx.flags = flags
+        ctx.set_materialize_grads(False)
+        return out, final
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_final):
+        x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
+        d_out = _grad(d_out, x)
+        d_final = None if d_final is None else d_final.to(x.dtype).contiguous()
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty_like(weight)
+        db, di = (None if t is None else torch.empty_like(t) for t in (bias, initial_state))
+        ws = _scratch(kda_conv_bwd_workspace_size(x.shape[0] * x.shape[1], x.shape[2], weight.shape[1]), x)
+        kda_conv_bwd(x, weight, d_out, dx, dw, ws, bias, db, initial_state, d_final, di, cu_seqlens, ctx.flags)
+        return dx, dw, db, di, None, None
+
+
+def kda_short_conv(x, weight, bias=None, *, silu=True, initial_state=None, cu_seqlens=None):
+    """Differentiable short causal depthwise convolution, with SiLU unless ``silu`` is False; returns
+    (out [B,T,C], final_state [N,W-1,C]), both of x's type.
+
+    x bf16 or fp32 [B,T,C], its tokens evenly apart (a slice of a wider projection's output will
+    do); weight fp32 [C,W], W 2 to 4; bias fp32 [C] or None; initial_state [N,W-1,C] of x's type
+    (the inputs before the first token, in order) or None for zeros; cu_seqlens int32 [N+1] (with
+    B = 1) or None; rows behind the last sequence come back as zeros.  The final state is the next
+    call's initial state.
+    """
+    return _Conv.apply(x, weight, bias, initial_state, cu_seqlens, (FLAG_SILU if silu else 0) | FLAG_ZERO_REST)
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, flags):
+        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        kda_qk_rope_fwd(q, k, q_out, k_out, positions, inv_freq, eps, q_weight, k_weight, flags)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.eps, ctx.flags = eps, flags
+        ctx.set_materialize_grads(False)
+        return q_out, k_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_q_out, d_k_out):
+        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        dqw, dkw = (None if t is None else torch.empty_like(t) for t in (q_weight, k_weight))
+        ws = None
+        if dqw is not None or dkw is not None:
+            B, T, Hq, D = q.shape
+            ws = _scratch(kda_qk_rope_bwd_workspace_size(B * T, Hq, k.shape[2], D), q)
+        kda_qk_rope_bwd(q, k, _grad(d_q_out, q), _grad(d_k_out, k), dq, dk, positions, inv_freq, ctx.eps, q_weight,
+                        k_weight, dqw, dkw, ws, ctx.flags)
+        return dq, dk, dqw, dkw, None, None, None, None
+
+
+_NORM = {"l2": 0, "rms": FLAG_RMS_NORM, "none": FLAG_NO_QK_NORM}
+
+
+def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_weight=None, norm="l2", eps=1e-6,
+                     interleaved=False):
+    """Differentiable norm of queries and keys per head with the position rotation in the same pass;
+    returns (q_out, k_out), contiguous, of the inputs' type.
+
+    q [B,T,Hq,D], k [B,T,Hk,D] bf16 or fp32, tokens and heads evenly apart (slices of one
+    projection's output will do); ``norm`` "l2" (x / sqrt(sum x^2 + eps), the core's), "rms"
+    (x / sqrt(mean x^2 + eps)) or "none"; q_weight, k_weight fp32 [D] or None; positions int32
+    [B,T] and inv_freq fp64 [R/2] (radians per position) turn the pairs (i, i + R/2) of the first
+    R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them.  With "l2" and no weights
+    the results are unit rows, as ``kda_fwd_ex`` takes them with FLAG_NO_QK_NORM.
+    """
+    if norm not in _NORM:
+        raise ValueError(f"norm must be one of {sorted(_NORM)}")
+    return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, float(eps),
+                             _NORM[norm] | (FLAG_INTERLEAVED if interleaved else 0))

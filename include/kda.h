@@ -402,6 +402,196 @@ kda_status_t kda_fwd_noalloc(const void* q, const void* k, const void* v, const 
                              float* final_state, const int32_t* cu_seqlens, int64_t B, int64_t T, int64_t H,
                              int64_t K, int64_t V, int64_t N, void* stream);
 
+/*
+ * Operators around the KDA core.  A layer that uses kda_fwd runs a short causal
+ * convolution in front of q, k and v, may rotate q and k by position, and often
+ * stands beside layers whose state is one value per channel.  These entry
+ * points take what kda_fwd takes: device pointers owned by the caller, fp32
+ * parameters, a stream, packed batches as cu_seqlens.  They allocate nothing,
+ * do not synchronise and record no memset, so they can be captured into a HIP
+ * graph; every result is the same bits from run to run.
+ *
+ *   dtype        type of the token arrays (KDA_DTYPE_*; other values give
+ *                KDA_ERR_UNSUPPORTED).  Arithmetic is fp32 in both; a bf16
+ *                output is rounded once.
+ *   cu_seqlens   as for kda_fwd (int32 [N + 1], B == 1, cu_seqlens[0] == 0,
+ *                non-decreasing), but cu_seqlens[N] may be less than T: rows
+ *                behind the last sequence belong to none, are not used and
+ *                are left as they were in every output (KDA_FLAG_ZERO_REST:
+ *                are written as zeros).
+ *   alignment    token arrays and states: 4 elements; fp32 parameters,
+ *                fp32 states and workspaces: 16 bytes (KDA_ERR_INVALID).
+ * Outputs must not overlap inputs or each other except where stated.
+ */
+typedef enum {
+  KDA_DTYPE_BF16 = 0,
+  KDA_DTYPE_FP32 = 1
+} kda_dtype_t;
+
+/*
+ * KDA_FLAG_COMPLEMENT   (kda_glr_*) the input is scaled by 1 - a.
+ * KDA_FLAG_SILU         (kda_conv_*) the convolution's sum z becomes z sigmoid(z).
+ * KDA_FLAG_RMS_NORM     (kda_qk_rope_*) divide by the root mean square instead
+ *                       of the L2 norm.
+ * KDA_FLAG_INTERLEAVED  (kda_qk_rope_*) rotate the channel pairs (2i, 2i + 1)
+ *                       instead of (i, i + R/2).
+ * KDA_FLAG_ZERO_REST    (kda_glr_fwd, kda_glr_bwd, kda_conv_fwd, kda_conv_bwd)
+ *                       rows behind the last sequence become zeros in out, dx
+ *                       and d_raw_gate, for callers whose outputs are fresh memory.
+ */
+#define KDA_FLAG_COMPLEMENT 128u
+#define KDA_FLAG_SILU 256u
+#define KDA_FLAG_RMS_NORM 512u
+#define KDA_FLAG_INTERLEAVED 1024u
+#define KDA_FLAG_ZERO_REST 2048u
+
+/*
+ * Gated linear recurrence: one state value per channel under KDA's gate,
+ *     g_t = lower_bound * sigmoid(exp(A_log[h]) * (raw_gate_t + dt_bias[h]))
+ *     a_t = exp(g_t),  h_t = a_t h_{t-1} + b_t x_t,  out_t = h_t,
+ * with b_t = 1, or 1 - a_t with KDA_FLAG_COMPLEMENT.
+ *
+ *   x, raw_gate   [B, T, H, K]
+ *   out           [B, T, H, K] written
+ *   workspace     scratch of >= kda_glr_workspace_size(B * T, H, K) bytes
+ *   A_log, dt_bias, lower_bound   as for kda_fwd.  With KDA_FLAG_GATE_GIVEN
+ *                 raw_gate holds g itself, any value (minus infinity: the
+ *                 state is dropped), these three are unused, and A_log and
+ *                 dt_bias may be NULL.
+ *   initial_state fp32 [N, H, K] or NULL for zeros
+ *   final_state   fp32 [N, H, K] written, or NULL
+ *   states        >= kda_glr_states_size(B * T, H, K) bytes, written for a
+ *                 following kda_glr_bwd with the same inputs; NULL where none
+ *                 follows.  (The states entering every tile of rows; the
+ *                 layout is the library's own.)
+ *   K             a multiple of 4; H, N, B >= 1, T >= 0
+ *   flags         KDA_FLAG_GATE_GIVEN, KDA_FLAG_COMPLEMENT, KDA_FLAG_ZERO_REST
+ * A NaN or infinity stays within its own sequence and channel.
+ */
+size_t kda_glr_workspace_size(int64_t T_total, int64_t H, int64_t K);
+size_t kda_glr_states_size(int64_t T_total, int64_t H, int64_t K);
+kda_status_t kda_glr_fwd(const void* x, const void* raw_gate, void* out, void* workspace, size_t workspace_bytes,
+                         const float* A_log, const float* dt_bias, float lower_bound, const float* initial_state,
+                         float* final_state, float* states, const int32_t* cu_seqlens, int64_t B, int64_t T,
+                         int64_t H, int64_t K, int64_t N, int dtype, unsigned flags, void* stream);
+
+/*
+ * Gradients of kda_glr_fwd for loss = <d_out, out> + <d_final, final_state>.
+ *   states        what the forward with the same inputs and flags left
+ *   d_out         [B, T, H, K];  d_final fp32 [N, H, K] or NULL for zero
+ *   dx, d_raw_gate  [B, T, H, K] written (with KDA_FLAG_GATE_GIVEN the latter
+ *                 is the gradient of g)
+ *   dA_log, d_dt_bias  fp32 [H], [H, K] written; unused with
+ *                 KDA_FLAG_GATE_GIVEN, where they may be NULL
+ *   d_initial_state fp32 [N, H, K] written, or NULL
+ *   workspace     >= kda_glr_bwd_workspace_size(B * T, H, K) bytes
+ */
+size_t kda_glr_bwd_workspace_size(int64_t T_total, int64_t H, int64_t K);
+kda_status_t kda_glr_bwd(const void* x, const void* raw_gate, const float* states, const void* d_out,
+                         const float* d_final, void* dx, void* d_raw_gate, float* dA_log, float* d_dt_bias,
+                         float* d_initial_state, void* workspace, size_t workspace_bytes, const float* A_log,
+                         const float* dt_bias, float lower_bound, const float* initial_state,
+                         const int32_t* cu_seqlens, int64_t B, int64_t T, int64_t H, int64_t K, int64_t N,
+                         int dtype, unsigned flags, void* stream);
+
+/*
+ * The recurrence for decoding: B sequences of T tokens each (T small), in one
+ * launch without a workspace.  States fp32 [B, H, K]; final_state may equal
+ * initial_state (the in-place update) or be NULL.
+ */
+kda_status_t kda_glr_step(const void* x, const void* raw_gate, void* out, const float* A_log, const float* dt_bias,
+                          float lower_bound, const float* initial_state, float* final_state, int64_t B, int64_t T,
+                          int64_t H, int64_t K, int dtype, unsigned flags, void* stream);
+
+/*
+ * Short causal depthwise convolution over tokens,
+ *     z_t[c] = bias[c] + sum_j weight[c][j] x_{t - (W - 1) + j}[c],
+ * out_t = z_t, or z_t sigmoid(z_t) with KDA_FLAG_SILU.
+ *
+ *   x             [B, T, C], rows x_stride elements apart (a multiple of 4,
+ *                 >= C; the rows of one sequence after those of the one
+ *                 before): a slice of a wider projection's output will do
+ *   weight        fp32 [C, W], W = 2, 3 or 4;  bias fp32 [C] or NULL
+ *   out           [B, T, C] written, contiguous
+ *   initial_state [N, W - 1, C] of x's type, the inputs before each sequence's
+ *                 first token in order, or NULL for zeros
+ *   final_state   [N, W - 1, C] of x's type written, or NULL: the last W - 1
+ *                 inputs (of a shorter sequence, the newest rows of its
+ *                 initial state before them)
+ *   C             a multiple of 8
+ */
+kda_status_t kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias, void* out,
+                          const void* initial_state, void* final_state, const int32_t* cu_seqlens, int64_t B,
+                          int64_t T, int64_t C, int64_t W, int64_t N, int dtype, unsigned flags, void* stream);
+
+/*
+ * Gradients of kda_conv_fwd for loss = <d_out, out> + <d_final, final_state>.
+ *   d_out         [B, T, C], contiguous;  d_final [N, W - 1, C] of x's type, or NULL
+ *   dx            [B, T, C] written, contiguous
+ *   d_weight      fp32 [C, W] written;  d_bias fp32 [C] written, or NULL
+ *   d_initial_state [N, W - 1, C] of x's type written, or NULL
+ *   workspace     >= kda_conv_bwd_workspace_size(B * T, C, W) bytes
+ */
+size_t kda_conv_bwd_workspace_size(int64_t T_total, int64_t C, int64_t W);
+kda_status_t kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias, const void* d_out,
+                          const void* d_final, void* dx, float* d_weight, float* d_bias, void* d_initial_state,
+                          void* workspace, size_t workspace_bytes, const void* initial_state,
+                          const int32_t* cu_seqlens, int64_t B, int64_t T, int64_t C, int64_t W, int64_t N, int dtype,
+                          unsigned flags, void* stream);
+
+/*
+ * The convolution for decoding: B sequences of T tokens each (T small).
+ * States [B, W - 1, C] of x's type; final_state may equal initial_state (the
+ * in-place update) or be NULL.
+ */
+kda_status_t kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias, void* out,
+                           const void* initial_state, void* final_state, int64_t B, int64_t T, int64_t C, int64_t W,
+                           int dtype, unsigned flags, void* stream);
+
+/*
+ * Norm of queries and keys per head, with the position rotation in the same
+ * pass.  Per token and head, for the D channels x at position p,
+ *     n = x / sqrt(sum x^2 + eps)    (the core's norm; its results are what
+ *                                     kda_fwd_ex takes with KDA_FLAG_NO_QK_NORM)
+ *         x / sqrt(mean x^2 + eps)   with KDA_FLAG_RMS_NORM
+ *         x                          with KDA_FLAG_NO_QK_NORM
+ *     m = n * weight                 (per channel, where a weight is given)
+ *     out = m, the R / 2 channel pairs (i, i + R/2) turned by p * inv_freq[i]
+ *           (KDA_FLAG_INTERLEAVED: the pairs (2i, 2i + 1)); channels from R on
+ *           stay.
+ *
+ *   q, k          [tokens, Hq, D], [tokens, Hk, D]; token and head strides in
+ *                 elements (multiples of 4): slices of one projection's output
+ *                 will do.  Hq or Hk may be 0.
+ *   q_out, k_out  contiguous, or equal to q and k: then in place, with their
+ *                 strides
+ *   q_weight, k_weight  fp32 [D] or NULL
+ *   positions     int32 [tokens], any value; inv_freq fp64 [R / 2], radians per
+ *                 position (angles are formed and reduced in fp64).  Both may
+ *                 be NULL with R == 0.
+ *   D, R          multiples of 8, 0 <= R <= D <= 512
+ */
+kda_status_t kda_qk_rope_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                             int64_t k_head_stride, void* q_out, void* k_out, const float* q_weight,
+                             const float* k_weight, const int32_t* positions, const double* inv_freq, float eps,
+                             int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int dtype, unsigned flags,
+                             void* stream);
+
+/*
+ * Gradients of kda_qk_rope_fwd (of its inputs, not of an in-place result).
+ *   d_q_out, d_k_out, dq, dk   contiguous; dq may equal d_q_out, dk d_k_out
+ *   d_q_weight, d_k_weight     fp32 [D] written, or NULL
+ *   workspace     >= kda_qk_rope_bwd_workspace_size(tokens, Hq, Hk, D) bytes;
+ *                 may be NULL where neither weight gradient is asked for
+ */
+size_t kda_qk_rope_bwd_workspace_size(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D);
+kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                             int64_t k_head_stride, const void* d_q_out, const void* d_k_out, void* dq, void* dk,
+                             float* d_q_weight, float* d_k_weight, void* workspace, size_t workspace_bytes,
+                             const float* q_weight, const float* k_weight, const int32_t* positions,
+                             const double* inv_freq, float eps, int64_t tokens, int64_t Hq, int64_t Hk, int64_t D,
+                             int64_t R, int dtype, unsigned flags, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* kda_status_string(kda_status_t status);
 
