@@ -5,21 +5,28 @@
 //
 // A run of tokens maps the state that enters it to h -> A h + B (A the product
 // of its decays, B its result from zero), and such maps compose.  The packed
-// token axis is cut into tiles of 128 rows, whatever the sequences: a tile
-// that holds the first row of a sequence has a map that does not depend on the
-// entering state (it is reset: the composition selects, it does not multiply
-// by zero, so that a sequence's NaN or infinity stays in it).  Three launches:
-//   1. the map of every tile (reads x and raw_gate);
-//   2. per channel, the state entering every tile, in order;
-//   3. every tile again from its entering state, writing the outputs.
-// A tile is 512 threads: 32 lanes of 4 channels by 16 runs of 8 rows, each run
+// token axis is cut into tiles of 64 rows by 128 channels, whatever the
+// sequences: a tile that holds the first row of a sequence has a map that does
+// not depend on the entering state (it is reset: the composition selects, it
+// does not multiply by zero, so that a sequence's NaN or infinity stays in it).
+// A tile is 512 threads: 32 lanes of 4 channels by 16 runs of 4 rows, each run
 // in one thread's registers, the runs joined through LDS in order.
+//
+// One pass over the data: a workgroup takes the tiles in order from a counter,
+// loads its tile once, publishes the tile's map, finds the state that enters
+// it and writes the outputs from registers.  To find that state, it looks back
+// over the flags of up to 64 tiles before it for the nearest one whose leaving
+// state is known, and applies the maps of the tiles in between, in order.  The
+// leaving state of a tile is always its map applied to its entering state, so
+// the result has the same bits however far back the search ends.  A tile waits
+// only for tiles that running workgroups took before it; the wait is bounded
+// all the same, and one that gives up sets the workspace's fault word.
 //
 // Backward, with dh_t = d_out_t + a_{t+1} dh_{t+1} (d_final joins at the last
 // row) and e_t = a_t dh_t, the gradient that row t hands to the row before:
 //     dx_t = b_t dh_t,   dg_t = a_t dh_t (h_{t-1} [- x_t if b = 1 - a])
-// the same three launches run from the right over e; h_{t-1} is recomputed
-// from the states that the forward left, one per tile.
+// the same pass runs over e from the right; h_{t-1} is recomputed from the
+// states entering every tile, which the forward leaves.
 //
 // All arithmetic is fp32.
 
@@ -30,11 +37,12 @@
 namespace kda {
 namespace {
 
-constexpr int GR = 8;           // rows of a run
+constexpr int GR = 4;           // rows of a run
 constexpr int GS = 16;          // runs of a tile
 constexpr int GL = GR * GS;     // rows of a tile
 constexpr int GC = 128;         // channels of a tile
 constexpr int GT = GS * GC / 4; // threads
+constexpr int64_t kMaxChannels = (int64_t)1 << 21;  // a tile's rows span less than 2^30 bytes
 
 struct GlrArgs {
   const void* x;
@@ -48,10 +56,13 @@ struct GlrArgs {
   const float* d_final;
   float* fin;
   float* d_init;
-  float* states;  // [tiles][C] state entering every tile
-  float2* maps;   // [tiles][C] A, B of every tile (backward: of its e map)
-  int* reset;     // [tiles] whether the tile's map ignores what enters
-  float* ends;    // [tiles][C] e entering every tile from the right
+  const float* states;  // [tiles][C] state entering every tile (backward)
+  // the pass's own, tiles counted in its order (the backward from the right):
+  float* enter;   // [tiles][C] what enters every tile (forward: states)
+  uint64_t* maps; // [tiles][C] A and B of every tile's map
+  int* flags;     // [2 nblk][tiles], one for 64 channels: 1 the map, 2 also what leaves is known
+  int* ticket;    // the next tile
+  unsigned* faults;
   float2* part;   // [tiles][C] sums over the tile of d_raw and of dz z
   float* dA_log;
   float* d_dt_bias;
@@ -123,30 +134,204 @@ __device__ __forceinline__ bool mark_tile(const Axis& ax, int64_t t0, int* S, in
   return __syncthreads_or(any);
 }
 
-// MAPS: write the tile's map.  Otherwise the outputs, from the entering state.
-template <typename T, bool GIVEN, bool COMPL, bool MAPS>
-__global__ void __launch_bounds__(GT) kda_glr_fwd_kernel(GlrArgs a) {
-  __shared__ float sA[GS][GC], sB[GS][GC];
-  __shared__ int sS[GL], sE[GL], sReset[GS];
+// Loads and stores of a tile by 32-bit offsets from its first row.  The
+// descriptor ends behind the last row that belongs to a sequence: rows behind
+// it load as zeros and are not stored, and so does an offset of OUTSIDE.
+constexpr int OUTSIDE = 0x7ffffff0;
+template <typename T>
+struct Rows {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Rows(const void* base, int64_t t0, int64_t rows, int64_t C) {
+    const int64_t left = rows - t0 < GL ? rows - t0 : GL;
+    r = buf(static_cast<const T*>(base) + t0 * C, (uint32_t)((left > 0 ? left : 0) * C * sizeof(T)));
+  }
+  __device__ __forceinline__ raw4<T> load(int voff, int soff) const {
+    if constexpr (sizeof(T) == 2) {
+      return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0));
+    } else {
+      return __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+    }
+  }
+  __device__ __forceinline__ void store(int voff, int soff, const float (&d)[4]) const {
+    if constexpr (sizeof(T) == 2) {
+      bf16x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (__bf16)d[i];
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), r, voff, soff, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, make_float4(d[0], d[1], d[2], d[3])), r, voff,
+                                             soff, 0);
+    }
+  }
+};
+
+// Device-scope words that other workgroups write while this kernel runs.  The
+// data of a tile is stored, then waited for, then flagged: each access goes to
+// where all XCDs agree (a relaxed atomic of device scope), and the wait orders
+// them without writing back or dropping whole caches.
+template <typename W>
+__device__ __forceinline__ W peek(const W* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W>
+__device__ __forceinline__ void post(W* p, W v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void flag_after(int* flag, int value) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if ((threadIdx.x & 63) == 0) post(flag, value);
+}
+
+// Polls before a wait gives up (about a second: each is a round trip to memory
+// and a 128-cycle sleep).
+constexpr int kPolls = 1 << 20;
+
+// What enters tile k (counted in the pass's order), for channel c, found by
+// the wave that has this 64-channel column `flags` of the tiles' flags.
+__device__ __forceinline__ float look_back(const GlrArgs& a, const int* flags, int k, int64_t c, bool in) {
+  const int lane = threadIdx.x & 63;
+  int p = 0;
+  bool found = false;
+  for (int poll = 0; poll < kPolls; ++poll) {
+    const int q = k - 1 - lane;
+    const int f = q >= 0 ? peek(flags + q) : 0;
+    const uint64_t known = __ballot(f == 2), mapped = __ballot(f >= 1);
+    if (known) {
+      p = __builtin_ctzll(known);
+      const uint64_t between = ((uint64_t)1 << p) - 1;
+      if ((mapped & between) == between) {
+        found = true;
+        break;
+      }
+    }
+    __builtin_amdgcn_s_sleep(2);
+  }
+  if (!found) {
+    if (lane == 0) atomicOr(a.faults, FAULT_WAIT_TIMEOUT);
+    return 0.f;
+  }
+  if (!in) return 0.f;
+  // tiles k - p .. k - 1 lie between; their maps are loaded 8 at a time
+  float s = peek(a.enter + (int64_t)(k - p) * a.C + c);
+  for (int q = k - p; q < k; q += 8) {
+    uint64_t m[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m[u] = q + u < k ? peek(a.maps + (int64_t)(q + u) * a.C + c) : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (q + u < k) s = __uint_as_float((uint32_t)m[u]) * s + __uint_as_float((uint32_t)(m[u] >> 32));
+  }
+  return s;
+}
+
+struct Tile {
+  float A[GS][GC], B[GS][GC];  // the runs' maps; then, in A, what enters every run
+  int reset[GS];
+};
+
+// Joins the runs of a tile, in the pass's order (REV: from the last run), by
+// the waves of its two 64-channel columns: the tile's map to the others, what
+// enters the tile from them (not where the tile begins `fresh`, with a
+// sequence's first row), and what enters every run into t.A.
+template <bool REV>
+__device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, int k, int blk, bool fresh) {
+  const int w = threadIdx.x >> 6;
+  const int ch = threadIdx.x;  // of the tile; w < 2
+  const int64_t c = (int64_t)blk * GC + ch;
+  const bool in = c < a.C;
+  float At = 1.f, Bt = 0.f;
+  bool resets = false;
+#pragma unroll
+  for (int i = 0; i < GS; ++i) {
+    const int run = REV ? GS - 1 - i : i;
+    const float Ai = t.A[run][ch], Bi = t.B[run][ch];
+    const bool ri = t.reset[run];
+    resets |= ri;
+    Bt = ri ? Bi : Ai * Bt + Bi;
+    At *= Ai;
+  }
+  int* flags = a.flags + (int64_t)(blk * 2 + w) * a.ntiles;
+  const bool last = k + 1 == a.ntiles;
+  float s = 0.f;
+  if (resets) {
+    // what leaves is known, whatever enters; that is only needed by rows before the reset
+    if (!last) {
+      if (in) post(a.enter + (int64_t)(k + 1) * a.C + c, Bt);
+      flag_after(flags + k, 2);
+    }
+    if (k > 0 && !fresh) s = look_back(a, flags, k, c, in);
+  } else {
+    if (!last) {
+      if (in) post(a.maps + (int64_t)k * a.C + c, (uint64_t)__float_as_uint(Bt) << 32 | __float_as_uint(At));
+      flag_after(flags + k, 1);
+    }
+    if (k > 0) s = look_back(a, flags, k, c, in);
+    if (!last) {
+      if (in) post(a.enter + (int64_t)(k + 1) * a.C + c, At * s + Bt);
+      flag_after(flags + k, 2);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < GS; ++i) {
+    const int run = REV ? GS - 1 - i : i;
+    const float Ai = t.A[run][ch], Bi = t.B[run][ch];
+    t.A[run][ch] = s;
+    s = t.reset[run] ? Bi : Ai * s + Bi;
+  }
+}
+
+// The next tile of the pass, for all threads; `next` is thread 0's ticket.
+__device__ __forceinline__ int64_t take(const GlrArgs& a, int* slot, int next) {
+  __syncthreads();
+  if (threadIdx.x == 0) *slot = next;
+  __syncthreads();
+  return *slot;
+}
+__device__ __forceinline__ int draw_ticket(const GlrArgs& a) {
+  return threadIdx.x == 0 ? (int)__hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+}
+
+__global__ void __launch_bounds__(256) kda_glr_clear_kernel(int* ticket, unsigned* faults, int* flags, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i == 0) {
+    *ticket = 0;
+    *faults = 0;
+  }
+  if (i < n) flags[i] = 0;
+}
+
+// State (or gradient) of sequence n at 4 channels, zeros where there is none.
+__device__ __forceinline__ void state4(const float* p, int n, int64_t C, int64_t c, bool in, float (&s)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[j] = 0.f;
+  if (p && in) load_f4(p + (int64_t)n * C + c, s);
+}
+
+template <typename T, bool GIVEN, bool COMPL>
+__global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
+  __shared__ Tile t;
+  __shared__ int sS[GL], sE[GL], slot;
   const int tid = threadIdx.x, lane = tid & 31, run = tid >> 5;
   const int64_t rows = axis_rows(a.ax);
-  for (int64_t item = blockIdx.x; item < (int64_t)a.ntiles * a.nblk; item += gridDim.x) {
-    const int tile = (int)(item / a.nblk), blk = (int)(item % a.nblk);
+  const int64_t items = (int64_t)a.ntiles * a.nblk;
+  const int row_bytes = (int)(a.C * sizeof(T));
+  int64_t item = take(a, &slot, draw_ticket(a));
+  while (item < items) {
+    const int next = draw_ticket(a);
+    const int k = (int)(item / a.nblk), blk = (int)(item % a.nblk);
     const int64_t c = (int64_t)blk * GC + lane * 4;
     const bool in = c < a.C;
-    const int64_t t0 = (int64_t)tile * GL, tr = t0 + run * GR;
+    const int64_t t0 = (int64_t)k * GL;
+    const int voff = in ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+    const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), os(a.out, t0, rows, a.C);
     raw4<T> xr[GR], gr[GR];
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
-      zero4(xr[i]);
-      zero4(gr[i]);
-      if (in && tr + i < rows) {
-        xr[i] = *reinterpret_cast<const raw4<T>*>(static_cast<const T*>(a.x) + (tr + i) * a.C + c);
-        gr[i] = *reinterpret_cast<const raw4<T>*>(static_cast<const T*>(a.g) + (tr + i) * a.C + c);
-      }
+      gr[i] = gs.load(voff, i * row_bytes);
+      xr[i] = xs.load(voff, i * row_bytes);
     }
     Gate<GIVEN> gate;
-    if (in) gate.init(a, c);
+    gate.init(a, in ? c : 0);
     const bool marked = mark_tile(a.ax, t0, sS, sE);
     float av[GR][4], u[GR][4];
 #pragma unroll
@@ -161,7 +346,6 @@ __global__ void __launch_bounds__(GT) kda_glr_fwd_kernel(GlrArgs a) {
         u[i][j] = COMPL ? one_minus(g2, av[i][j]) * xv[j] : xv[j];
       }
     }
-    // the run's map
     float A[4], B[4];
     bool reset = false;
 #pragma unroll
@@ -173,10 +357,7 @@ __global__ void __launch_bounds__(GT) kda_glr_fwd_kernel(GlrArgs a) {
     for (int i = 0; i < GR; ++i) {
       if (marked && sS[run * GR + i] >= 0) {
         reset = true;
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) B[j] = zero[j];
-        if (a.init && in) load_f4(a.init + (int64_t)sS[run * GR + i] * a.C + c, B);
+        state4(a.init, sS[run * GR + i], a.C, c, in, B);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -184,52 +365,31 @@ __global__ void __launch_bounds__(GT) kda_glr_fwd_kernel(GlrArgs a) {
         B[j] = av[i][j] * B[j] + u[i][j];
       }
     }
-    store4(&sA[run][lane * 4], A);
-    store4(&sB[run][lane * 4], B);
-    if (lane == 0) sReset[run] = reset;
+    store4(&t.A[run][lane * 4], A);
+    store4(&t.B[run][lane * 4], B);
+    if (lane == 0) t.reset[run] = reset;
     __syncthreads();
-    if constexpr (MAPS) {
-      if (tid < GC && (int64_t)blk * GC + tid < a.C) {
-        float At = 1.f, Bt = 0.f;
-        bool r = false;
-        for (int k = 0; k < GS; ++k) {
-          const bool rk = sReset[k];
-          Bt = rk ? sB[k][tid] : sA[k][tid] * Bt + sB[k][tid];
-          At *= sA[k][tid];
-          r |= rk;
-        }
-        a.maps[(int64_t)tile * a.C + (int64_t)blk * GC + tid] = make_float2(At, Bt);
-        if (tid == 0 && blk == 0) a.reset[tile] = r;
-      }
-    } else {
-      float h[4] = {0.f, 0.f, 0.f, 0.f};
-      if (in) load_f4(a.states + (int64_t)tile * a.C + c, h);
-      for (int k = 0; k < run; ++k) {
-        float Ak[4], Bk[4];
-        load_f4(&sA[k][lane * 4], Ak);
-        load_f4(&sB[k][lane * 4], Bk);
-        const bool rk = sReset[k];
+    if (tid < GC) join_runs<false>(a, t, k, blk, marked && sS[0] >= 0);
+    __syncthreads();
+    float h[4];
+    load_f4(&t.A[run][lane * 4], h);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = rk ? Bk[j] : Ak[j] * h[j] + Bk[j];
-      }
+    for (int i = 0; i < GR; ++i) {
+      if (marked && sS[run * GR + i] >= 0) state4(a.init, sS[run * GR + i], a.C, c, in, h);
 #pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = av[i][j] * h[j] + u[i][j];
+      os.store(voff, i * row_bytes, h);
+      if (marked && a.fin && in && sE[run * GR + i] >= 0) store4(a.fin + (int64_t)sE[run * GR + i] * a.C + c, h);
+    }
+    if (a.zero_rest && t0 + GL > rows && in) {
       for (int i = 0; i < GR; ++i) {
-        if (marked && sS[run * GR + i] >= 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = 0.f;
-          if (a.init && in) load_f4(a.init + (int64_t)sS[run * GR + i] * a.C + c, h);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = av[i][j] * h[j] + u[i][j];
-        if (in && tr + i < rows) store4(static_cast<T*>(a.out) + (tr + i) * a.C + c, h);
-        else if (in && a.zero_rest && tr + i < a.ax.total) store_zero4(static_cast<T*>(a.out) + (tr + i) * a.C + c);
-        if (marked && a.fin && in && sE[run * GR + i] >= 0)
-          store4(a.fin + (int64_t)sE[run * GR + i] * a.C + c, h);
+        const int64_t r = t0 + run * GR + i;
+        if (r >= rows && r < a.ax.total) store_zero4(static_cast<T*>(a.out) + r * a.C + c);
       }
     }
-    __syncthreads();
+    item = take(a, &slot, next);
   }
-  if (!MAPS && a.fin) {  // empty sequences hand their state on
+  if (a.fin) {  // empty sequences hand their state on
     for (int64_t n = blockIdx.x; n < a.ax.N; n += gridDim.x) {
       if (axis_start(a.ax, n + 1) > axis_start(a.ax, n)) continue;
       for (int64_t c = tid; c < a.C; c += GT) a.fin[n * a.C + c] = a.init ? a.init[n * a.C + c] : 0.f;
@@ -237,128 +397,80 @@ __global__ void __launch_bounds__(GT) kda_glr_fwd_kernel(GlrArgs a) {
   }
 }
 
-// Per channel: what enters every tile, in order.  REV: from the right.
-template <bool REV>
-__global__ void __launch_bounds__(64) kda_glr_fold_kernel(GlrArgs a) {
-  const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (c >= a.C) return;
-  float* to = REV ? a.ends : a.states;
-  float s = 0.f;
-  constexpr int U = 8;
-  for (int k0 = 0; k0 < a.ntiles; k0 += U) {
-    float2 m[U];
-    int r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int k = k0 + u < a.ntiles ? k0 + u : a.ntiles - 1;
-      k = REV ? a.ntiles - 1 - k : k;
-      m[u] = a.maps[(int64_t)k * a.C + c];
-      r[u] = a.reset[k];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k0 + u < a.ntiles) {
-        const int k = REV ? a.ntiles - 1 - k0 - u : k0 + u;
-        to[(int64_t)k * a.C + c] = s;
-        s = r[u] ? m[u].y : m[u].x * s + m[u].y;
-      }
-    }
-  }
-}
-
-template <typename T, bool GIVEN, bool COMPL, bool MAPS>
-__global__ void __launch_bounds__(GT) kda_glr_bwd_kernel(GlrArgs a) {
-  __shared__ float sA[GS][GC], sB[GS][GC];
-  __shared__ int sS[GL], sE[GL], sReset[GS];
+template <typename T, bool GIVEN, bool COMPL>
+__global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
+  __shared__ Tile t;   // of e, from the right
+  __shared__ Tile ft;  // of h
+  __shared__ int sS[GL], sE[GL], slot;
   const int tid = threadIdx.x, lane = tid & 31, run = tid >> 5;
   const int64_t rows = axis_rows(a.ax);
-  for (int64_t item = blockIdx.x; item < (int64_t)a.ntiles * a.nblk; item += gridDim.x) {
-    const int tile = (int)(item / a.nblk), blk = (int)(item % a.nblk);
+  const int64_t items = (int64_t)a.ntiles * a.nblk;
+  const int row_bytes = (int)(a.C * sizeof(T));
+  int64_t item = take(a, &slot, draw_ticket(a));
+  while (item < items) {
+    const int next = draw_ticket(a);
+    const int k = (int)(item / a.nblk), blk = (int)(item % a.nblk);
+    const int tile = a.ntiles - 1 - k;
     const int64_t c = (int64_t)blk * GC + lane * 4;
     const bool in = c < a.C;
     const int64_t t0 = (int64_t)tile * GL, tr = t0 + run * GR;
+    const int voff = in ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+    const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
     raw4<T> xr[GR], gr[GR], dr[GR];
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
-      zero4(xr[i]);
-      zero4(gr[i]);
-      zero4(dr[i]);
-      if (in && tr + i < rows) {
-        const int64_t o = (tr + i) * a.C + c;
-        if (!MAPS) xr[i] = *reinterpret_cast<const raw4<T>*>(static_cast<const T*>(a.x) + o);
-        gr[i] = *reinterpret_cast<const raw4<T>*>(static_cast<const T*>(a.g) + o);
-        dr[i] = *reinterpret_cast<const raw4<T>*>(static_cast<const T*>(a.d_out) + o);
-      }
+      gr[i] = gs.load(voff, i * row_bytes);
+      dr[i] = ds.load(voff, i * row_bytes);
+      xr[i] = xs.load(voff, i * row_bytes);
     }
     Gate<GIVEN> gate;
-    if (in) gate.init(a, c);
+    gate.init(a, in ? c : 0);
     const bool marked = mark_tile(a.ax, t0, sS, sE);
-    float g2[GR][4];
+    float av[GR][4], b[GR][4];  // decay, input scale
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
       float gv[4];
       widen4(gr[i], gv);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) g2[i][j] = gate.g2(gv[j], j);
-    }
-    // the run's map of e, from the right
-    float P[4], Q[4];
-    bool reset = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      P[j] = 1.f;
-      Q[j] = 0.f;
-    }
-#pragma unroll
-    for (int i = GR - 1; i >= 0; --i) {
-      if (tr + i >= rows) continue;  // rows behind the last sequence hand nothing on
-      if (marked && sE[run * GR + i] >= 0) {
-        reset = true;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) Q[j] = 0.f;
-        if (a.d_final && in) load_f4(a.d_final + (int64_t)sE[run * GR + i] * a.C + c, Q);
+      for (int j = 0; j < 4; ++j) {
+        const float g2 = gate.g2(gv[j], j);
+        av[i][j] = fexp2(g2);
+        b[i][j] = COMPL ? one_minus(g2, av[i][j]) : 1.0f;
       }
-      float dv[4];
-      widen4(dr[i], dv);
+    }
+    // the run's map of e; rows behind the last sequence hand nothing on
+    {
+      float P[4], Q[4];
+      bool reset = false;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float av = fexp2(g2[i][j]);
-        P[j] *= av;
-        Q[j] = av * (dv[j] + Q[j]);
+        P[j] = 1.f;
+        Q[j] = 0.f;
       }
-    }
-    store4(&sA[run][lane * 4], P);
-    store4(&sB[run][lane * 4], Q);
-    if (lane == 0) sReset[run] = reset;
-    __syncthreads();
-    if constexpr (MAPS) {
-      if (tid < GC && (int64_t)blk * GC + tid < a.C) {
-        float Pt = 1.f, Qt = 0.f;
-        bool r = false;
-        for (int k = GS - 1; k >= 0; --k) {
-          const bool rk = sReset[k];
-          Qt = rk ? sB[k][tid] : sA[k][tid] * Qt + sB[k][tid];
-          Pt *= sA[k][tid];
-          r |= rk;
-        }
-        a.maps[(int64_t)tile * a.C + (int64_t)blk * GC + tid] = make_float2(Pt, Qt);
-        if (tid == 0 && blk == 0) a.reset[tile] = r;
-      }
-    } else {
-      float e[4] = {0.f, 0.f, 0.f, 0.f};
-      if (in) load_f4(a.ends + (int64_t)tile * a.C + c, e);
-      for (int k = GS - 1; k > run; --k) {
-        float Pk[4], Qk[4];
-        load_f4(&sA[k][lane * 4], Pk);
-        load_f4(&sB[k][lane * 4], Qk);
-        const bool rk = sReset[k];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = rk ? Qk[j] : Pk[j] * e[j] + Qk[j];
+      for (int i = GR - 1; i >= 0; --i) {
+        if (tr + i < rows) {
+          if (marked && sE[run * GR + i] >= 0) {
+            reset = true;
+            state4(a.d_final, sE[run * GR + i], a.C, c, in, Q);
+          }
+          float dv[4];
+          widen4(dr[i], dv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            P[j] *= av[i][j];
+            Q[j] = av[i][j] * (dv[j] + Q[j]);
+          }
+        }
       }
-      __syncthreads();
-      // the run's forward map, and the state that enters the run
+      store4(&t.A[run][lane * 4], P);
+      store4(&t.B[run][lane * 4], Q);
+      if (lane == 0) t.reset[run] = reset;
+    }
+    // the run's map of h
+    {
       float A[4], B[4];
-      bool fresh = false;
+      bool reset = false;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         A[j] = 1.f;
@@ -367,78 +479,68 @@ __global__ void __launch_bounds__(GT) kda_glr_bwd_kernel(GlrArgs a) {
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         if (marked && sS[run * GR + i] >= 0) {
-          fresh = true;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) B[j] = 0.f;
-          if (a.init && in) load_f4(a.init + (int64_t)sS[run * GR + i] * a.C + c, B);
+          reset = true;
+          state4(a.init, sS[run * GR + i], a.C, c, in, B);
         }
         float xv[4];
         widen4(xr[i], xv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float av = fexp2(g2[i][j]);
-          A[j] *= av;
-          B[j] = av * B[j] + (COMPL ? one_minus(g2[i][j], av) * xv[j] : xv[j]);
+          A[j] *= av[i][j];
+          B[j] = av[i][j] * B[j] + b[i][j] * xv[j];
         }
       }
-      store4(&sA[run][lane * 4], A);
-      store4(&sB[run][lane * 4], B);
-      if (lane == 0) sReset[run] = fresh;
-      __syncthreads();
-      float h[4] = {0.f, 0.f, 0.f, 0.f};
-      if (in) load_f4(a.states + (int64_t)tile * a.C + c, h);
-      for (int k = 0; k < run; ++k) {
-        float Ak[4], Bk[4];
-        load_f4(&sA[k][lane * 4], Ak);
-        load_f4(&sB[k][lane * 4], Bk);
-        const bool rk = sReset[k];
+      store4(&ft.A[run][lane * 4], A);
+      store4(&ft.B[run][lane * 4], B);
+      if (lane == 0) ft.reset[run] = reset;
+    }
+    __syncthreads();
+    if (tid < GC) {
+      join_runs<true>(a, t, k, blk, marked && sE[GL - 1] >= 0);
+    } else if (tid < 2 * GC) {
+      // what enters every run, by the next two waves
+      const int ch = tid - GC;
+      const int64_t cc = (int64_t)blk * GC + ch;
+      float s = cc < a.C ? a.states[(int64_t)tile * a.C + cc] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = rk ? Bk[j] : Ak[j] * h[j] + Bk[j];
+      for (int i = 0; i < GS; ++i) {
+        const float Ai = ft.A[i][ch], Bi = ft.B[i][ch];
+        ft.A[i][ch] = s;
+        s = ft.reset[i] ? Bi : Ai * s + Bi;
       }
-      // h_{t-1} of every row
-      float hp[GR][4];
+    }
+    __syncthreads();
+    float h[4], hp[GR][4];
+    load_f4(&ft.A[run][lane * 4], h);
 #pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        if (marked && sS[run * GR + i] >= 0) {
+    for (int i = 0; i < GR; ++i) {
+      if (marked && sS[run * GR + i] >= 0) state4(a.init, sS[run * GR + i], a.C, c, in, h);
+      float xv[4];
+      widen4(xr[i], xv);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = 0.f;
-          if (a.init && in) load_f4(a.init + (int64_t)sS[run * GR + i] * a.C + c, h);
-        }
-        float xv[4];
-        widen4(xr[i], xv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float av = fexp2(g2[i][j]);
-          hp[i][j] = h[j];
-          h[j] = av * h[j] + (COMPL ? one_minus(g2[i][j], av) * xv[j] : xv[j]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        hp[i][j] = COMPL ? h[j] - xv[j] : h[j];
+        h[j] = av[i][j] * h[j] + b[i][j] * xv[j];
       }
-      float dsum[4] = {0.f, 0.f, 0.f, 0.f}, zsum[4] = {0.f, 0.f, 0.f, 0.f};
+    }
+    float e[4], dsum[4], zsum[4];
+    load_f4(&t.A[run][lane * 4], e);
 #pragma unroll
-      for (int i = GR - 1; i >= 0; --i) {
-        if (tr + i >= rows) {
-          if (in && a.zero_rest && tr + i < a.ax.total) {
-            store_zero4(static_cast<T*>(a.out) + (tr + i) * a.C + c);
-            store_zero4(static_cast<T*>(a.dg) + (tr + i) * a.C + c);
-          }
-          continue;
-        }
-        if (marked && sE[run * GR + i] >= 0) {
+    for (int j = 0; j < 4; ++j) dsum[j] = zsum[j] = 0.f;
+    const Rows<T> dxs(a.out, t0, rows, a.C), dgs(a.dg, t0, rows, a.C);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = 0.f;
-          if (a.d_final && in) load_f4(a.d_final + (int64_t)sE[run * GR + i] * a.C + c, e);
-        }
-        float dv[4], xv[4], gv[4], dx[4], dg[4];
+    for (int i = GR - 1; i >= 0; --i) {
+      if (tr + i < rows) {
+        if (marked && sE[run * GR + i] >= 0) state4(a.d_final, sE[run * GR + i], a.C, c, in, e);
+        float dv[4], gv[4], dx[4], dg[4];
         widen4(dr[i], dv);
-        widen4(xr[i], xv);
         widen4(gr[i], gv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float av = fexp2(g2[i][j]);
           const float dh = dv[j] + e[j];
-          e[j] = av * dh;
-          dx[j] = COMPL ? one_minus(g2[i][j], av) * dh : dh;
-          dg[j] = e[j] * (COMPL ? hp[i][j] - xv[j] : hp[i][j]);
+          e[j] = av[i][j] * dh;
+          dx[j] = b[i][j] * dh;
+          dg[j] = e[j] * hp[i][j];
           if constexpr (!GIVEN) {
             // dg/dz = lb s (1 - s), s = 1 / (1 + w), w = exp(-z).  w is kept
             // finite (a comparison, so that NaN stays) so that w s does not
@@ -452,32 +554,33 @@ __global__ void __launch_bounds__(GT) kda_glr_bwd_kernel(GlrArgs a) {
             dsum[j] += dg[j];
           }
         }
-        if (in) {
-          const int64_t o = (tr + i) * a.C + c;
-          store4(static_cast<T*>(a.out) + o, dx);
-          store4(static_cast<T*>(a.dg) + o, dg);
-          if (marked && a.d_init && sS[run * GR + i] >= 0)
-            store4(a.d_init + (int64_t)sS[run * GR + i] * a.C + c, e);
-        }
-      }
-      if constexpr (!GIVEN) {
-        __syncthreads();
-        store4(&sA[run][lane * 4], dsum);
-        store4(&sB[run][lane * 4], zsum);
-        __syncthreads();
-        if (tid < GC && (int64_t)blk * GC + tid < a.C) {
-          float d = 0.f, z = 0.f;
-          for (int k = 0; k < GS; ++k) {
-            d += sA[k][tid];
-            z += sB[k][tid];
-          }
-          a.part[(int64_t)tile * a.C + (int64_t)blk * GC + tid] = make_float2(d, z);
-        }
+        dxs.store(voff, i * row_bytes, dx);
+        dgs.store(voff, i * row_bytes, dg);
+        if (marked && a.d_init && in && sS[run * GR + i] >= 0)
+          store4(a.d_init + (int64_t)sS[run * GR + i] * a.C + c, e);
+      } else if (in && a.zero_rest && tr + i < a.ax.total) {
+        store_zero4(static_cast<T*>(a.out) + (tr + i) * a.C + c);
+        store_zero4(static_cast<T*>(a.dg) + (tr + i) * a.C + c);
       }
     }
-    __syncthreads();
+    if constexpr (!GIVEN) {
+      // ft is free: a thread's own entry of it is all that was read since the last barrier
+      store4(&ft.B[run][lane * 4], dsum);
+      store4(&ft.A[run][lane * 4], zsum);
+      __syncthreads();
+      if (tid < GC && (int64_t)blk * GC + tid < a.C) {
+        float d = 0.f, z = 0.f;
+#pragma unroll
+        for (int i = 0; i < GS; ++i) {
+          d += ft.B[i][tid];
+          z += ft.A[i][tid];
+        }
+        a.part[(int64_t)tile * a.C + (int64_t)blk * GC + tid] = make_float2(d, z);
+      }
+    }
+    item = take(a, &slot, next);
   }
-  if (!MAPS && a.d_init) {
+  if (a.d_init) {
     for (int64_t n = blockIdx.x; n < a.ax.N; n += gridDim.x) {
       if (axis_start(a.ax, n + 1) > axis_start(a.ax, n)) continue;
       for (int64_t c = tid; c < a.C; c += GT) a.d_init[n * a.C + c] = a.d_final ? a.d_final[n * a.C + c] : 0.f;
@@ -546,25 +649,26 @@ __global__ void __launch_bounds__(GST) kda_glr_step_kernel(GlrArgs a) {
   if (a.fin) store4(a.fin + i, h);
 }
 
+// The counter and the fault word (where kda_workspace_faults looks for it) come
+// first.  The forward keeps the states here where the caller takes none.
 struct GlrLayout {
-  size_t maps, reset, states, ends, part, total;
+  size_t ticket, faults, flags, maps, enter, part, total;
 };
-// Forward: tile maps and reset words, and the states where the caller keeps
-// none.  Backward: tile maps, reset words, entering gradients, partial sums.
 GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
   const size_t tiles = (size_t)((T_total + GL - 1) / GL), w = tiles * (size_t)C;
   GlrLayout l;
-  l.maps = 256;
-  l.reset = l.maps + align256(w * sizeof(float2));
-  l.states = l.reset + align256(tiles * sizeof(int));
-  l.ends = l.states;
-  l.part = l.states + align256(w * sizeof(float));
+  l.ticket = 0;
+  l.faults = 4;
+  l.flags = 256;
+  l.maps = l.flags + align256(tiles * 2 * (size_t)((C + GC - 1) / GC) * sizeof(int));
+  l.enter = l.maps + align256(w * sizeof(uint64_t));
+  l.part = l.enter + align256(w * sizeof(float));
   l.total = l.part + (bwd ? align256(w * sizeof(float2)) : 0);
   return l;
 }
 
 bool glr_sizes_ok(int64_t T_total, int64_t H, int64_t K) {
-  return T_total >= 0 && H >= 1 && K >= 1 && fits(H, K, (int64_t)1 << 30) && fits(T_total, H * K, kMaxElements);
+  return T_total >= 0 && H >= 1 && K >= 1 && fits(H, K, kMaxChannels) && fits(T_total, H * K, kMaxElements);
 }
 
 // Checks shared by the entry points; fills the sizes and the gate.
@@ -582,7 +686,7 @@ kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, f
   if (cu_seqlens && T > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   if (!(flags & FLAG_GATE_GIVEN) && !aligned(dt_bias, 16)) return KDA_ERR_INVALID;
   const int64_t tiles = (B * T + GL - 1) / GL, nblk = (H * K + GC - 1) / GC;
-  if (tiles > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
+  if (!fits(tiles, 2 * nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // the counter and the flags are 32-bit
   a = GlrArgs{};
   a.A_log = A_log;
   a.dt_bias = dt_bias;
@@ -607,29 +711,27 @@ kda_status_t by_variant(int dtype, unsigned flags, P... p) {
            : (c ? F<float, false, true>::run(p...) : F<float, false, false>::run(p...));
 }
 
+// Workgroups of a pass: as many as run at once (two on a CU), fewer tiles than that one each.
+int64_t pass_grid(const GlrArgs& a) {
+  const int64_t items = (int64_t)a.ntiles * a.nblk, most = 512;
+  return items < 1 ? 1 : items < most ? items : most;
+}
+kda_status_t clear(const GlrArgs& a, hipStream_t st) {
+  const int64_t n = (int64_t)a.ntiles * a.nblk * 2;
+  return launch(&kda_glr_clear_kernel, n / 256 + 1, 256, st, "glr clear", a.ticket, a.faults, a.flags, n);
+}
 template <typename T, bool GIVEN, bool COMPL>
 struct RunFwd {
   static kda_status_t run(const GlrArgs& a, hipStream_t st) {
-    const int64_t items = (int64_t)a.ntiles * a.nblk;
-    if (items > 0) {
-      kda_status_t s = launch(&kda_glr_fwd_kernel<T, GIVEN, COMPL, true>, grid_of(items), GT, st, "glr maps", a);
-      if (s == KDA_SUCCESS) s = launch(&kda_glr_fold_kernel<false>, (a.C + 63) / 64, 64, st, "glr fold", a);
-      if (s != KDA_SUCCESS) return s;
-    }
-    return launch(&kda_glr_fwd_kernel<T, GIVEN, COMPL, false>, grid_of(items), GT, st, "glr forward", a);
+    const kda_status_t s = clear(a, st);
+    return s != KDA_SUCCESS ? s : launch(&kda_glr_fwd_kernel<T, GIVEN, COMPL>, pass_grid(a), GT, st, "glr forward", a);
   }
 };
 template <typename T, bool GIVEN, bool COMPL>
 struct RunBwd {
   static kda_status_t run(const GlrArgs& a, hipStream_t st) {
-    const int64_t items = (int64_t)a.ntiles * a.nblk;
-    kda_status_t s = KDA_SUCCESS;
-    if (items > 0) {
-      s = launch(&kda_glr_bwd_kernel<T, GIVEN, COMPL, true>, grid_of(items), GT, st, "glr backward maps", a);
-      if (s == KDA_SUCCESS) s = launch(&kda_glr_fold_kernel<true>, (a.C + 63) / 64, 64, st, "glr fold", a);
-      if (s != KDA_SUCCESS) return s;
-    }
-    s = launch(&kda_glr_bwd_kernel<T, GIVEN, COMPL, false>, grid_of(items), GT, st, "glr backward", a);
+    kda_status_t s = clear(a, st);
+    if (s == KDA_SUCCESS) s = launch(&kda_glr_bwd_kernel<T, GIVEN, COMPL>, pass_grid(a), GT, st, "glr backward", a);
     if (s != KDA_SUCCESS || GIVEN) return s;
     return launch(&kda_glr_reduce_kernel, a.H, GRED, st, "glr reduce", a);
   }
@@ -640,6 +742,13 @@ struct RunStep {
     return launch(&kda_glr_step_kernel<T, GIVEN, COMPL>, grid, GST, st, "glr step", a);
   }
 };
+
+void carve(GlrArgs& a, char* ws, const GlrLayout& l) {
+  a.ticket = reinterpret_cast<int*>(ws + l.ticket);
+  a.faults = reinterpret_cast<unsigned*>(ws + l.faults);
+  a.flags = reinterpret_cast<int*>(ws + l.flags);
+  a.maps = reinterpret_cast<uint64_t*>(ws + l.maps);
+}
 
 }  // namespace
 }  // namespace kda
@@ -680,9 +789,8 @@ kda_status_t kda_glr_fwd(const void* x, const void* raw_gate, void* out, void* w
   a.out = out;
   a.init = initial_state;
   a.fin = final_state;
-  a.maps = reinterpret_cast<float2*>(ws + l.maps);
-  a.reset = reinterpret_cast<int*>(ws + l.reset);
-  a.states = states ? states : reinterpret_cast<float*>(ws + l.states);
+  carve(a, ws, l);
+  a.enter = states ? states : reinterpret_cast<float*>(ws + l.enter);
   return by_variant<RunFwd>(dtype, flags, a, reinterpret_cast<hipStream_t>(stream));
 }
 
@@ -713,10 +821,9 @@ kda_status_t kda_glr_bwd(const void* x, const void* raw_gate, const float* state
   a.d_init = d_initial_state;
   a.dA_log = dA_log;
   a.d_dt_bias = d_dt_bias;
-  a.maps = reinterpret_cast<float2*>(ws + l.maps);
-  a.reset = reinterpret_cast<int*>(ws + l.reset);
-  a.states = const_cast<float*>(states);
-  a.ends = reinterpret_cast<float*>(ws + l.ends);
+  carve(a, ws, l);
+  a.states = states;
+  a.enter = reinterpret_cast<float*>(ws + l.enter);
   a.part = reinterpret_cast<float2*>(ws + l.part);
   return by_variant<RunBwd>(dtype, flags, a, reinterpret_cast<hipStream_t>(stream));
 }

@@ -18,6 +18,8 @@ constexpr unsigned FLAG_RMS_NORM = 512;     // q, k divided by their root mean s
 constexpr unsigned FLAG_INTERLEAVED = 1024; // rotated pairs are channels 2i, 2i + 1
 constexpr unsigned FLAG_ZERO_REST = 2048;   // rows behind the last sequence become zeros
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // Token arrays are bf16 or fp32; arithmetic is fp32 in both, and a store
 // rounds once, to nearest even.
 template <typename T>
