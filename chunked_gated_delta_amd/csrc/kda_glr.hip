@@ -37,11 +37,14 @@
 namespace kda {
 namespace {
 
-constexpr int GR = 4;           // rows of a run
-constexpr int GS = 16;          // runs of a tile
-constexpr int GL = GR * GS;     // rows of a tile
-constexpr int GC = 128;         // channels of a tile
-constexpr int GT = GS * GC / 4; // threads
+constexpr int GR = 4;            // rows of a run
+constexpr int GS = 28;           // runs of a tile
+constexpr int GL = GR * GS;      // rows of a tile
+constexpr int GC = 64;           // channels of a tile
+constexpr int GW = GC / 4;       // lanes of a row
+constexpr int GD = GS * GW;      // threads that hold data: seven waves
+constexpr int GT = GD + GC;      // and one, a lane a channel, that finds what enters the tile
+static_assert(GD % 64 == 0 && GT == 512, "whole waves");
 constexpr int64_t kMaxChannels = (int64_t)1 << 21;  // a tile's rows span less than 2^30 bytes
 
 struct GlrArgs {
@@ -58,9 +61,10 @@ struct GlrArgs {
   float* d_init;
   const float* states;  // [tiles][C] state entering every tile (backward)
   // the pass's own, tiles counted in its order (the backward from the right):
-  float* enter;   // [tiles][C] what enters every tile (forward: states)
-  uint64_t* maps; // [tiles][C] A and B of every tile's map
-  int* flags;     // [2 nblk][tiles], one for 64 channels: 1 the map, 2 also what leaves is known
+  uint64_t* enter; // [tiles][C] what enters every tile, with KNOWN above it
+  uint64_t* maps;  // [tiles][C] A and B of every tile's map
+  int* flags;      // [nblk][tiles]: 1 the map, 2 (also) what leaves has been written
+  float* keep;     // forward: [tiles][C] what enters every tile, for the backward, or NULL
   int* ticket;    // the next tile
   unsigned* faults;
   float2* part;   // [tiles][C] sums over the tile of d_raw and of dz z
@@ -107,31 +111,35 @@ __device__ __forceinline__ float one_minus(float g2, float a) {
   return fabsf(y) < 0.25f ? -p : 1.0f - a;
 }
 
-// The sequences that start (S) or end (E) at each row of the tile, -1 for
-// none; returns whether there is any.  Ends with a barrier.
-__device__ __forceinline__ bool mark_tile(const Axis& ax, int64_t t0, int* S, int* E) {
-  const int tid = threadIdx.x;
-  for (int i = tid; i < GL; i += GT) S[i] = E[i] = -1;
+// The sequences that start (S) or end (E) at each row of the tile at t0, -1 for
+// none, and whether there is any; by one wave.
+struct Marks {
+  int S[GL], E[GL], any;
+};
+__device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, Marks& m) {
+  const int lane = threadIdx.x & 63;
+  for (int i = lane; i < GL; i += 64) m.S[i] = m.E[i] = -1;
   const int64_t t1 = t0 + GL;
   const int64_t n0 = axis_lower(ax, t0);
   int64_t n1 = axis_lower(ax, t1);
   n1 = n1 < ax.N ? n1 : ax.N;
-  __syncthreads();
+  __builtin_amdgcn_wave_barrier();
   bool any = false;
   // sequence n0 - 1 is the one that reaches the tile from before it
-  for (int64_t n = (n0 > 0 ? n0 - 1 : 0) + tid; n < n1; n += GT) {
+  for (int64_t n = (n0 > 0 ? n0 - 1 : 0) + lane; n < n1; n += 64) {
     const int64_t s = axis_start(ax, n), e = axis_start(ax, n + 1);
     if (e <= s) continue;
     if (s >= t0 && s < t1) {
-      S[s - t0] = (int)n;
+      m.S[s - t0] = (int)n;
       any = true;
     }
     if (e > t0 && e <= t1) {
-      E[e - 1 - t0] = (int)n;
+      m.E[e - 1 - t0] = (int)n;
       any = true;
     }
   }
-  return __syncthreads_or(any);
+  any = __any(any);
+  if (lane == 0) m.any = any;
 }
 
 // Loads and stores of a tile by 32-bit offsets from its first row.  The
@@ -165,10 +173,12 @@ struct Rows {
   }
 };
 
-// Device-scope words that other workgroups write while this kernel runs.  The
-// data of a tile is stored, then waited for, then flagged: each access goes to
-// where all XCDs agree (a relaxed atomic of device scope), and the wait orders
-// them without writing back or dropping whole caches.
+// Device-scope words that other workgroups write while this kernel runs, all by
+// relaxed atomics, which go to where the XCDs agree.  What leaves a tile is one
+// 64-bit word a channel, the value with KNOWN above it, so that the next tile's
+// poll brings flag and value in one round trip.  Maps fill their words: they
+// are stored, waited for, then flagged.
+constexpr uint64_t KNOWN = (uint64_t)1 << 32;
 template <typename W>
 __device__ __forceinline__ W peek(const W* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -182,46 +192,46 @@ __device__ __forceinline__ void flag_after(int* flag, int value) {
   if ((threadIdx.x & 63) == 0) post(flag, value);
 }
 
-// Polls before a wait gives up (about a second: each is a round trip to memory
-// and a 128-cycle sleep).
+// Polls before a wait gives up (about a second: each is a round trip to memory).
 constexpr int kPolls = 1 << 20;
 
-// What enters tile k (counted in the pass's order), for channel c, found by
-// the wave that has this 64-channel column `flags` of the tiles' flags.
-__device__ __forceinline__ float look_back(const GlrArgs& a, const int* flags, int k, int64_t c, bool in) {
+// What enters tile k (tiles counted in the pass's order) at channel c.  `word`
+// is a first look at the word that holds it; where that is not there yet, the
+// tile's own map is published for the tiles behind, and the flags of the 64
+// tiles before are searched for the nearest one whose leaving value is known.
+__device__ __forceinline__ float look_back(const GlrArgs& a, int* flags, int k, int64_t c, bool in, uint64_t word,
+                                           bool publish, float At, float Bt) {
+  if (__all(!in || (word & KNOWN))) return __uint_as_float((uint32_t)word);
+  if (publish) {
+    if (in) post(a.maps + (int64_t)k * a.C + c, (uint64_t)__float_as_uint(Bt) << 32 | __float_as_uint(At));
+    flag_after(flags + k, 1);
+  }
   const int lane = threadIdx.x & 63;
-  int p = 0;
-  bool found = false;
   for (int poll = 0; poll < kPolls; ++poll) {
     const int q = k - 1 - lane;
     const int f = q >= 0 ? peek(flags + q) : 0;
+    word = in ? peek(a.enter + (int64_t)k * a.C + c) : KNOWN;
+    if (__all(word & KNOWN)) return __uint_as_float((uint32_t)word);
     const uint64_t known = __ballot(f == 2), mapped = __ballot(f >= 1);
-    if (known) {
-      p = __builtin_ctzll(known);
-      const uint64_t between = ((uint64_t)1 << p) - 1;
-      if ((mapped & between) == between) {
-        found = true;
-        break;
-      }
+    if (!known) continue;
+    const int p = __builtin_ctzll(known);
+    const uint64_t between = ((uint64_t)1 << p) - 1;
+    if ((mapped & between) != between) continue;
+    // tiles k - p .. k - 1 lie between; their maps are loaded 32 at a time, in one round trip
+    constexpr int U = 32;
+    float s = in ? __uint_as_float((uint32_t)peek(a.enter + (int64_t)(k - p) * a.C + c)) : 0.f;
+    for (int j = k - p; j < k; j += U) {
+      uint64_t m[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) m[u] = in && j + u < k ? peek(a.maps + (int64_t)(j + u) * a.C + c) : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j + u < k) s = __uint_as_float((uint32_t)m[u]) * s + __uint_as_float((uint32_t)(m[u] >> 32));
     }
-    __builtin_amdgcn_s_sleep(2);
+    return s;
   }
-  if (!found) {
-    if (lane == 0) atomicOr(a.faults, FAULT_WAIT_TIMEOUT);
-    return 0.f;
-  }
-  if (!in) return 0.f;
-  // tiles k - p .. k - 1 lie between; their maps are loaded 8 at a time
-  float s = peek(a.enter + (int64_t)(k - p) * a.C + c);
-  for (int q = k - p; q < k; q += 8) {
-    uint64_t m[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) m[u] = q + u < k ? peek(a.maps + (int64_t)(q + u) * a.C + c) : 0;
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (q + u < k) s = __uint_as_float((uint32_t)m[u]) * s + __uint_as_float((uint32_t)(m[u] >> 32));
-  }
-  return s;
+  if (lane == 0) atomicOr(a.faults, FAULT_WAIT_TIMEOUT);
+  return 0.f;
 }
 
 struct Tile {
@@ -230,15 +240,16 @@ struct Tile {
 };
 
 // Joins the runs of a tile, in the pass's order (REV: from the last run), by
-// the waves of its two 64-channel columns: the tile's map to the others, what
-// enters the tile from them (not where the tile begins `fresh`, with a
-// sequence's first row), and what enters every run into t.A.
+// the wave that holds no data: finds what enters the tile (not where the tile
+// begins `fresh`, with a sequence's first row), hands on what leaves it, and
+// puts what enters every run into t.A.
 template <bool REV>
 __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, int k, int blk, bool fresh) {
-  const int w = threadIdx.x >> 6;
-  const int ch = threadIdx.x;  // of the tile; w < 2
+  const int ch = threadIdx.x & 63;
   const int64_t c = (int64_t)blk * GC + ch;
   const bool in = c < a.C;
+  const bool ask = k > 0 && !fresh, last = k + 1 == a.ntiles;
+  const uint64_t word = ask && in ? peek(a.enter + (int64_t)k * a.C + c) : KNOWN;
   float At = 1.f, Bt = 0.f;
   bool resets = false;
 #pragma unroll
@@ -250,27 +261,21 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, int k, int 
     Bt = ri ? Bi : Ai * Bt + Bi;
     At *= Ai;
   }
-  int* flags = a.flags + (int64_t)(blk * 2 + w) * a.ntiles;
-  const bool last = k + 1 == a.ntiles;
-  float s = 0.f;
-  if (resets) {
-    // what leaves is known, whatever enters; that is only needed by rows before the reset
+  int* flags = a.flags + (int64_t)blk * a.ntiles;
+  uint64_t* to = a.enter + (int64_t)(k + 1) * a.C + c;
+  float s = 0.f, leave = Bt;
+  if (resets) {  // what leaves does not depend on what enters
     if (!last) {
-      if (in) post(a.enter + (int64_t)(k + 1) * a.C + c, Bt);
+      if (in) post(to, KNOWN | __float_as_uint(leave));
       flag_after(flags + k, 2);
     }
-    if (k > 0 && !fresh) s = look_back(a, flags, k, c, in);
+    if (ask) s = look_back(a, flags, k, c, in, word, false, At, Bt);
   } else {
-    if (!last) {
-      if (in) post(a.maps + (int64_t)k * a.C + c, (uint64_t)__float_as_uint(Bt) << 32 | __float_as_uint(At));
-      flag_after(flags + k, 1);
-    }
-    if (k > 0) s = look_back(a, flags, k, c, in);
-    if (!last) {
-      if (in) post(a.enter + (int64_t)(k + 1) * a.C + c, At * s + Bt);
-      flag_after(flags + k, 2);
-    }
+    if (ask) s = look_back(a, flags, k, c, in, word, !last, At, Bt);
+    leave = At * s + Bt;
+    if (!last && in) post(to, KNOWN | __float_as_uint(leave));
   }
+  if (a.keep && in && !last) a.keep[(int64_t)(k + 1) * a.C + c] = leave;
 #pragma unroll
   for (int i = 0; i < GS; ++i) {
     const int run = REV ? GS - 1 - i : i;
@@ -278,26 +283,23 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, int k, int 
     t.A[run][ch] = s;
     s = t.reset[run] ? Bi : Ai * s + Bi;
   }
+  if (!last && !resets) flag_after(flags + k, 2);
 }
 
-// The next tile of the pass, for all threads; `next` is thread 0's ticket.
-__device__ __forceinline__ int64_t take(const GlrArgs& a, int* slot, int next) {
-  __syncthreads();
-  if (threadIdx.x == 0) *slot = next;
-  __syncthreads();
-  return *slot;
-}
 __device__ __forceinline__ int draw_ticket(const GlrArgs& a) {
-  return threadIdx.x == 0 ? (int)__hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  return __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__global__ void __launch_bounds__(256) kda_glr_clear_kernel(int* ticket, unsigned* faults, int* flags, int64_t n) {
+// Clears the counter, the fault word, the flags and the words that other
+// workgroups wait for (a kernel rather than a memset, so that a captured graph
+// replays it as a kernel node).
+__global__ void __launch_bounds__(256) kda_glr_clear_kernel(int* ticket, unsigned* faults, uint4* words, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i == 0) {
     *ticket = 0;
     *faults = 0;
   }
-  if (i < n) flags[i] = 0;
+  for (int64_t j = i; j < n; j += (int64_t)gridDim.x * 256) words[j] = make_uint4(0, 0, 0, 0);
 }
 
 // State (or gradient) of sequence n at 4 channels, zeros where there is none.
@@ -307,33 +309,11 @@ __device__ __forceinline__ void state4(const float* p, int n, int64_t C, int64_t
   if (p && in) load_f4(p + (int64_t)n * C + c, s);
 }
 
+// One run of 4 rows by 4 channels, in one thread: decays and inputs.
 template <typename T, bool GIVEN, bool COMPL>
-__global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
-  __shared__ Tile t;
-  __shared__ int sS[GL], sE[GL], slot;
-  const int tid = threadIdx.x, lane = tid & 31, run = tid >> 5;
-  const int64_t rows = axis_rows(a.ax);
-  const int64_t items = (int64_t)a.ntiles * a.nblk;
-  const int row_bytes = (int)(a.C * sizeof(T));
-  int64_t item = take(a, &slot, draw_ticket(a));
-  while (item < items) {
-    const int next = draw_ticket(a);
-    const int k = (int)(item / a.nblk), blk = (int)(item % a.nblk);
-    const int64_t c = (int64_t)blk * GC + lane * 4;
-    const bool in = c < a.C;
-    const int64_t t0 = (int64_t)k * GL;
-    const int voff = in ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
-    const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), os(a.out, t0, rows, a.C);
-    raw4<T> xr[GR], gr[GR];
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      gr[i] = gs.load(voff, i * row_bytes);
-      xr[i] = xs.load(voff, i * row_bytes);
-    }
-    Gate<GIVEN> gate;
-    gate.init(a, in ? c : 0);
-    const bool marked = mark_tile(a.ax, t0, sS, sE);
-    float av[GR][4], u[GR][4];
+struct Run {
+  float a[GR][4], u[GR][4];
+  __device__ __forceinline__ void make(const Gate<GIVEN>& gate, const raw4<T> (&xr)[GR], const raw4<T> (&gr)[GR]) {
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
       float xv[4], gv[4];
@@ -342,52 +322,147 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float g2 = gate.g2(gv[j], j);
-        av[i][j] = fexp2(g2);
-        u[i][j] = COMPL ? one_minus(g2, av[i][j]) * xv[j] : xv[j];
+        a[i][j] = fexp2(g2);
+        u[i][j] = COMPL ? one_minus(g2, a[i][j]) * xv[j] : xv[j];
       }
     }
-    float A[4], B[4];
-    bool reset = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      A[j] = 1.f;
-      B[j] = 0.f;
+  }
+};
+
+// Seven waves hold the data and one finds what enters the tiles, so that rows
+// are under way while it waits for other workgroups (loads come back in order:
+// a wave that had asked for rows could not see a word before they arrive).
+// They run a tile apart, with one barrier a tile: while the one joins tile i,
+// the seven write the outputs of tile i - 1, form the maps of tile i + 1 from
+// rows that have arrived, and ask for the rows of tile i + 2.  A workgroup
+// holds the tickets of those tiles and works on them in order, so the lowest
+// unfinished ticket is always being worked on.
+template <typename T, bool GIVEN, bool COMPL>
+__global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
+  __shared__ Tile tiles[2];
+  __shared__ Marks marks[4];
+  __shared__ int slot[4];  // tickets, by turns
+  const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
+  const int64_t rows = axis_rows(a.ax);
+  const int items = a.ntiles * a.nblk;
+  if (tid >= GD) {
+    if (tid == GD)
+      for (int i = 0; i < 3; ++i) slot[i] = draw_ticket(a);
+    __builtin_amdgcn_wave_barrier();
+    for (int i = 0; i < 2; ++i)
+      if (slot[i] < items) mark_tile(a.ax, (int64_t)(slot[i] / a.nblk) * GL, marks[i]);
+    __syncthreads();  // tickets and marks
+    __syncthreads();  // the maps of the first tile
+    for (int i = 0;; ++i) {
+      const int item = slot[i & 3];
+      if (item >= items) break;
+      const int ahead = slot[(i + 2) & 3];
+      int after = 0;
+      if (tid == GD) after = draw_ticket(a);
+      const Marks& m = marks[i & 3];
+      join_runs<false>(a, tiles[i & 1], item / a.nblk, item % a.nblk, m.any && m.S[0] >= 0);
+      if (ahead < items) mark_tile(a.ax, (int64_t)(ahead / a.nblk) * GL, marks[(i + 2) & 3]);
+      if (tid == GD) slot[(i + 3) & 3] = after;
+      __syncthreads();  // what enters tile i, the maps of tile i + 1
     }
+  } else {
+    const int row_bytes = (int)(a.C * sizeof(T));
+    raw4<T> xr[GR], gr[GR];
+    auto place = [&](int item, int64_t& t0, int64_t& c) {
+      t0 = (int64_t)(item / a.nblk) * GL;
+      c = (int64_t)(item % a.nblk) * GC + lane * 4;
+      return c < a.C ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+    };
+    auto fetch = [&](int item) {
+      int64_t t0, c;
+      const int voff = place(item, t0, c);
+      const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C);
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      if (marked && sS[run * GR + i] >= 0) {
-        reset = true;
-        state4(a.init, sS[run * GR + i], a.C, c, in, B);
+      for (int i = 0; i < GR; ++i) {
+        gr[i] = gs.load(voff, i * row_bytes);
+        xr[i] = xs.load(voff, i * row_bytes);
       }
+    };
+    // the maps of tile i, from rows that were asked for
+    auto map = [&](int item, int i, Run<T, GIVEN, COMPL>& r) {
+      int64_t t0, c;
+      place(item, t0, c);
+      const bool in = c < a.C;
+      Gate<GIVEN> gate;
+      gate.init(a, in ? c : 0);
+      r.make(gate, xr, gr);
+      const Marks& m = marks[i & 3];
+      Tile& t = tiles[i & 1];
+      float A[4], B[4];
+      bool reset = false;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        A[j] *= av[i][j];
-        B[j] = av[i][j] * B[j] + u[i][j];
+        A[j] = 1.f;
+        B[j] = 0.f;
       }
-    }
-    store4(&t.A[run][lane * 4], A);
-    store4(&t.B[run][lane * 4], B);
-    if (lane == 0) t.reset[run] = reset;
-    __syncthreads();
-    if (tid < GC) join_runs<false>(a, t, k, blk, marked && sS[0] >= 0);
-    __syncthreads();
-    float h[4];
-    load_f4(&t.A[run][lane * 4], h);
+      const bool marked = m.any;
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      if (marked && sS[run * GR + i] >= 0) state4(a.init, sS[run * GR + i], a.C, c, in, h);
+      for (int q = 0; q < GR; ++q) {
+        if (marked && m.S[run * GR + q] >= 0) {
+          reset = true;
+          state4(a.init, m.S[run * GR + q], a.C, c, in, B);
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = av[i][j] * h[j] + u[i][j];
-      os.store(voff, i * row_bytes, h);
-      if (marked && a.fin && in && sE[run * GR + i] >= 0) store4(a.fin + (int64_t)sE[run * GR + i] * a.C + c, h);
-    }
-    if (a.zero_rest && t0 + GL > rows && in) {
-      for (int i = 0; i < GR; ++i) {
-        const int64_t r = t0 + run * GR + i;
-        if (r >= rows && r < a.ax.total) store_zero4(static_cast<T*>(a.out) + r * a.C + c);
+        for (int j = 0; j < 4; ++j) {
+          A[j] *= r.a[q][j];
+          B[j] = r.a[q][j] * B[j] + r.u[q][j];
+        }
       }
+      store4(&t.A[run][lane * 4], A);
+      store4(&t.B[run][lane * 4], B);
+      if (lane == 0) t.reset[run] = reset;
+    };
+    // the outputs of tile i
+    auto finish = [&](int item, int i, const Run<T, GIVEN, COMPL>& r) {
+      int64_t t0, c;
+      const int voff = place(item, t0, c);
+      const bool in = c < a.C;
+      const Marks& m = marks[i & 3];
+      const bool marked = m.any;
+      float h[4];
+      load_f4(&tiles[i & 1].A[run][lane * 4], h);
+      const Rows<T> os(a.out, t0, rows, a.C);
+#pragma unroll
+      for (int q = 0; q < GR; ++q) {
+        if (marked && m.S[run * GR + q] >= 0) state4(a.init, m.S[run * GR + q], a.C, c, in, h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = r.a[q][j] * h[j] + r.u[q][j];
+        os.store(voff, q * row_bytes, h);
+        if (marked && a.fin && in && m.E[run * GR + q] >= 0) store4(a.fin + (int64_t)m.E[run * GR + q] * a.C + c, h);
+      }
+      if (a.zero_rest && t0 + GL > rows && in) {
+        for (int q = 0; q < GR; ++q) {
+          const int64_t t = t0 + run * GR + q;
+          if (t >= rows && t < a.ax.total) store_zero4(static_cast<T*>(a.out) + t * a.C + c);
+        }
+      }
+    };
+    __syncthreads();  // tickets and marks
+    int item = slot[0], next = slot[1];
+    Run<T, GIVEN, COMPL> now, then;
+    if (item < items) {
+      fetch(item);
+      map(item, 0, now);
+      if (next < items) fetch(next);
     }
-    item = take(a, &slot, next);
+    __syncthreads();  // the maps of the first tile
+    for (int i = 0; item < items; ++i) {
+      const int ahead = slot[(i + 2) & 3];
+      if (next < items) {
+        map(next, i + 1, then);
+        if (ahead < items) fetch(ahead);
+      }
+      __syncthreads();  // what enters tile i, the maps of tile i + 1
+      finish(item, i, now);
+      now = then;
+      item = next;
+      next = ahead;
+    }
   }
   if (a.fin) {  // empty sequences hand their state on
     for (int64_t n = blockIdx.x; n < a.ax.N; n += gridDim.x) {
@@ -401,184 +476,195 @@ template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
   __shared__ Tile t;   // of e, from the right
   __shared__ Tile ft;  // of h
-  __shared__ int sS[GL], sE[GL], slot;
-  const int tid = threadIdx.x, lane = tid & 31, run = tid >> 5;
+  __shared__ Marks m;
+  __shared__ int slot;
+  const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
-  const int64_t items = (int64_t)a.ntiles * a.nblk;
+  const int items = a.ntiles * a.nblk;
   const int row_bytes = (int)(a.C * sizeof(T));
-  int64_t item = take(a, &slot, draw_ticket(a));
-  while (item < items) {
-    const int next = draw_ticket(a);
-    const int k = (int)(item / a.nblk), blk = (int)(item % a.nblk);
-    const int tile = a.ntiles - 1 - k;
-    const int64_t c = (int64_t)blk * GC + lane * 4;
-    const bool in = c < a.C;
-    const int64_t t0 = (int64_t)tile * GL, tr = t0 + run * GR;
-    const int voff = in ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
-    const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
-    raw4<T> xr[GR], gr[GR], dr[GR];
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      gr[i] = gs.load(voff, i * row_bytes);
-      dr[i] = ds.load(voff, i * row_bytes);
-      xr[i] = xs.load(voff, i * row_bytes);
-    }
-    Gate<GIVEN> gate;
-    gate.init(a, in ? c : 0);
-    const bool marked = mark_tile(a.ax, t0, sS, sE);
-    float av[GR][4], b[GR][4];  // decay, input scale
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      float gv[4];
-      widen4(gr[i], gv);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float g2 = gate.g2(gv[j], j);
-        av[i][j] = fexp2(g2);
-        b[i][j] = COMPL ? one_minus(g2, av[i][j]) : 1.0f;
-      }
-    }
-    // the run's map of e; rows behind the last sequence hand nothing on
-    {
-      float P[4], Q[4];
-      bool reset = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        P[j] = 1.f;
-        Q[j] = 0.f;
-      }
-#pragma unroll
-      for (int i = GR - 1; i >= 0; --i) {
-        if (tr + i < rows) {
-          if (marked && sE[run * GR + i] >= 0) {
-            reset = true;
-            state4(a.d_final, sE[run * GR + i], a.C, c, in, Q);
-          }
-          float dv[4];
-          widen4(dr[i], dv);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            P[j] *= av[i][j];
-            Q[j] = av[i][j] * (dv[j] + Q[j]);
-          }
-        }
-      }
-      store4(&t.A[run][lane * 4], P);
-      store4(&t.B[run][lane * 4], Q);
-      if (lane == 0) t.reset[run] = reset;
-    }
-    // the run's map of h
-    {
-      float A[4], B[4];
-      bool reset = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        A[j] = 1.f;
-        B[j] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        if (marked && sS[run * GR + i] >= 0) {
-          reset = true;
-          state4(a.init, sS[run * GR + i], a.C, c, in, B);
-        }
-        float xv[4];
-        widen4(xr[i], xv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          A[j] *= av[i][j];
-          B[j] = av[i][j] * B[j] + b[i][j] * xv[j];
-        }
-      }
-      store4(&ft.A[run][lane * 4], A);
-      store4(&ft.B[run][lane * 4], B);
-      if (lane == 0) ft.reset[run] = reset;
-    }
+  for (;;) {
+    if (tid == GD) slot = draw_ticket(a);
     __syncthreads();
-    if (tid < GC) {
-      join_runs<true>(a, t, k, blk, marked && sE[GL - 1] >= 0);
-    } else if (tid < 2 * GC) {
-      // what enters every run, by the next two waves
-      const int ch = tid - GC;
+    const int item = slot;
+    if (item >= items) break;
+    const int k = item / a.nblk, blk = item % a.nblk;
+    const int tile = a.ntiles - 1 - k;
+    const int64_t t0 = (int64_t)tile * GL;
+    if (tid >= GD) {
+      const int ch = tid - GD;
       const int64_t cc = (int64_t)blk * GC + ch;
       float s = cc < a.C ? a.states[(int64_t)tile * a.C + cc] : 0.f;
+      mark_tile(a.ax, t0, m);
+      __syncthreads();  // the marks
+      __syncthreads();  // the runs' maps
 #pragma unroll
       for (int i = 0; i < GS; ++i) {
         const float Ai = ft.A[i][ch], Bi = ft.B[i][ch];
         ft.A[i][ch] = s;
         s = ft.reset[i] ? Bi : Ai * s + Bi;
       }
-    }
-    __syncthreads();
-    float h[4], hp[GR][4];
-    load_f4(&ft.A[run][lane * 4], h);
+      join_runs<true>(a, t, k, blk, m.any && m.E[GL - 1] >= 0);
+      __syncthreads();  // what enters them
+      if constexpr (!GIVEN) {
+        __syncthreads();  // the runs' sums
+        if (cc < a.C) {
+          float d = 0.f, z = 0.f;
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      if (marked && sS[run * GR + i] >= 0) state4(a.init, sS[run * GR + i], a.C, c, in, h);
-      float xv[4];
-      widen4(xr[i], xv);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        hp[i][j] = COMPL ? h[j] - xv[j] : h[j];
-        h[j] = av[i][j] * h[j] + b[i][j] * xv[j];
+          for (int i = 0; i < GS; ++i) {
+            d += ft.B[i][ch];
+            z += ft.A[i][ch];
+          }
+          a.part[(int64_t)tile * a.C + cc] = make_float2(d, z);
+        }
       }
-    }
-    float e[4], dsum[4], zsum[4];
-    load_f4(&t.A[run][lane * 4], e);
+    } else {
+      const int64_t c = (int64_t)blk * GC + lane * 4;
+      const bool in = c < a.C;
+      const int64_t tr = t0 + run * GR;
+      const int voff = in ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+      const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
+      raw4<T> xr[GR], gr[GR], dr[GR];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dsum[j] = zsum[j] = 0.f;
-    const Rows<T> dxs(a.out, t0, rows, a.C), dgs(a.dg, t0, rows, a.C);
+      for (int i = 0; i < GR; ++i) {
+        gr[i] = gs.load(voff, i * row_bytes);
+        dr[i] = ds.load(voff, i * row_bytes);
+        xr[i] = xs.load(voff, i * row_bytes);
+      }
+      Gate<GIVEN> gate;
+      gate.init(a, in ? c : 0);
+      __syncthreads();  // the marks
+      const bool marked = m.any;
+      float av[GR][4], b[GR][4];  // decay, input scale
 #pragma unroll
-    for (int i = GR - 1; i >= 0; --i) {
-      if (tr + i < rows) {
-        if (marked && sE[run * GR + i] >= 0) state4(a.d_final, sE[run * GR + i], a.C, c, in, e);
-        float dv[4], gv[4], dx[4], dg[4];
-        widen4(dr[i], dv);
+      for (int i = 0; i < GR; ++i) {
+        float gv[4];
         widen4(gr[i], gv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float dh = dv[j] + e[j];
-          e[j] = av[i][j] * dh;
-          dx[j] = b[i][j] * dh;
-          dg[j] = e[j] * hp[i][j];
-          if constexpr (!GIVEN) {
-            // dg/dz = lb s (1 - s), s = 1 / (1 + w), w = exp(-z).  w is kept
-            // finite (a comparison, so that NaN stays) so that w s does not
-            // become infinity times zero.
-            const float mz = gv[j] * gate.na + gate.nb[j];  // -z log2(e)
-            const float w = fexp2(mz > 126.f ? 126.f : mz);
-            const float s = __builtin_amdgcn_rcpf(1.0f + w);
-            const float dz = dg[j] * (a.lb * s * (w * s));
-            zsum[j] += dz * (mz * -0.6931471805599453f);
-            dg[j] = dz * (gate.na * -0.6931471805599453f);  // dz/draw = exp(A_log)
-            dsum[j] += dg[j];
+          const float g2 = gate.g2(gv[j], j);
+          av[i][j] = fexp2(g2);
+          b[i][j] = COMPL ? one_minus(g2, av[i][j]) : 1.0f;
+        }
+      }
+      // the run's map of e; rows behind the last sequence hand nothing on
+      {
+        float P[4], Q[4];
+        bool reset = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          P[j] = 1.f;
+          Q[j] = 0.f;
+        }
+#pragma unroll
+        for (int i = GR - 1; i >= 0; --i) {
+          if (tr + i < rows) {
+            if (marked && m.E[run * GR + i] >= 0) {
+              reset = true;
+              state4(a.d_final, m.E[run * GR + i], a.C, c, in, Q);
+            }
+            float dv[4];
+            widen4(dr[i], dv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              P[j] *= av[i][j];
+              Q[j] = av[i][j] * (dv[j] + Q[j]);
+            }
           }
         }
-        dxs.store(voff, i * row_bytes, dx);
-        dgs.store(voff, i * row_bytes, dg);
-        if (marked && a.d_init && in && sS[run * GR + i] >= 0)
-          store4(a.d_init + (int64_t)sS[run * GR + i] * a.C + c, e);
-      } else if (in && a.zero_rest && tr + i < a.ax.total) {
-        store_zero4(static_cast<T*>(a.out) + (tr + i) * a.C + c);
-        store_zero4(static_cast<T*>(a.dg) + (tr + i) * a.C + c);
+        store4(&t.A[run][lane * 4], P);
+        store4(&t.B[run][lane * 4], Q);
+        if (lane == 0) t.reset[run] = reset;
       }
-    }
-    if constexpr (!GIVEN) {
-      // ft is free: a thread's own entry of it is all that was read since the last barrier
-      store4(&ft.B[run][lane * 4], dsum);
-      store4(&ft.A[run][lane * 4], zsum);
-      __syncthreads();
-      if (tid < GC && (int64_t)blk * GC + tid < a.C) {
-        float d = 0.f, z = 0.f;
+      // the run's map of h
+      {
+        float A[4], B[4];
+        bool reset = false;
 #pragma unroll
-        for (int i = 0; i < GS; ++i) {
-          d += ft.B[i][tid];
-          z += ft.A[i][tid];
+        for (int j = 0; j < 4; ++j) {
+          A[j] = 1.f;
+          B[j] = 0.f;
         }
-        a.part[(int64_t)tile * a.C + (int64_t)blk * GC + tid] = make_float2(d, z);
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+          if (marked && m.S[run * GR + i] >= 0) {
+            reset = true;
+            state4(a.init, m.S[run * GR + i], a.C, c, in, B);
+          }
+          float xv[4];
+          widen4(xr[i], xv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            A[j] *= av[i][j];
+            B[j] = av[i][j] * B[j] + b[i][j] * xv[j];
+          }
+        }
+        store4(&ft.A[run][lane * 4], A);
+        store4(&ft.B[run][lane * 4], B);
+        if (lane == 0) ft.reset[run] = reset;
+      }
+      __syncthreads();  // the runs' maps
+      __syncthreads();  // what enters them
+      float h[4], hp[GR][4];
+      load_f4(&ft.A[run][lane * 4], h);
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        if (marked && m.S[run * GR + i] >= 0) state4(a.init, m.S[run * GR + i], a.C, c, in, h);
+        float xv[4];
+        widen4(xr[i], xv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hp[i][j] = COMPL ? h[j] - xv[j] : h[j];
+          h[j] = av[i][j] * h[j] + b[i][j] * xv[j];
+        }
+      }
+      float e[4], dsum[4], zsum[4];
+      load_f4(&t.A[run][lane * 4], e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dsum[j] = zsum[j] = 0.f;
+      const Rows<T> dxs(a.out, t0, rows, a.C), dgs(a.dg, t0, rows, a.C);
+#pragma unroll
+      for (int i = GR - 1; i >= 0; --i) {
+        if (tr + i < rows) {
+          if (marked && m.E[run * GR + i] >= 0) state4(a.d_final, m.E[run * GR + i], a.C, c, in, e);
+          float dv[4], gv[4], dx[4], dg[4];
+          widen4(dr[i], dv);
+          widen4(gr[i], gv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float dh = dv[j] + e[j];
+            e[j] = av[i][j] * dh;
+            dx[j] = b[i][j] * dh;
+            dg[j] = e[j] * hp[i][j];
+            if constexpr (!GIVEN) {
+              // dg/dz = lb s (1 - s), s = 1 / (1 + w), w = exp(-z).  w is kept
+              // finite (a comparison, so that NaN stays) so that w s does not
+              // become infinity times zero.
+              const float mz = gv[j] * gate.na + gate.nb[j];  // -z log2(e)
+              const float w = fexp2(mz > 126.f ? 126.f : mz);
+              const float s = __builtin_amdgcn_rcpf(1.0f + w);
+              const float dz = dg[j] * (a.lb * s * (w * s));
+              zsum[j] += dz * (mz * -0.6931471805599453f);
+              dg[j] = dz * (gate.na * -0.6931471805599453f);  // dz/draw = exp(A_log)
+              dsum[j] += dg[j];
+            }
+          }
+          dxs.store(voff, i * row_bytes, dx);
+          dgs.store(voff, i * row_bytes, dg);
+          if (marked && a.d_init && in && m.S[run * GR + i] >= 0)
+            store4(a.d_init + (int64_t)m.S[run * GR + i] * a.C + c, e);
+        } else if (in && a.zero_rest && tr + i < a.ax.total) {
+          store_zero4(static_cast<T*>(a.out) + (tr + i) * a.C + c);
+          store_zero4(static_cast<T*>(a.dg) + (tr + i) * a.C + c);
+        }
+      }
+      if constexpr (!GIVEN) {
+        // ft is free: a thread's own entry of it is all that was read since the last barrier
+        store4(&ft.B[run][lane * 4], dsum);
+        store4(&ft.A[run][lane * 4], zsum);
+        __syncthreads();  // the runs' sums
       }
     }
-    item = take(a, &slot, next);
+    __syncthreads();
   }
   if (a.d_init) {
     for (int64_t n = blockIdx.x; n < a.ax.N; n += gridDim.x) {
@@ -650,9 +736,9 @@ __global__ void __launch_bounds__(GST) kda_glr_step_kernel(GlrArgs a) {
 }
 
 // The counter and the fault word (where kda_workspace_faults looks for it) come
-// first.  The forward keeps the states here where the caller takes none.
+// first, then what is cleared: the flags and the words of what enters a tile.
 struct GlrLayout {
-  size_t ticket, faults, flags, maps, enter, part, total;
+  size_t ticket, faults, flags, enter, maps, part, total;
 };
 GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
   const size_t tiles = (size_t)((T_total + GL - 1) / GL), w = tiles * (size_t)C;
@@ -660,9 +746,9 @@ GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
   l.ticket = 0;
   l.faults = 4;
   l.flags = 256;
-  l.maps = l.flags + align256(tiles * 2 * (size_t)((C + GC - 1) / GC) * sizeof(int));
-  l.enter = l.maps + align256(w * sizeof(uint64_t));
-  l.part = l.enter + align256(w * sizeof(float));
+  l.enter = l.flags + align256(tiles * (size_t)((C + GC - 1) / GC) * sizeof(int));
+  l.maps = l.enter + align256(w * sizeof(uint64_t));
+  l.part = l.maps + align256(w * sizeof(uint64_t));
   l.total = l.part + (bwd ? align256(w * sizeof(float2)) : 0);
   return l;
 }
@@ -686,7 +772,7 @@ kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, f
   if (cu_seqlens && T > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   if (!(flags & FLAG_GATE_GIVEN) && !aligned(dt_bias, 16)) return KDA_ERR_INVALID;
   const int64_t tiles = (B * T + GL - 1) / GL, nblk = (H * K + GC - 1) / GC;
-  if (!fits(tiles, 2 * nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // the counter and the flags are 32-bit
+  if (!fits(tiles, nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // the counter and the flags are 32-bit
   a = GlrArgs{};
   a.A_log = A_log;
   a.dt_bias = dt_bias;
@@ -717,8 +803,10 @@ int64_t pass_grid(const GlrArgs& a) {
   return items < 1 ? 1 : items < most ? items : most;
 }
 kda_status_t clear(const GlrArgs& a, hipStream_t st) {
-  const int64_t n = (int64_t)a.ntiles * a.nblk * 2;
-  return launch(&kda_glr_clear_kernel, n / 256 + 1, 256, st, "glr clear", a.ticket, a.faults, a.flags, n);
+  const int64_t n = (reinterpret_cast<char*>(a.maps) - reinterpret_cast<char*>(a.flags)) / sizeof(uint4);
+  const int64_t blocks = (n + 255) / 256, most = 2048;
+  return launch(&kda_glr_clear_kernel, blocks < 1 ? 1 : blocks < most ? blocks : most, 256, st, "glr clear", a.ticket,
+                a.faults, reinterpret_cast<uint4*>(a.flags), n);
 }
 template <typename T, bool GIVEN, bool COMPL>
 struct RunFwd {
@@ -747,6 +835,7 @@ void carve(GlrArgs& a, char* ws, const GlrLayout& l) {
   a.ticket = reinterpret_cast<int*>(ws + l.ticket);
   a.faults = reinterpret_cast<unsigned*>(ws + l.faults);
   a.flags = reinterpret_cast<int*>(ws + l.flags);
+  a.enter = reinterpret_cast<uint64_t*>(ws + l.enter);
   a.maps = reinterpret_cast<uint64_t*>(ws + l.maps);
 }
 
@@ -790,7 +879,7 @@ kda_status_t kda_glr_fwd(const void* x, const void* raw_gate, void* out, void* w
   a.init = initial_state;
   a.fin = final_state;
   carve(a, ws, l);
-  a.enter = states ? states : reinterpret_cast<float*>(ws + l.enter);
+  a.keep = states;
   return by_variant<RunFwd>(dtype, flags, a, reinterpret_cast<hipStream_t>(stream));
 }
 
@@ -823,7 +912,6 @@ kda_status_t kda_glr_bwd(const void* x, const void* raw_gate, const float* state
   a.d_dt_bias = d_dt_bias;
   carve(a, ws, l);
   a.states = states;
-  a.enter = reinterpret_cast<float*>(ws + l.enter);
   a.part = reinterpret_cast<float2*>(ws + l.part);
   return by_variant<RunBwd>(dtype, flags, a, reinterpret_cast<hipStream_t>(stream));
 }
