@@ -402,7 +402,7 @@ kda_status_t conv_prepare(ConvArgs& a, const void* x, int64_t x_stride, const vo
   a.w = static_cast<const float*>(w);
   a.bias = static_cast<const float*>(bias);
   a.init = init;
-  a.ax = Axis{cu_seqlens, T, B * T, (int)N};
+  a.ax = make_axis(cu_seqlens, T, B * T, N);
   a.C = C;
   a.groups = C / (bwd ? BV : CV);
   a.rows = tile_rows(B * T, a.groups, bwd);

@@ -30,6 +30,8 @@
 //
 // All arithmetic is fp32.
 
+#include <limits.h>
+
 #include "../../include/kda.h"
 #include "kda_host.h"
 #include "kda_token.h"
@@ -44,7 +46,7 @@ constexpr int GC = 64;           // channels of a tile
 constexpr int GW = GC / 4;       // lanes of a row
 constexpr int GD = GS * GW;      // threads that hold data: seven waves
 constexpr int GT = GD + GC;      // and one, a lane a channel, that finds what enters the tile
-static_assert(GD % 64 == 0 && GT == 512, "whole waves");
+static_assert(GD % 64 == 0 && GT == 512 && GS <= 32, "whole waves, runs in a 32-bit mask");
 constexpr int64_t kMaxChannels = (int64_t)1 << 21;  // a tile's rows span less than 2^30 bytes
 
 struct GlrArgs {
@@ -62,10 +64,10 @@ struct GlrArgs {
   const float* states;  // [tiles][C] state entering every tile (backward)
   // the pass's own, tiles counted in its order (the backward from the right):
   uint64_t* enter; // [tiles][C] what enters every tile, with KNOWN above it
-  uint64_t* maps;  // [tiles][C] A and B of every tile's map
-  int* flags;      // [nblk][tiles]: 1 the map, 2 (also) what leaves has been written
+  uint64_t* maps;  // [tiles][C] A (with KNOWN_MAP) and B of every tile's map
   float* keep;     // forward: [tiles][C] what enters every tile, for the backward, or NULL
-  int* ticket;    // the next tile
+  int* tickets;   // [sets] the next tile of each set of columns, TICKET_LINE apart
+  int sets;
   unsigned* faults;
   float2* part;   // [tiles][C] sums over the tile of d_raw and of dz z
   float* dA_log;
@@ -118,28 +120,31 @@ struct Marks {
 };
 __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, Marks& m) {
   const int lane = threadIdx.x & 63;
-  for (int i = lane; i < GL; i += 64) m.S[i] = m.E[i] = -1;
   const int64_t t1 = t0 + GL;
+  // n0, n1: first sequences that start at t0, t1 or behind
   const int64_t n0 = axis_lower(ax, t0);
-  int64_t n1 = axis_lower(ax, t1);
+  int64_t n1 = n0;
+  if (ax.cu) {
+    const bool before = n0 + lane <= ax.N && axis_start(ax, n0 + lane) < t1;
+    n1 += __popcll(__ballot(before));
+    if (n1 == n0 + 64) n1 = axis_lower(ax, t1);
+  } else {
+    n1 = axis_lower(ax, t1);
+  }
+  // (an end is the next one's start, so one at the very end of the tile is no start of it)
+  const bool any = n1 > n0 || (n0 <= ax.N && axis_start(ax, n0) == t1);
+  if (lane == 0) m.any = any;
+  if (!any) return;
+  for (int i = lane; i < GL; i += 64) m.S[i] = m.E[i] = -1;
   n1 = n1 < ax.N ? n1 : ax.N;
   __builtin_amdgcn_wave_barrier();
-  bool any = false;
   // sequence n0 - 1 is the one that reaches the tile from before it
   for (int64_t n = (n0 > 0 ? n0 - 1 : 0) + lane; n < n1; n += 64) {
     const int64_t s = axis_start(ax, n), e = axis_start(ax, n + 1);
     if (e <= s) continue;
-    if (s >= t0 && s < t1) {
-      m.S[s - t0] = (int)n;
-      any = true;
-    }
-    if (e > t0 && e <= t1) {
-      m.E[e - 1 - t0] = (int)n;
-      any = true;
-    }
+    if (s >= t0 && s < t1) m.S[s - t0] = (int)n;
+    if (e > t0 && e <= t1) m.E[e - 1 - t0] = (int)n;
   }
-  any = __any(any);
-  if (lane == 0) m.any = any;
 }
 
 // Loads and stores of a tile by 32-bit offsets from its first row.  The
@@ -174,11 +179,14 @@ struct Rows {
 };
 
 // Device-scope words that other workgroups write while this kernel runs, all by
-// relaxed atomics, which go to where the XCDs agree.  What leaves a tile is one
-// 64-bit word a channel, the value with KNOWN above it, so that the next tile's
-// poll brings flag and value in one round trip.  Maps fill their words: they
-// are stored, waited for, then flagged.
+// relaxed atomics, which go to where the XCDs agree.  A word carries its value
+// and the sign that it is there, so nothing has to be ordered: what leaves a
+// tile has KNOWN above it, and a map has KNOWN_MAP in the sign of its A, a
+// product of exponentials, which has none of its own.  A round trip takes
+// microseconds under load, so none is spent on waiting for a store and then
+// flagging it.
 constexpr uint64_t KNOWN = (uint64_t)1 << 32;
+constexpr uint32_t KNOWN_MAP = 0x80000000u;
 template <typename W>
 __device__ __forceinline__ W peek(const W* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -187,50 +195,68 @@ template <typename W>
 __device__ __forceinline__ void post(W* p, W v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void flag_after(int* flag, int value) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  if ((threadIdx.x & 63) == 0) post(flag, value);
-}
 
-// Polls before a wait gives up (about a second: each is a round trip to memory).
-constexpr int kPolls = 1 << 20;
+// Rounds before a wait gives up (about a second: each is a round trip to memory).
+constexpr int kPolls = 1 << 19;
 
-// What enters tile k (tiles counted in the pass's order) at channel c.  `word`
-// is a first look at the word that holds it; where that is not there yet, the
-// tile's own map is published for the tiles behind, and the flags of the 64
-// tiles before are searched for the nearest one whose leaving value is known.
-__device__ __forceinline__ float look_back(const GlrArgs& a, int* flags, int k, int64_t c, bool in, uint64_t word,
-                                           bool publish, float At, float Bt) {
-  if (__all(!in || (word & KNOWN))) return __uint_as_float((uint32_t)word);
-  if (publish) {
-    if (in) post(a.maps + (int64_t)k * a.C + c, (uint64_t)__float_as_uint(Bt) << 32 | __float_as_uint(At));
-    flag_after(flags + k, 1);
-  }
-  const int lane = threadIdx.x & 63;
+// What enters tile k (tiles counted in the pass's order) at channel c: its own
+// word, or the word of a tile up to REACH before it with the maps in between
+// applied, in order.  `word` is a first look at its own.  Where that is not
+// there yet, the maps of the tiles before are collected in LDS, the nearest
+// first and a batch a round, and every round looks at the words of several
+// distances at once, so that a value that arrives anywhere in reach is taken up
+// in one round trip.
+constexpr int REACH = 32, BATCH = 8;
+typedef uint64_t Maps[REACH][GC];
+// Of a row of words (a wave-uniform address) the one of channel c.
+__device__ __forceinline__ uint64_t peek_row(const uint64_t* row, uint32_t c) { return peek(row + c); }
+__device__ __forceinline__ float look_back(const GlrArgs& a, Maps& maps, int k, int64_t c, bool in, uint64_t word) {
+  constexpr int ND = 7;
+  if (__all((word & KNOWN) != 0)) return __uint_as_float((uint32_t)word);
+  const int ch = threadIdx.x & 63;
+  const uint32_t at = in ? (uint32_t)c : 0;
+  const int before = k < REACH ? k : REACH;  // tiles in reach
+  const uint64_t* enter = a.enter + (int64_t)k * a.C;
+  uint32_t have = 0;  // maps that are there, in all channels: bit u, of tile k - 1 - u
   for (int poll = 0; poll < kPolls; ++poll) {
-    const int q = k - 1 - lane;
-    const int f = q >= 0 ? peek(flags + q) : 0;
-    word = in ? peek(a.enter + (int64_t)k * a.C + c) : KNOWN;
-    if (__all(word & KNOWN)) return __uint_as_float((uint32_t)word);
-    const uint64_t known = __ballot(f == 2), mapped = __ballot(f >= 1);
-    if (!known) continue;
-    const int p = __builtin_ctzll(known);
-    const uint64_t between = ((uint64_t)1 << p) - 1;
-    if ((mapped & between) != between) continue;
-    // tiles k - p .. k - 1 lie between; their maps are loaded 32 at a time, in one round trip
-    constexpr int U = 32;
-    float s = in ? __uint_as_float((uint32_t)peek(a.enter + (int64_t)(k - p) * a.C + c)) : 0.f;
-    for (int j = k - p; j < k; j += U) {
-      uint64_t m[U];
+    // one round trip: the words, and the nearest BATCH maps that are not all there yet
+    const int u0 = have == ~0u ? REACH : __builtin_ctz(~have) & -BATCH;
+    const int reach = u0 + BATCH < before ? u0 + BATCH : before;
+    uint64_t w[ND], m[BATCH];  // entering words at distances 0, 1, 2, 4, 8, 16, 32
 #pragma unroll
-      for (int u = 0; u < U; ++u) m[u] = in && j + u < k ? peek(a.maps + (int64_t)(j + u) * a.C + c) : 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + u < k) s = __uint_as_float((uint32_t)m[u]) * s + __uint_as_float((uint32_t)(m[u] >> 32));
+    for (int i = 0; i < ND; ++i) {
+      const int d = i == 0 ? 0 : 1 << (i - 1);
+      w[i] = d <= reach ? peek_row(enter - d * a.C, at) : 0;
     }
-    return s;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) m[u] = u0 + u < reach ? peek_row(a.maps + (int64_t)(k - 1 - u0 - u) * a.C, at) : 0;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u)
+      if (u0 + u < reach) {
+        maps[u0 + u][ch] = m[u];
+        if (__all(!in || (m[u] & KNOWN_MAP) != 0)) have |= 1u << (u0 + u);
+      }
+    float s = 0.f;
+    int found = -1;
+#pragma unroll
+    for (int i = ND - 1; i >= 0; --i) {
+      const int d = i == 0 ? 0 : 1 << (i - 1);
+      const uint32_t need = d == 32 ? ~0u : (1u << (d & 31)) - 1;
+      if (d <= reach && (have & need) == need && __all(!in || (w[i] & KNOWN) != 0)) {
+        s = __uint_as_float((uint32_t)w[i]);
+        found = d;
+      }
+    }
+    if (found >= 0) {
+#pragma unroll 4
+      for (int u = found - 1; u >= 0; --u) {
+        const uint64_t m = maps[u][ch];
+        s = __uint_as_float((uint32_t)m & ~KNOWN_MAP) * s + __uint_as_float((uint32_t)(m >> 32));
+      }
+      return s;
+    }
   }
-  if (lane == 0) atomicOr(a.faults, FAULT_WAIT_TIMEOUT);
+  if (ch == 0) atomicOr(a.faults, FAULT_WAIT_TIMEOUT);
   return 0.f;
 }
 
@@ -243,62 +269,91 @@ struct Tile {
 // the wave that holds no data: finds what enters the tile (not where the tile
 // begins `fresh`, with a sequence's first row), hands on what leaves it, and
 // puts what enters every run into t.A.
-template <bool REV>
-__device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, int k, int blk, bool fresh) {
+template <bool REV, bool MARKED>
+__device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps, int k, int blk, bool fresh) {
   const int ch = threadIdx.x & 63;
   const int64_t c = (int64_t)blk * GC + ch;
   const bool in = c < a.C;
   const bool ask = k > 0 && !fresh, last = k + 1 == a.ntiles;
   const uint64_t word = ask && in ? peek(a.enter + (int64_t)k * a.C + c) : KNOWN;
   float At = 1.f, Bt = 0.f;
-  bool resets = false;
+  uint32_t resets = 0;  // runs that hold a sequence's first row (REV: last row)
+  if (MARKED) resets = (uint32_t)__ballot(ch < GS && t.reset[ch < GS ? ch : 0]);
+  {
+    float A[GS], B[GS];
 #pragma unroll
-  for (int i = 0; i < GS; ++i) {
-    const int run = REV ? GS - 1 - i : i;
-    const float Ai = t.A[run][ch], Bi = t.B[run][ch];
-    const bool ri = t.reset[run];
-    resets |= ri;
-    Bt = ri ? Bi : Ai * Bt + Bi;
-    At *= Ai;
-  }
-  int* flags = a.flags + (int64_t)blk * a.ntiles;
-  uint64_t* to = a.enter + (int64_t)(k + 1) * a.C + c;
-  float s = 0.f, leave = Bt;
-  if (resets) {  // what leaves does not depend on what enters
-    if (!last) {
-      if (in) post(to, KNOWN | __float_as_uint(leave));
-      flag_after(flags + k, 2);
+    for (int i = 0; i < GS; ++i) {
+      A[i] = t.A[i][ch];
+      B[i] = t.B[i][ch];
     }
-    if (ask) s = look_back(a, flags, k, c, in, word, false, At, Bt);
-  } else {
-    if (ask) s = look_back(a, flags, k, c, in, word, !last, At, Bt);
-    leave = At * s + Bt;
-    if (!last && in) post(to, KNOWN | __float_as_uint(leave));
+#pragma unroll
+    for (int i = 0; i < GS; ++i) {
+      const int run = REV ? GS - 1 - i : i;
+      Bt = MARKED && (resets >> run & 1) ? B[run] : A[run] * Bt + B[run];
+      At *= A[run];
+    }
   }
+  float s = 0.f, leave = Bt;
+  if (!resets && ask && !last && in)  // for the tiles behind, should they have to wait
+    post(a.maps + (int64_t)k * a.C + c, (uint64_t)__float_as_uint(Bt) << 32 | __float_as_uint(At) | KNOWN_MAP);
+  // what leaves a reset tile does not depend on what enters it: it is handed on first
+  if (!resets) {
+    if (ask) s = look_back(a, maps, k, c, in, word);
+    leave = At * s + Bt;
+  }
+  if (!last && in) post(a.enter + (int64_t)(k + 1) * a.C + c, KNOWN | __float_as_uint(leave));
+  if (resets && ask) s = look_back(a, maps, k, c, in, word);
   if (a.keep && in && !last) a.keep[(int64_t)(k + 1) * a.C + c] = leave;
+  float A[GS], B[GS];
+#pragma unroll
+  for (int i = 0; i < GS; ++i) {
+    A[i] = t.A[i][ch];
+    B[i] = t.B[i][ch];
+  }
 #pragma unroll
   for (int i = 0; i < GS; ++i) {
     const int run = REV ? GS - 1 - i : i;
-    const float Ai = t.A[run][ch], Bi = t.B[run][ch];
     t.A[run][ch] = s;
-    s = t.reset[run] ? Bi : Ai * s + Bi;
+    s = MARKED && (resets >> run & 1) ? B[run] : A[run] * s + B[run];
   }
-  if (!last && !resets) flag_after(flags + k, 2);
 }
 
-__device__ __forceinline__ int draw_ticket(const GlrArgs& a) {
-  return __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
+// Tiles are handed out in order by counters.  One counter serves a tile each
+// 13 ns at best (measured: every pass ran at that pace, whatever it computed),
+// less than memory allows, so the columns are split into up to eight sets of
+// neighbours, each with its counter.  A workgroup takes from its own set first,
+// and from the others when that is used up.  Whatever it waits for was drawn
+// before its own ticket, by a workgroup that works on its tickets in the order
+// it drew them: so no two can wait for each other.
+constexpr int SETS = 8;
+constexpr int TICKET_LINE = 64;  // ints: counters on lines of their own
+struct Drawer {
+  int set, left;  // the set drawn from, sets not used up
+  __device__ __forceinline__ Drawer(const GlrArgs& a) : set(blockIdx.x % a.sets), left(a.sets) {}
+  // A ticket is asked for by ask() and turned into a tile's number, tile * nblk
+  // + column block, or INT_MAX, by answer(), later: the round trip lies between.
+  // By one thread.
+  __device__ __forceinline__ int ask(const GlrArgs& a) const {
+    return __hip_atomic_fetch_add(a.tickets + set * TICKET_LINE, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ int answer(const GlrArgs& a, int t) {
+    while (left > 0) {
+      const int first = (int)((int64_t)a.nblk * set / a.sets), n = (int)((int64_t)a.nblk * (set + 1) / a.sets) - first;
+      if (t / n < a.ntiles) return t / n * a.nblk + first + t % n;
+      if (--left == 0) break;
+      set = set + 1 < a.sets ? set + 1 : 0;
+      t = ask(a);
+    }
+    return INT_MAX;
+  }
+};
 
-// Clears the counter, the fault word, the flags and the words that other
-// workgroups wait for (a kernel rather than a memset, so that a captured graph
+// Clears the fault word, the counters and the words that other workgroups wait
+// for (a kernel rather than a memset, so that a captured graph
 // replays it as a kernel node).
-__global__ void __launch_bounds__(256) kda_glr_clear_kernel(int* ticket, unsigned* faults, uint4* words, int64_t n) {
+__global__ void __launch_bounds__(256) kda_glr_clear_kernel(unsigned* faults, uint4* words, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i == 0) {
-    *ticket = 0;
-    *faults = 0;
-  }
+  if (i == 0) *faults = 0;
   for (int64_t j = i; j < n; j += (int64_t)gridDim.x * 256) words[j] = make_uint4(0, 0, 0, 0);
 }
 
@@ -340,29 +395,33 @@ struct Run {
 template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
   __shared__ Tile tiles[2];
+  __shared__ Maps maps;
   __shared__ Marks marks[4];
   __shared__ int slot[4];  // tickets, by turns
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
   const int items = a.ntiles * a.nblk;
   if (tid >= GD) {
+    Drawer drawer(a);
     if (tid == GD)
-      for (int i = 0; i < 3; ++i) slot[i] = draw_ticket(a);
-    __builtin_amdgcn_wave_barrier();
-    for (int i = 0; i < 2; ++i)
-      if (slot[i] < items) mark_tile(a.ax, (int64_t)(slot[i] / a.nblk) * GL, marks[i]);
-    __syncthreads();  // tickets and marks
+      for (int i = 0; i < 3; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
+    int asked = tid == GD ? drawer.ask(a) : 0;
+    // everything else waits for this wave: its instructions go first
+    __builtin_amdgcn_s_setprio(3);
+    __syncthreads();  // tickets
+    __syncthreads();  // marks
     __syncthreads();  // the maps of the first tile
     for (int i = 0;; ++i) {
       const int item = slot[i & 3];
       if (item >= items) break;
-      const int ahead = slot[(i + 2) & 3];
-      int after = 0;
-      if (tid == GD) after = draw_ticket(a);
+      if (tid == GD) {  // the ticket asked for a tile ago
+        slot[(i + 3) & 3] = drawer.answer(a, asked);
+        asked = drawer.ask(a);
+      }
       const Marks& m = marks[i & 3];
-      join_runs<false>(a, tiles[i & 1], item / a.nblk, item % a.nblk, m.any && m.S[0] >= 0);
-      if (ahead < items) mark_tile(a.ax, (int64_t)(ahead / a.nblk) * GL, marks[(i + 2) & 3]);
-      if (tid == GD) slot[(i + 3) & 3] = after;
+      const int k = item / a.nblk, blk = item % a.nblk;
+      if (m.any) join_runs<false, true>(a, tiles[i & 1], maps, k, blk, m.S[0] >= 0);
+      else join_runs<false, false>(a, tiles[i & 1], maps, k, blk, false);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
     }
   } else {
@@ -442,17 +501,25 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
         }
       }
     };
-    __syncthreads();  // tickets and marks
+    // the marks of tile i, by the first wave, before anybody needs them
+    auto mark = [&](int item, int i) {
+      if (tid < 64 && item < items) mark_tile(a.ax, (int64_t)(item / a.nblk) * GL, marks[i & 3]);
+    };
+    __syncthreads();  // tickets
     int item = slot[0], next = slot[1];
     Run<T, GIVEN, COMPL> now, then;
+    mark(item, 0);
+    mark(next, 1);
+    if (item < items) fetch(item);
+    __syncthreads();  // marks
     if (item < items) {
-      fetch(item);
       map(item, 0, now);
       if (next < items) fetch(next);
     }
     __syncthreads();  // the maps of the first tile
     for (int i = 0; item < items; ++i) {
       const int ahead = slot[(i + 2) & 3];
+      mark(ahead, i + 2);
       if (next < items) {
         map(next, i + 1, then);
         if (ahead < items) fetch(ahead);
@@ -476,14 +543,16 @@ template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
   __shared__ Tile t;   // of e, from the right
   __shared__ Tile ft;  // of h
+  __shared__ Maps maps;
   __shared__ Marks m;
   __shared__ int slot;
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
   const int items = a.ntiles * a.nblk;
   const int row_bytes = (int)(a.C * sizeof(T));
+  Drawer drawer(a);
   for (;;) {
-    if (tid == GD) slot = draw_ticket(a);
+    if (tid == GD) slot = drawer.answer(a, drawer.ask(a));
     __syncthreads();
     const int item = slot;
     if (item >= items) break;
@@ -494,6 +563,7 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
       const int ch = tid - GD;
       const int64_t cc = (int64_t)blk * GC + ch;
       float s = cc < a.C ? a.states[(int64_t)tile * a.C + cc] : 0.f;
+      __builtin_amdgcn_s_setprio(3);
       mark_tile(a.ax, t0, m);
       __syncthreads();  // the marks
       __syncthreads();  // the runs' maps
@@ -503,7 +573,8 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
         ft.A[i][ch] = s;
         s = ft.reset[i] ? Bi : Ai * s + Bi;
       }
-      join_runs<true>(a, t, k, blk, m.any && m.E[GL - 1] >= 0);
+      if (m.any) join_runs<true, true>(a, t, maps, k, blk, m.E[GL - 1] >= 0);
+      else join_runs<true, false>(a, t, maps, k, blk, false);
       __syncthreads();  // what enters them
       if constexpr (!GIVEN) {
         __syncthreads();  // the runs' sums
@@ -735,18 +806,17 @@ __global__ void __launch_bounds__(GST) kda_glr_step_kernel(GlrArgs a) {
   if (a.fin) store4(a.fin + i, h);
 }
 
-// The counter and the fault word (where kda_workspace_faults looks for it) come
-// first, then what is cleared: the flags and the words of what enters a tile.
+// The fault word comes where kda_workspace_faults looks for it, then what is
+// cleared: the counters and the words that tiles hand each other.
 struct GlrLayout {
-  size_t ticket, faults, flags, enter, maps, part, total;
+  size_t faults, tickets, enter, maps, part, total;
 };
 GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
   const size_t tiles = (size_t)((T_total + GL - 1) / GL), w = tiles * (size_t)C;
   GlrLayout l;
-  l.ticket = 0;
   l.faults = 4;
-  l.flags = 256;
-  l.enter = l.flags + align256(tiles * (size_t)((C + GC - 1) / GC) * sizeof(int));
+  l.tickets = 256;
+  l.enter = l.tickets + SETS * TICKET_LINE * sizeof(int);
   l.maps = l.enter + align256(w * sizeof(uint64_t));
   l.part = l.maps + align256(w * sizeof(uint64_t));
   l.total = l.part + (bwd ? align256(w * sizeof(float2)) : 0);
@@ -772,16 +842,17 @@ kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, f
   if (cu_seqlens && T > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   if (!(flags & FLAG_GATE_GIVEN) && !aligned(dt_bias, 16)) return KDA_ERR_INVALID;
   const int64_t tiles = (B * T + GL - 1) / GL, nblk = (H * K + GC - 1) / GC;
-  if (!fits(tiles, nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // the counter and the flags are 32-bit
+  if (!fits(tiles, nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // tile numbers are 32-bit
   a = GlrArgs{};
   a.A_log = A_log;
   a.dt_bias = dt_bias;
-  a.ax = Axis{cu_seqlens, T, B * T, (int)N};
+  a.ax = make_axis(cu_seqlens, T, B * T, N);
   a.C = H * K;
   a.H = (int)H;
   a.K = (int)K;
   a.nblk = (int)nblk;
   a.ntiles = (int)tiles;
+  a.sets = nblk < SETS ? (int)nblk : SETS;
   a.lb = lower_bound;
   a.zero_rest = flags & FLAG_ZERO_REST ? 1 : 0;
   return KDA_SUCCESS;
@@ -803,10 +874,10 @@ int64_t pass_grid(const GlrArgs& a) {
   return items < 1 ? 1 : items < most ? items : most;
 }
 kda_status_t clear(const GlrArgs& a, hipStream_t st) {
-  const int64_t n = (reinterpret_cast<char*>(a.maps) - reinterpret_cast<char*>(a.flags)) / sizeof(uint4);
+  const int64_t n = (reinterpret_cast<char*>(a.maps + (int64_t)a.ntiles * a.C) - reinterpret_cast<char*>(a.tickets)) / sizeof(uint4);
   const int64_t blocks = (n + 255) / 256, most = 2048;
-  return launch(&kda_glr_clear_kernel, blocks < 1 ? 1 : blocks < most ? blocks : most, 256, st, "glr clear", a.ticket,
-                a.faults, reinterpret_cast<uint4*>(a.flags), n);
+  return launch(&kda_glr_clear_kernel, blocks < 1 ? 1 : blocks < most ? blocks : most, 256, st, "glr clear",
+                a.faults, reinterpret_cast<uint4*>(a.tickets), n);
 }
 template <typename T, bool GIVEN, bool COMPL>
 struct RunFwd {
@@ -832,9 +903,8 @@ struct RunStep {
 };
 
 void carve(GlrArgs& a, char* ws, const GlrLayout& l) {
-  a.ticket = reinterpret_cast<int*>(ws + l.ticket);
+  a.tickets = reinterpret_cast<int*>(ws + l.tickets);
   a.faults = reinterpret_cast<unsigned*>(ws + l.faults);
-  a.flags = reinterpret_cast<int*>(ws + l.flags);
   a.enter = reinterpret_cast<uint64_t*>(ws + l.enter);
   a.maps = reinterpret_cast<uint64_t*>(ws + l.maps);
 }

@@ -116,7 +116,19 @@ struct Axis {
   int64_t T;
   int64_t total;
   int N;
+  double per_row;  // 1 / T (0 for T == 0)
 };
+inline Axis make_axis(const int32_t* cu, int64_t T, int64_t total, int64_t N) {
+  return Axis{cu, T, total, (int)N, T > 0 ? 1.0 / (double)T : 0.0};
+}
+// t / T for 0 <= t <= total (cu NULL): from the quotient in fp64, which is off
+// by one at most, instead of a 64-bit integer division.
+__device__ __forceinline__ int64_t axis_div(const Axis& ax, int64_t t) {
+  int64_t n = (int64_t)((double)t * ax.per_row);
+  n -= n * ax.T > t;
+  n += (n + 1) * ax.T <= t;
+  return n;
+}
 // Rows that belong to sequences.  Held to the array, and the first offset to 0,
 // so that offsets that break the contract cannot lead outside the arrays.
 __device__ __forceinline__ int64_t axis_rows(const Axis& ax) {
@@ -134,7 +146,7 @@ __device__ __forceinline__ int64_t axis_lower(const Axis& ax, int64_t t) {
   if (!ax.cu) {
     if (t <= 0) return 0;
     if (ax.T == 0) return (int64_t)ax.N + 1;
-    const int64_t n = (t + ax.T - 1) / ax.T;
+    const int64_t n = axis_div(ax, t - 1) + 1;
     return n <= ax.N ? n : (int64_t)ax.N + 1;
   }
   const int lane = threadIdx.x & 63;
@@ -155,7 +167,7 @@ __device__ __forceinline__ int64_t axis_lower(const Axis& ax, int64_t t) {
 // The sequence that row t (< axis_rows) belongs to: the largest n with
 // start(n) <= t, which is not empty.  Any lane, any t.
 __device__ __forceinline__ int axis_owner(const Axis& ax, int64_t t) {
-  if (!ax.cu) return (int)(t / ax.T);
+  if (!ax.cu) return (int)axis_div(ax, t);
   int lo = 0, hi = ax.N - 1;
   while (lo < hi) {
     const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
