@@ -39,14 +39,21 @@
 namespace kda {
 namespace {
 
-constexpr int GR = 4;            // rows of a run
 constexpr int GS = 28;           // runs of a tile
-constexpr int GL = GR * GS;      // rows of a tile
 constexpr int GC = 64;           // channels of a tile
 constexpr int GW = GC / 4;       // lanes of a row
 constexpr int GD = GS * GW;      // threads that hold data: seven waves
 constexpr int GT = GD + GC;      // and one, a lane a channel, that finds what enters the tile
 static_assert(GD % 64 == 0 && GT == 512 && GS <= 32, "whole waves, runs in a 32-bit mask");
+// Rows of a run and of a tile: as many as the registers of one workgroup a CU
+// hold (8 of bf16, 4 of fp32: 224 and 112 rows).  More rows a tile mean fewer
+// tiles in flight on a column, and so less waiting, for the same bytes.
+template <typename T>
+constexpr int GR = sizeof(T) == 2 ? 8 : 4;
+template <typename T>
+constexpr int GL = GR<T> * GS;
+constexpr int GL_MAX = GS * 8;
+inline int tile_rows(int dtype) { return dtype == KDA_DTYPE_BF16 ? GL<__bf16> : GL<float>; }
 constexpr int64_t kMaxChannels = (int64_t)1 << 21;  // a tile's rows span less than 2^30 bytes
 
 struct GlrArgs {
@@ -116,11 +123,11 @@ __device__ __forceinline__ float one_minus(float g2, float a) {
 // The sequences that start (S) or end (E) at each row of the tile at t0, -1 for
 // none, and whether there is any; by one wave.
 struct Marks {
-  int S[GL], E[GL], any;
+  int S[GL_MAX], E[GL_MAX], any;
 };
-__device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, Marks& m) {
+__device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_len, Marks& m) {
   const int lane = threadIdx.x & 63;
-  const int64_t t1 = t0 + GL;
+  const int64_t t1 = t0 + tile_len;
   // n0, n1: first sequences that start at t0, t1 or behind
   const int64_t n0 = axis_lower(ax, t0);
   int64_t n1 = n0;
@@ -135,7 +142,7 @@ __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, Marks& m) 
   const bool any = n1 > n0 || (n0 <= ax.N && axis_start(ax, n0) == t1);
   if (lane == 0) m.any = any;
   if (!any) return;
-  for (int i = lane; i < GL; i += 64) m.S[i] = m.E[i] = -1;
+  for (int i = lane; i < tile_len; i += 64) m.S[i] = m.E[i] = -1;
   n1 = n1 < ax.N ? n1 : ax.N;
   __builtin_amdgcn_wave_barrier();
   // sequence n0 - 1 is the one that reaches the tile from before it
@@ -155,7 +162,7 @@ template <typename T>
 struct Rows {
   __amdgpu_buffer_rsrc_t r;
   __device__ __forceinline__ Rows(const void* base, int64_t t0, int64_t rows, int64_t C) {
-    const int64_t left = rows - t0 < GL ? rows - t0 : GL;
+    const int64_t left = rows - t0 < GL<T> ? rows - t0 : GL<T>;
     r = buf(static_cast<const T*>(base) + t0 * C, (uint32_t)((left > 0 ? left : 0) * C * sizeof(T)));
   }
   __device__ __forceinline__ raw4<T> load(int voff, int soff) const {
@@ -279,19 +286,17 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps,
   float At = 1.f, Bt = 0.f;
   uint32_t resets = 0;  // runs that hold a sequence's first row (REV: last row)
   if (MARKED) resets = (uint32_t)__ballot(ch < GS && t.reset[ch < GS ? ch : 0]);
-  {
-    float A[GS], B[GS];
+  float A[GS], B[GS];
 #pragma unroll
-    for (int i = 0; i < GS; ++i) {
-      A[i] = t.A[i][ch];
-      B[i] = t.B[i][ch];
-    }
+  for (int i = 0; i < GS; ++i) {
+    A[i] = t.A[i][ch];
+    B[i] = t.B[i][ch];
+  }
 #pragma unroll
-    for (int i = 0; i < GS; ++i) {
-      const int run = REV ? GS - 1 - i : i;
-      Bt = MARKED && (resets >> run & 1) ? B[run] : A[run] * Bt + B[run];
-      At *= A[run];
-    }
+  for (int i = 0; i < GS; ++i) {
+    const int run = REV ? GS - 1 - i : i;
+    Bt = MARKED && (resets >> run & 1) ? B[run] : A[run] * Bt + B[run];
+    At *= A[run];
   }
   float s = 0.f, leave = Bt;
   if (!resets && ask && !last && in)  // for the tiles behind, should they have to wait
@@ -304,12 +309,6 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps,
   if (!last && in) post(a.enter + (int64_t)(k + 1) * a.C + c, KNOWN | __float_as_uint(leave));
   if (resets && ask) s = look_back(a, maps, k, c, in, word);
   if (a.keep && in && !last) a.keep[(int64_t)(k + 1) * a.C + c] = leave;
-  float A[GS], B[GS];
-#pragma unroll
-  for (int i = 0; i < GS; ++i) {
-    A[i] = t.A[i][ch];
-    B[i] = t.B[i][ch];
-  }
 #pragma unroll
   for (int i = 0; i < GS; ++i) {
     const int run = REV ? GS - 1 - i : i;
@@ -364,24 +363,14 @@ __device__ __forceinline__ void state4(const float* p, int n, int64_t C, int64_t
   if (p && in) load_f4(p + (int64_t)n * C + c, s);
 }
 
-// One run of 4 rows by 4 channels, in one thread: decays and inputs.
-template <typename T, bool GIVEN, bool COMPL>
+// One run in one thread: decays and inputs.
+template <typename T>
 struct Run {
-  float a[GR][4], u[GR][4];
-  __device__ __forceinline__ void make(const Gate<GIVEN>& gate, const raw4<T> (&xr)[GR], const raw4<T> (&gr)[GR]) {
-#pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      float xv[4], gv[4];
-      widen4(xr[i], xv);
-      widen4(gr[i], gv);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float g2 = gate.g2(gv[j], j);
-        a[i][j] = fexp2(g2);
-        u[i][j] = COMPL ? one_minus(g2, a[i][j]) * xv[j] : xv[j];
-      }
-    }
-  }
+  float a[GR<T>][4], u[GR<T>][4];
+};
+template <typename T>
+struct Raw {
+  raw4<T> x[GR<T>], g[GR<T>];
 };
 
 // Seven waves hold the data and one finds what enters the tiles, so that rows
@@ -389,35 +378,33 @@ struct Run {
 // a wave that had asked for rows could not see a word before they arrive).
 // They run a tile apart, with one barrier a tile: while the one joins tile i,
 // the seven write the outputs of tile i - 1, form the maps of tile i + 1 from
-// rows that have arrived, and ask for the rows of tile i + 2.  A workgroup
-// holds the tickets of those tiles and works on them in order, so the lowest
-// unfinished ticket is always being worked on.
+// rows that have arrived, and ask for the rows of tile i + 3.  A workgroup
+// holds the tickets of those tiles and works on them in order.
 template <typename T, bool GIVEN, bool COMPL>
-__global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
+__global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
+  constexpr int R = GR<T>, L = GL<T>;
   __shared__ Tile tiles[2];
   __shared__ Maps maps;
   __shared__ Marks marks[4];
-  __shared__ int slot[4];  // tickets, by turns
+  __shared__ int slot[8];  // tickets, by turns
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
   const int items = a.ntiles * a.nblk;
+  Drawer drawer(a);
+  int asked = 0;
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
+    asked = drawer.ask(a);
+  }
+  __syncthreads();  // tickets
   if (tid >= GD) {
-    Drawer drawer(a);
-    if (tid == GD)
-      for (int i = 0; i < 3; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
-    int asked = tid == GD ? drawer.ask(a) : 0;
     // everything else waits for this wave: its instructions go first
     __builtin_amdgcn_s_setprio(3);
-    __syncthreads();  // tickets
     __syncthreads();  // marks
     __syncthreads();  // the maps of the first tile
     for (int i = 0;; ++i) {
-      const int item = slot[i & 3];
+      const int item = slot[i & 7];
       if (item >= items) break;
-      if (tid == GD) {  // the ticket asked for a tile ago
-        slot[(i + 3) & 3] = drawer.answer(a, asked);
-        asked = drawer.ask(a);
-      }
       const Marks& m = marks[i & 3];
       const int k = item / a.nblk, blk = item % a.nblk;
       if (m.any) join_runs<false, true>(a, tiles[i & 1], maps, k, blk, m.S[0] >= 0);
@@ -426,30 +413,46 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
     }
   } else {
     const int row_bytes = (int)(a.C * sizeof(T));
-    raw4<T> xr[GR], gr[GR];
     auto place = [&](int item, int64_t& t0, int64_t& c) {
-      t0 = (int64_t)(item / a.nblk) * GL;
+      t0 = (int64_t)(item / a.nblk) * L;
       c = (int64_t)(item % a.nblk) * GC + lane * 4;
-      return c < a.C ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+      return c < a.C ? run * R * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
     };
-    auto fetch = [&](int item) {
+    auto fetch = [&](int item, Raw<T>& w) {
+      if (item >= items) return;
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C);
 #pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        gr[i] = gs.load(voff, i * row_bytes);
-        xr[i] = xs.load(voff, i * row_bytes);
+      for (int i = 0; i < R; ++i) {
+        w.g[i] = gs.load(voff, i * row_bytes);
+        w.x[i] = xs.load(voff, i * row_bytes);
       }
     };
+    // the marks of tile i, by the first wave, before anybody needs them
+    auto mark = [&](int item, int i) {
+      if (tid < 64 && item < items) mark_tile(a.ax, (int64_t)(item / a.nblk) * L, L, marks[i & 3]);
+    };
     // the maps of tile i, from rows that were asked for
-    auto map = [&](int item, int i, Run<T, GIVEN, COMPL>& r) {
+    auto map = [&](int item, int i, const Raw<T>& w, Run<T>& r) {
+      if (item >= items) return;
       int64_t t0, c;
       place(item, t0, c);
       const bool in = c < a.C;
       Gate<GIVEN> gate;
       gate.init(a, in ? c : 0);
-      r.make(gate, xr, gr);
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        float xv[4], gv[4];
+        widen4(w.x[q], xv);
+        widen4(w.g[q], gv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float g2 = gate.g2(gv[j], j);
+          r.a[q][j] = fexp2(g2);
+          r.u[q][j] = COMPL ? one_minus(g2, r.a[q][j]) * xv[j] : xv[j];
+        }
+      }
       const Marks& m = marks[i & 3];
       Tile& t = tiles[i & 1];
       float A[4], B[4];
@@ -461,10 +464,10 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
       }
       const bool marked = m.any;
 #pragma unroll
-      for (int q = 0; q < GR; ++q) {
-        if (marked && m.S[run * GR + q] >= 0) {
+      for (int q = 0; q < R; ++q) {
+        if (marked && m.S[run * R + q] >= 0) {
           reset = true;
-          state4(a.init, m.S[run * GR + q], a.C, c, in, B);
+          state4(a.init, m.S[run * R + q], a.C, c, in, B);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
       if (lane == 0) t.reset[run] = reset;
     };
     // the outputs of tile i
-    auto finish = [&](int item, int i, const Run<T, GIVEN, COMPL>& r) {
+    auto finish = [&](int item, int i, const Run<T>& r) {
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const bool in = c < a.C;
@@ -487,49 +490,46 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
       load_f4(&tiles[i & 1].A[run][lane * 4], h);
       const Rows<T> os(a.out, t0, rows, a.C);
 #pragma unroll
-      for (int q = 0; q < GR; ++q) {
-        if (marked && m.S[run * GR + q] >= 0) state4(a.init, m.S[run * GR + q], a.C, c, in, h);
+      for (int q = 0; q < R; ++q) {
+        if (marked && m.S[run * R + q] >= 0) state4(a.init, m.S[run * R + q], a.C, c, in, h);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[j] = r.a[q][j] * h[j] + r.u[q][j];
         os.store(voff, q * row_bytes, h);
-        if (marked && a.fin && in && m.E[run * GR + q] >= 0) store4(a.fin + (int64_t)m.E[run * GR + q] * a.C + c, h);
+        if (marked && a.fin && in && m.E[run * R + q] >= 0) store4(a.fin + (int64_t)m.E[run * R + q] * a.C + c, h);
       }
-      if (a.zero_rest && t0 + GL > rows && in) {
-        for (int q = 0; q < GR; ++q) {
-          const int64_t t = t0 + run * GR + q;
+      if (a.zero_rest && t0 + L > rows && in) {
+        for (int q = 0; q < R; ++q) {
+          const int64_t t = t0 + run * R + q;
           if (t >= rows && t < a.ax.total) store_zero4(static_cast<T*>(a.out) + t * a.C + c);
         }
       }
     };
-    // the marks of tile i, by the first wave, before anybody needs them
-    auto mark = [&](int item, int i) {
-      if (tid < 64 && item < items) mark_tile(a.ax, (int64_t)(item / a.nblk) * GL, marks[i & 3]);
-    };
-    __syncthreads();  // tickets
-    int item = slot[0], next = slot[1];
-    Run<T, GIVEN, COMPL> now, then;
-    mark(item, 0);
-    mark(next, 1);
-    if (item < items) fetch(item);
-    __syncthreads();  // marks
-    if (item < items) {
-      map(item, 0, now);
-      if (next < items) fetch(next);
-    }
-    __syncthreads();  // the maps of the first tile
-    for (int i = 0; item < items; ++i) {
-      const int ahead = slot[(i + 2) & 3];
-      mark(ahead, i + 2);
-      if (next < items) {
-        map(next, i + 1, then);
-        if (ahead < items) fetch(ahead);
+    Run<T> r0, r1;
+    Raw<T> w0, w1;
+    // tile i: its run `now` is ready; tile i + 1 is made from `w`, which then takes tile i + 3
+    auto turn = [&](int i, Run<T>& now, Run<T>& then, Raw<T>& w) {
+      const int item = slot[i & 7];
+      if (item >= items) return false;
+      mark(slot[(i + 2) & 7], i + 2);
+      map(slot[(i + 1) & 7], i + 1, w, then);
+      if (tid == 0) {  // the ticket that was asked for a tile ago
+        slot[(i + 4) & 7] = drawer.answer(a, asked);
+        asked = drawer.ask(a);
       }
+      fetch(slot[(i + 3) & 7], w);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
       finish(item, i, now);
-      now = then;
-      item = next;
-      next = ahead;
-    }
+      return true;
+    };
+    mark(slot[0], 0);
+    mark(slot[1], 1);
+    fetch(slot[0], w0);
+    fetch(slot[1], w1);
+    __syncthreads();  // marks
+    map(slot[0], 0, w0, r0);
+    fetch(slot[2], w0);
+    __syncthreads();  // the maps of the first tile
+    for (int i = 0; turn(i, r0, r1, w1) && turn(i + 1, r1, r0, w0); i += 2) {}
   }
   if (a.fin) {  // empty sequences hand their state on
     for (int64_t n = blockIdx.x; n < a.ax.N; n += gridDim.x) {
@@ -539,115 +539,121 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_fwd_kernel(GlrArgs a) {
   }
 }
 
+// The backward's run keeps its rows as loaded: they are needed again.
+template <typename T>
+struct Kept {
+  float a[GR<T>][4];
+  raw4<T> x[GR<T>], g[GR<T>], d[GR<T>];
+};
+
+// As the forward, from the right, with a second set of maps for h, whose
+// entering states are given: the wave that joins does both.
 template <typename T, bool GIVEN, bool COMPL>
-__global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
-  __shared__ Tile t;   // of e, from the right
-  __shared__ Tile ft;  // of h
+__global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
+  constexpr int R = GR<T>, L = GL<T>;
+  __shared__ Tile et[2], ht[2];  // maps of e, from the right, and of h
+  __shared__ float dsums[GIVEN ? 1 : 2][GS][GC], zsums[GIVEN ? 1 : 2][GS][GC];
   __shared__ Maps maps;
-  __shared__ Marks m;
-  __shared__ int slot;
+  __shared__ Marks marks[4];
+  __shared__ int slot[8];
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
   const int items = a.ntiles * a.nblk;
-  const int row_bytes = (int)(a.C * sizeof(T));
   Drawer drawer(a);
-  for (;;) {
-    if (tid == GD) slot = drawer.answer(a, drawer.ask(a));
-    __syncthreads();
-    const int item = slot;
-    if (item >= items) break;
-    const int k = item / a.nblk, blk = item % a.nblk;
-    const int tile = a.ntiles - 1 - k;
-    const int64_t t0 = (int64_t)tile * GL;
-    if (tid >= GD) {
-      const int ch = tid - GD;
-      const int64_t cc = (int64_t)blk * GC + ch;
-      float s = cc < a.C ? a.states[(int64_t)tile * a.C + cc] : 0.f;
-      __builtin_amdgcn_s_setprio(3);
-      mark_tile(a.ax, t0, m);
-      __syncthreads();  // the marks
-      __syncthreads();  // the runs' maps
+  int asked = 0;
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
+    asked = drawer.ask(a);
+  }
+  __syncthreads();  // tickets
+  if (tid >= GD) {
+    __builtin_amdgcn_s_setprio(3);
+    const int ch = tid - GD;
+    auto state_of = [&](int item) {  // h entering the tile
+      const int64_t c = (int64_t)(item % a.nblk) * GC + ch;
+      return item < items && c < a.C ? a.states[(int64_t)(a.ntiles - 1 - item / a.nblk) * a.C + c] : 0.f;
+    };
+    // d_raw and dz z over the tile, from the runs' sums of tile i, a tile behind
+    auto add_up = [&](int item, int i) {
+      const int64_t c = (int64_t)(item % a.nblk) * GC + ch;
+      if (c >= a.C) return;
+      float d = 0.f, z = 0.f;
 #pragma unroll
-      for (int i = 0; i < GS; ++i) {
-        const float Ai = ft.A[i][ch], Bi = ft.B[i][ch];
-        ft.A[i][ch] = s;
-        s = ft.reset[i] ? Bi : Ai * s + Bi;
+      for (int q = 0; q < GS; ++q) {
+        d += dsums[i & (GIVEN ? 0 : 1)][q][ch];
+        z += zsums[i & (GIVEN ? 0 : 1)][q][ch];
       }
-      if (m.any) join_runs<true, true>(a, t, maps, k, blk, m.E[GL - 1] >= 0);
-      else join_runs<true, false>(a, t, maps, k, blk, false);
-      __syncthreads();  // what enters them
-      if constexpr (!GIVEN) {
-        __syncthreads();  // the runs' sums
-        if (cc < a.C) {
-          float d = 0.f, z = 0.f;
+      a.part[(int64_t)(a.ntiles - 1 - item / a.nblk) * a.C + c] = make_float2(d, z);
+    };
+    float s = state_of(slot[0]);
+    int last = -1;
+    __syncthreads();  // marks
+    __syncthreads();  // the maps of the first tile
+    for (int i = 0;; ++i) {
+      const int item = slot[i & 7];
+      if (item >= items) break;
+      const Marks& m = marks[i & 3];
+      const int k = item / a.nblk, blk = item % a.nblk;
+      if (m.any) join_runs<true, true>(a, et[i & 1], maps, k, blk, m.E[L - 1] >= 0);
+      else join_runs<true, false>(a, et[i & 1], maps, k, blk, false);
+      Tile& t = ht[i & 1];
+      const uint32_t resets = m.any ? (uint32_t)__ballot(ch < GS && t.reset[ch < GS ? ch : 0]) : 0;
 #pragma unroll
-          for (int i = 0; i < GS; ++i) {
-            d += ft.B[i][ch];
-            z += ft.A[i][ch];
-          }
-          a.part[(int64_t)tile * a.C + cc] = make_float2(d, z);
+      for (int q0 = 0; q0 < GS; q0 += 14) {
+        float A[14], B[14];
+#pragma unroll
+        for (int q = 0; q < 14; ++q) {
+          A[q] = t.A[q0 + q][ch];
+          B[q] = t.B[q0 + q][ch];
+        }
+#pragma unroll
+        for (int q = 0; q < 14; ++q) {
+          t.A[q0 + q][ch] = s;
+          s = (resets >> (q0 + q) & 1) ? B[q] : A[q] * s + B[q];
         }
       }
-    } else {
-      const int64_t c = (int64_t)blk * GC + lane * 4;
-      const bool in = c < a.C;
-      const int64_t tr = t0 + run * GR;
-      const int voff = in ? run * GR * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+      s = state_of(slot[(i + 1) & 7]);
+      __syncthreads();  // what enters tile i, the maps of tile i + 1
+      if (!GIVEN && i > 0) add_up(slot[(i - 1) & 7], i - 1);
+      last = i;
+    }
+    __syncthreads();  // the sums of the last tile
+    if (!GIVEN && last >= 0) add_up(slot[last & 7], last);
+  } else {
+    const int row_bytes = (int)(a.C * sizeof(T));
+    auto place = [&](int item, int64_t& t0, int64_t& c) {
+      t0 = (int64_t)(a.ntiles - 1 - item / a.nblk) * L;
+      c = (int64_t)(item % a.nblk) * GC + lane * 4;
+      return c < a.C ? run * R * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
+    };
+    auto fetch = [&](int item, Kept<T>& r) {
+      if (item >= items) return;
+      int64_t t0, c;
+      const int voff = place(item, t0, c);
       const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
-      raw4<T> xr[GR], gr[GR], dr[GR];
 #pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        gr[i] = gs.load(voff, i * row_bytes);
-        dr[i] = ds.load(voff, i * row_bytes);
-        xr[i] = xs.load(voff, i * row_bytes);
+      for (int i = 0; i < R; ++i) {
+        r.g[i] = gs.load(voff, i * row_bytes);
+        r.d[i] = ds.load(voff, i * row_bytes);
+        r.x[i] = xs.load(voff, i * row_bytes);
       }
+    };
+    auto mark = [&](int item, int i) {
+      if (tid < 64 && item < items)
+        mark_tile(a.ax, (int64_t)(a.ntiles - 1 - item / a.nblk) * L, L, marks[i & 3]);
+    };
+    auto map = [&](int item, int i, Kept<T>& r) {
+      if (item >= items) return;
+      int64_t t0, c;
+      place(item, t0, c);
+      const bool in = c < a.C;
+      const int64_t tr = t0 + run * R;
       Gate<GIVEN> gate;
       gate.init(a, in ? c : 0);
-      __syncthreads();  // the marks
+      const Marks& m = marks[i & 3];
       const bool marked = m.any;
-      float av[GR][4], b[GR][4];  // decay, input scale
-#pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        float gv[4];
-        widen4(gr[i], gv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float g2 = gate.g2(gv[j], j);
-          av[i][j] = fexp2(g2);
-          b[i][j] = COMPL ? one_minus(g2, av[i][j]) : 1.0f;
-        }
-      }
-      // the run's map of e; rows behind the last sequence hand nothing on
-      {
-        float P[4], Q[4];
-        bool reset = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          P[j] = 1.f;
-          Q[j] = 0.f;
-        }
-#pragma unroll
-        for (int i = GR - 1; i >= 0; --i) {
-          if (tr + i < rows) {
-            if (marked && m.E[run * GR + i] >= 0) {
-              reset = true;
-              state4(a.d_final, m.E[run * GR + i], a.C, c, in, Q);
-            }
-            float dv[4];
-            widen4(dr[i], dv);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              P[j] *= av[i][j];
-              Q[j] = av[i][j] * (dv[j] + Q[j]);
-            }
-          }
-        }
-        store4(&t.A[run][lane * 4], P);
-        store4(&t.B[run][lane * 4], Q);
-        if (lane == 0) t.reset[run] = reset;
-      }
-      // the run's map of h
-      {
+      {  // of h
+        Tile& t = ht[i & 1];
         float A[4], B[4];
         bool reset = false;
 #pragma unroll
@@ -656,56 +662,96 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
           B[j] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < GR; ++i) {
-          if (marked && m.S[run * GR + i] >= 0) {
+        for (int q = 0; q < R; ++q) {
+          if (marked && m.S[run * R + q] >= 0) {
             reset = true;
-            state4(a.init, m.S[run * GR + i], a.C, c, in, B);
+            state4(a.init, m.S[run * R + q], a.C, c, in, B);
           }
-          float xv[4];
-          widen4(xr[i], xv);
+          float xv[4], gv[4];
+          widen4(r.x[q], xv);
+          widen4(r.g[q], gv);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            A[j] *= av[i][j];
-            B[j] = av[i][j] * B[j] + b[i][j] * xv[j];
+            const float g2 = gate.g2(gv[j], j);
+            r.a[q][j] = fexp2(g2);
+            A[j] *= r.a[q][j];
+            B[j] = r.a[q][j] * B[j] + (COMPL ? one_minus(g2, r.a[q][j]) * xv[j] : xv[j]);
           }
         }
-        store4(&ft.A[run][lane * 4], A);
-        store4(&ft.B[run][lane * 4], B);
-        if (lane == 0) ft.reset[run] = reset;
+        store4(&t.A[run][lane * 4], A);
+        store4(&t.B[run][lane * 4], B);
+        if (lane == 0) t.reset[run] = reset;
       }
-      __syncthreads();  // the runs' maps
-      __syncthreads();  // what enters them
-      float h[4], hp[GR][4];
-      load_f4(&ft.A[run][lane * 4], h);
-#pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        if (marked && m.S[run * GR + i] >= 0) state4(a.init, m.S[run * GR + i], a.C, c, in, h);
-        float xv[4];
-        widen4(xr[i], xv);
+      {  // of e; rows behind the last sequence hand nothing on
+        Tile& t = et[i & 1];
+        float P[4], Q[4];
+        bool reset = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          hp[i][j] = COMPL ? h[j] - xv[j] : h[j];
-          h[j] = av[i][j] * h[j] + b[i][j] * xv[j];
+          P[j] = 1.f;
+          Q[j] = 0.f;
+        }
+#pragma unroll
+        for (int q = R - 1; q >= 0; --q) {
+          if (tr + q < rows) {
+            if (marked && m.E[run * R + q] >= 0) {
+              reset = true;
+              state4(a.d_final, m.E[run * R + q], a.C, c, in, Q);
+            }
+            float dv[4];
+            widen4(r.d[q], dv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              P[j] *= r.a[q][j];
+              Q[j] = r.a[q][j] * (dv[j] + Q[j]);
+            }
+          }
+        }
+        store4(&t.A[run][lane * 4], P);
+        store4(&t.B[run][lane * 4], Q);
+        if (lane == 0) t.reset[run] = reset;
+      }
+    };
+    auto finish = [&](int item, int i, const Kept<T>& r) {
+      int64_t t0, c;
+      const int voff = place(item, t0, c);
+      const bool in = c < a.C;
+      const int64_t tr = t0 + run * R;
+      Gate<GIVEN> gate;
+      gate.init(a, in ? c : 0);
+      const Marks& m = marks[i & 3];
+      const bool marked = m.any;
+      float h[4], e[4], hp[R][4], dsum[4], zsum[4];
+      load_f4(&ht[i & 1].A[run][lane * 4], h);
+      load_f4(&et[i & 1].A[run][lane * 4], e);
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (marked && m.S[run * R + q] >= 0) state4(a.init, m.S[run * R + q], a.C, c, in, h);
+        float xv[4], gv[4];
+        widen4(r.x[q], xv);
+        widen4(r.g[q], gv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hp[q][j] = COMPL ? h[j] - xv[j] : h[j];
+          h[j] = r.a[q][j] * h[j] + (COMPL ? one_minus(gate.g2(gv[j], j), r.a[q][j]) * xv[j] : xv[j]);
         }
       }
-      float e[4], dsum[4], zsum[4];
-      load_f4(&t.A[run][lane * 4], e);
 #pragma unroll
       for (int j = 0; j < 4; ++j) dsum[j] = zsum[j] = 0.f;
       const Rows<T> dxs(a.out, t0, rows, a.C), dgs(a.dg, t0, rows, a.C);
 #pragma unroll
-      for (int i = GR - 1; i >= 0; --i) {
-        if (tr + i < rows) {
-          if (marked && m.E[run * GR + i] >= 0) state4(a.d_final, m.E[run * GR + i], a.C, c, in, e);
+      for (int q = R - 1; q >= 0; --q) {
+        if (tr + q < rows) {
+          if (marked && m.E[run * R + q] >= 0) state4(a.d_final, m.E[run * R + q], a.C, c, in, e);
           float dv[4], gv[4], dx[4], dg[4];
-          widen4(dr[i], dv);
-          widen4(gr[i], gv);
+          widen4(r.d[q], dv);
+          widen4(r.g[q], gv);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float dh = dv[j] + e[j];
-            e[j] = av[i][j] * dh;
-            dx[j] = b[i][j] * dh;
-            dg[j] = e[j] * hp[i][j];
+            e[j] = r.a[q][j] * dh;
+            dx[j] = COMPL ? one_minus(gate.g2(gv[j], j), r.a[q][j]) * dh : dh;
+            dg[j] = e[j] * hp[q][j];
             if constexpr (!GIVEN) {
               // dg/dz = lb s (1 - s), s = 1 / (1 + w), w = exp(-z).  w is kept
               // finite (a comparison, so that NaN stays) so that w s does not
@@ -719,23 +765,44 @@ __global__ void __launch_bounds__(GT, 4) kda_glr_bwd_kernel(GlrArgs a) {
               dsum[j] += dg[j];
             }
           }
-          dxs.store(voff, i * row_bytes, dx);
-          dgs.store(voff, i * row_bytes, dg);
-          if (marked && a.d_init && in && m.S[run * GR + i] >= 0)
-            store4(a.d_init + (int64_t)m.S[run * GR + i] * a.C + c, e);
-        } else if (in && a.zero_rest && tr + i < a.ax.total) {
-          store_zero4(static_cast<T*>(a.out) + (tr + i) * a.C + c);
-          store_zero4(static_cast<T*>(a.dg) + (tr + i) * a.C + c);
+          dxs.store(voff, q * row_bytes, dx);
+          dgs.store(voff, q * row_bytes, dg);
+          if (marked && a.d_init && in && m.S[run * R + q] >= 0)
+            store4(a.d_init + (int64_t)m.S[run * R + q] * a.C + c, e);
+        } else if (in && a.zero_rest && tr + q < a.ax.total) {
+          store_zero4(static_cast<T*>(a.out) + (tr + q) * a.C + c);
+          store_zero4(static_cast<T*>(a.dg) + (tr + q) * a.C + c);
         }
       }
       if constexpr (!GIVEN) {
-        // ft is free: a thread's own entry of it is all that was read since the last barrier
-        store4(&ft.B[run][lane * 4], dsum);
-        store4(&ft.A[run][lane * 4], zsum);
-        __syncthreads();  // the runs' sums
+        store4(&dsums[i & 1][run][lane * 4], dsum);
+        store4(&zsums[i & 1][run][lane * 4], zsum);
       }
-    }
-    __syncthreads();
+    };
+    Kept<T> r0, r1;
+    auto turn = [&](int i, Kept<T>& now, Kept<T>& then) {
+      const int item = slot[i & 7];
+      if (item >= items) return false;
+      mark(slot[(i + 2) & 7], i + 2);
+      map(slot[(i + 1) & 7], i + 1, then);
+      if (tid == 0) {
+        slot[(i + 3) & 7] = drawer.answer(a, asked);
+        asked = drawer.ask(a);
+      }
+      __syncthreads();  // what enters tile i, the maps of tile i + 1
+      finish(item, i, now);
+      fetch(slot[(i + 2) & 7], now);
+      return true;
+    };
+    mark(slot[0], 0);
+    mark(slot[1], 1);
+    fetch(slot[0], r0);
+    fetch(slot[1], r1);
+    __syncthreads();  // marks
+    map(slot[0], 0, r0);
+    __syncthreads();  // the maps of the first tile
+    for (int i = 0; turn(i, r0, r1) && turn(i + 1, r1, r0); i += 2) {}
+    __syncthreads();  // the sums of the last tile
   }
   if (a.d_init) {
     for (int64_t n = blockIdx.x; n < a.ax.N; n += gridDim.x) {
@@ -812,7 +879,8 @@ struct GlrLayout {
   size_t faults, tickets, enter, maps, part, total;
 };
 GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
-  const size_t tiles = (size_t)((T_total + GL - 1) / GL), w = tiles * (size_t)C;
+  const size_t tiles = (size_t)((T_total + GL<float> - 1) / GL<float>);  // of the shorter kind
+  const size_t w = tiles * (size_t)C;
   GlrLayout l;
   l.faults = 4;
   l.tickets = 256;
@@ -841,7 +909,7 @@ kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, f
   if (N > (int64_t)1 << 30 || !fits(N, H * K, kMaxElements)) return KDA_ERR_INVALID;
   if (cu_seqlens && T > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   if (!(flags & FLAG_GATE_GIVEN) && !aligned(dt_bias, 16)) return KDA_ERR_INVALID;
-  const int64_t tiles = (B * T + GL - 1) / GL, nblk = (H * K + GC - 1) / GC;
+  const int64_t L = tile_rows(dtype), tiles = (B * T + L - 1) / L, nblk = (H * K + GC - 1) / GC;
   if (!fits(tiles, nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // tile numbers are 32-bit
   a = GlrArgs{};
   a.A_log = A_log;
@@ -868,9 +936,9 @@ kda_status_t by_variant(int dtype, unsigned flags, P... p) {
            : (c ? F<float, false, true>::run(p...) : F<float, false, false>::run(p...));
 }
 
-// Workgroups of a pass: as many as run at once (two on a CU), fewer tiles than that one each.
+// Workgroups of a pass: as many as run at once, one on a CU.
 int64_t pass_grid(const GlrArgs& a) {
-  const int64_t items = (int64_t)a.ntiles * a.nblk, most = 512;
+  const int64_t items = (int64_t)a.ntiles * a.nblk, most = 256;
   return items < 1 ? 1 : items < most ? items : most;
 }
 kda_status_t clear(const GlrArgs& a, hipStream_t st) {
@@ -918,7 +986,7 @@ extern "C" {
 
 size_t kda_glr_states_size(int64_t T_total, int64_t H, int64_t K) {
   if (!glr_sizes_ok(T_total, H, K)) return 0;
-  return align256((size_t)((T_total + GL - 1) / GL) * (size_t)(H * K) * sizeof(float)) + 256;
+  return align256((size_t)((T_total + GL<float> - 1) / GL<float>) * (size_t)(H * K) * sizeof(float)) + 256;
 }
 
 size_t kda_glr_workspace_size(int64_t T_total, int64_t H, int64_t K) {
