@@ -32,6 +32,8 @@
 
 #include <limits.h>
 
+#include <type_traits>
+
 #include "../../include/kda.h"
 #include "kda_host.h"
 #include "kda_token.h"
@@ -45,15 +47,16 @@ constexpr int GW = GC / 4;       // lanes of a row
 constexpr int GD = GS * GW;      // threads that hold data: seven waves
 constexpr int GT = GD + GC;      // and one, a lane a channel, that finds what enters the tile
 static_assert(GD % 64 == 0 && GT == 512 && GS <= 32, "whole waves, runs in a 32-bit mask");
-// Rows of a run and of a tile: as many as the registers of one workgroup a CU
-// hold (8 of bf16, 4 of fp32: 224 and 112 rows).  More rows a tile mean fewer
-// tiles in flight on a column, and so less waiting, for the same bytes.
+// Rows of a run: as many as the registers of one workgroup a CU hold.  More
+// rows a tile mean fewer tiles in flight on a column, and so less waiting, for
+// the same bytes.  The forward has 8 of bf16 and 4 of fp32, tiles of 224 and 112
+// rows; the backward, which holds three arrays and h_{t-1}, has 4 of both.
+constexpr int BR = 4, BL = BR * GS;
 template <typename T>
-constexpr int GR = sizeof(T) == 2 ? 8 : 4;
+constexpr int FR = sizeof(T) == 2 ? 2 * BR : BR;
 template <typename T>
-constexpr int GL = GR<T> * GS;
-constexpr int GL_MAX = GS * 8;
-inline int tile_rows(int dtype) { return dtype == KDA_DTYPE_BF16 ? GL<__bf16> : GL<float>; }
+constexpr int FL = FR<T> * GS;
+constexpr int L_MAX = 2 * BL;
 constexpr int64_t kMaxChannels = (int64_t)1 << 21;  // a tile's rows span less than 2^30 bytes
 
 struct GlrArgs {
@@ -68,11 +71,11 @@ struct GlrArgs {
   const float* d_final;
   float* fin;
   float* d_init;
-  const float* states;  // [tiles][C] state entering every tile (backward)
+  const float* states;  // [backward tiles][C] state entering every BL rows
   // the pass's own, tiles counted in its order (the backward from the right):
   uint64_t* enter; // [tiles][C] what enters every tile, with KNOWN above it
   uint64_t* maps;  // [tiles][C] A (with KNOWN_MAP) and B of every tile's map
-  float* keep;     // forward: [tiles][C] what enters every tile, for the backward, or NULL
+  float* keep;     // forward: what enters every BL rows, for the backward, or NULL
   int* tickets;   // [sets] the next tile of each set of columns, TICKET_LINE apart
   int sets;
   unsigned* faults;
@@ -121,11 +124,12 @@ __device__ __forceinline__ float one_minus(float g2, float a) {
 }
 
 // The sequences that start (S) or end (E) at each row of the tile at t0, -1 for
-// none, and whether there is any; by one wave.
+// none, and whether there is any, or any row behind the last sequence; by one
+// wave.  S and E are only written where there is.
 struct Marks {
-  int S[GL_MAX], E[GL_MAX], any;
+  int S[L_MAX], E[L_MAX], any;
 };
-__device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_len, Marks& m) {
+__device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_len, int64_t rows, Marks& m) {
   const int lane = threadIdx.x & 63;
   const int64_t t1 = t0 + tile_len;
   // n0, n1: first sequences that start at t0, t1 or behind
@@ -139,7 +143,7 @@ __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_l
     n1 = axis_lower(ax, t1);
   }
   // (an end is the next one's start, so one at the very end of the tile is no start of it)
-  const bool any = n1 > n0 || (n0 <= ax.N && axis_start(ax, n0) == t1);
+  const bool any = n1 > n0 || (n0 <= ax.N && axis_start(ax, n0) == t1) || t1 > rows;
   if (lane == 0) m.any = any;
   if (!any) return;
   for (int i = lane; i < tile_len; i += 64) m.S[i] = m.E[i] = -1;
@@ -158,11 +162,11 @@ __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_l
 // descriptor ends behind the last row that belongs to a sequence: rows behind
 // it load as zeros and are not stored, and so does an offset of OUTSIDE.
 constexpr int OUTSIDE = 0x7ffffff0;
-template <typename T>
+template <typename T, int L>
 struct Rows {
   __amdgpu_buffer_rsrc_t r;
   __device__ __forceinline__ Rows(const void* base, int64_t t0, int64_t rows, int64_t C) {
-    const int64_t left = rows - t0 < GL<T> ? rows - t0 : GL<T>;
+    const int64_t left = rows - t0 < L ? rows - t0 : L;
     r = buf(static_cast<const T*>(base) + t0 * C, (uint32_t)((left > 0 ? left : 0) * C * sizeof(T)));
   }
   __device__ __forceinline__ raw4<T> load(int voff, int soff) const {
@@ -276,7 +280,8 @@ struct Tile {
 // the wave that holds no data: finds what enters the tile (not where the tile
 // begins `fresh`, with a sequence's first row), hands on what leaves it, and
 // puts what enters every run into t.A.
-template <bool REV, bool MARKED>
+// HALVES: keep what enters every half (2) or whole (1) tile for the backward.
+template <bool REV, bool MARKED, int HALVES>
 __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps, int k, int blk, bool fresh) {
   const int ch = threadIdx.x & 63;
   const int64_t c = (int64_t)blk * GC + ch;
@@ -308,10 +313,12 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps,
   }
   if (!last && in) post(a.enter + (int64_t)(k + 1) * a.C + c, KNOWN | __float_as_uint(leave));
   if (resets && ask) s = look_back(a, maps, k, c, in, word);
-  if (a.keep && in && !last) a.keep[(int64_t)(k + 1) * a.C + c] = leave;
+  // (what enters a fresh tile is not asked for, and what is kept for it not used)
+  float* keep = HALVES > 0 && a.keep && in ? a.keep + (int64_t)k * HALVES * a.C + c : nullptr;
 #pragma unroll
   for (int i = 0; i < GS; ++i) {
     const int run = REV ? GS - 1 - i : i;
+    if (HALVES > 0 && i % (GS / (HALVES > 0 ? HALVES : 1)) == 0 && keep) keep[i / (GS / (HALVES > 0 ? HALVES : 1)) * a.C] = s;
     t.A[run][ch] = s;
     s = MARKED && (resets >> run & 1) ? B[run] : A[run] * s + B[run];
   }
@@ -366,11 +373,11 @@ __device__ __forceinline__ void state4(const float* p, int n, int64_t C, int64_t
 // One run in one thread: decays and inputs.
 template <typename T>
 struct Run {
-  float a[GR<T>][4], u[GR<T>][4];
+  float a[FR<T>][4], u[FR<T>][4];
 };
 template <typename T>
 struct Raw {
-  raw4<T> x[GR<T>], g[GR<T>];
+  raw4<T> x[FR<T>], g[FR<T>];
 };
 
 // Seven waves hold the data and one finds what enters the tiles, so that rows
@@ -382,7 +389,7 @@ struct Raw {
 // holds the tickets of those tiles and works on them in order.
 template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
-  constexpr int R = GR<T>, L = GL<T>;
+  constexpr int R = FR<T>, L = FL<T>;
   __shared__ Tile tiles[2];
   __shared__ Maps maps;
   __shared__ Marks marks[4];
@@ -407,8 +414,8 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       if (item >= items) break;
       const Marks& m = marks[i & 3];
       const int k = item / a.nblk, blk = item % a.nblk;
-      if (m.any) join_runs<false, true>(a, tiles[i & 1], maps, k, blk, m.S[0] >= 0);
-      else join_runs<false, false>(a, tiles[i & 1], maps, k, blk, false);
+      if (m.any) join_runs<false, true, FR<T> / BR>(a, tiles[i & 1], maps, k, blk, m.S[0] >= 0);
+      else join_runs<false, false, FR<T> / BR>(a, tiles[i & 1], maps, k, blk, false);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
     }
   } else {
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       if (item >= items) return;
       int64_t t0, c;
       const int voff = place(item, t0, c);
-      const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C);
+      const Rows<T, L> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         w.g[i] = gs.load(voff, i * row_bytes);
@@ -431,11 +438,10 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
     };
     // the marks of tile i, by the first wave, before anybody needs them
     auto mark = [&](int item, int i) {
-      if (tid < 64 && item < items) mark_tile(a.ax, (int64_t)(item / a.nblk) * L, L, marks[i & 3]);
+      if (tid < 64 && item < items) mark_tile(a.ax, (int64_t)(item / a.nblk) * L, L, rows, marks[i & 3]);
     };
     // the maps of tile i, from rows that were asked for
-    auto map = [&](int item, int i, const Raw<T>& w, Run<T>& r) {
-      if (item >= items) return;
+    auto map_ = [&](auto marked, int item, int i, const Raw<T>& w, Run<T>& r) {
       int64_t t0, c;
       place(item, t0, c);
       const bool in = c < a.C;
@@ -462,10 +468,9 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
         A[j] = 1.f;
         B[j] = 0.f;
       }
-      const bool marked = m.any;
 #pragma unroll
       for (int q = 0; q < R; ++q) {
-        if (marked && m.S[run * R + q] >= 0) {
+        if (marked() && m.S[run * R + q] >= 0) {
           reset = true;
           state4(a.init, m.S[run * R + q], a.C, c, in, B);
         }
@@ -479,23 +484,27 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       store4(&t.B[run][lane * 4], B);
       if (lane == 0) t.reset[run] = reset;
     };
+    auto map = [&](int item, int i, const Raw<T>& w, Run<T>& r) {
+      if (item >= items) return;
+      if (marks[i & 3].any) map_(std::true_type{}, item, i, w, r);
+      else map_(std::false_type{}, item, i, w, r);
+    };
     // the outputs of tile i
-    auto finish = [&](int item, int i, const Run<T>& r) {
+    auto finish_ = [&](auto marked, int item, int i, const Run<T>& r) {
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const bool in = c < a.C;
       const Marks& m = marks[i & 3];
-      const bool marked = m.any;
       float h[4];
       load_f4(&tiles[i & 1].A[run][lane * 4], h);
-      const Rows<T> os(a.out, t0, rows, a.C);
+      const Rows<T, L> os(a.out, t0, rows, a.C);
 #pragma unroll
       for (int q = 0; q < R; ++q) {
-        if (marked && m.S[run * R + q] >= 0) state4(a.init, m.S[run * R + q], a.C, c, in, h);
+        if (marked() && m.S[run * R + q] >= 0) state4(a.init, m.S[run * R + q], a.C, c, in, h);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[j] = r.a[q][j] * h[j] + r.u[q][j];
         os.store(voff, q * row_bytes, h);
-        if (marked && a.fin && in && m.E[run * R + q] >= 0) store4(a.fin + (int64_t)m.E[run * R + q] * a.C + c, h);
+        if (marked() && a.fin && in && m.E[run * R + q] >= 0) store4(a.fin + (int64_t)m.E[run * R + q] * a.C + c, h);
       }
       if (a.zero_rest && t0 + L > rows && in) {
         for (int q = 0; q < R; ++q) {
@@ -503,6 +512,10 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
           if (t >= rows && t < a.ax.total) store_zero4(static_cast<T*>(a.out) + t * a.C + c);
         }
       }
+    };
+    auto finish = [&](int item, int i, const Run<T>& r) {
+      if (marks[i & 3].any) finish_(std::true_type{}, item, i, r);
+      else finish_(std::false_type{}, item, i, r);
     };
     Run<T> r0, r1;
     Raw<T> w0, w1;
@@ -542,15 +555,16 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
 // The backward's run keeps its rows as loaded: they are needed again.
 template <typename T>
 struct Kept {
-  float a[GR<T>][4];
-  raw4<T> x[GR<T>], g[GR<T>], d[GR<T>];
+  float a[BR][4];
+  raw4<T> x[BR], g[BR], d[BR];
 };
 
 // As the forward, from the right, with a second set of maps for h, whose
-// entering states are given: the wave that joins does both.
+// entering states are given: the wave that joins does both.  Rows are asked for
+// when a tile is finished, into its registers.
 template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
-  constexpr int R = GR<T>, L = GL<T>;
+  constexpr int R = BR, L = BL;
   __shared__ Tile et[2], ht[2];  // maps of e, from the right, and of h
   __shared__ float dsums[GIVEN ? 1 : 2][GS][GC], zsums[GIVEN ? 1 : 2][GS][GC];
   __shared__ Maps maps;
@@ -594,8 +608,8 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       if (item >= items) break;
       const Marks& m = marks[i & 3];
       const int k = item / a.nblk, blk = item % a.nblk;
-      if (m.any) join_runs<true, true>(a, et[i & 1], maps, k, blk, m.E[L - 1] >= 0);
-      else join_runs<true, false>(a, et[i & 1], maps, k, blk, false);
+      if (m.any) join_runs<true, true, 0>(a, et[i & 1], maps, k, blk, m.E[L - 1] >= 0);
+      else join_runs<true, false, 0>(a, et[i & 1], maps, k, blk, false);
       Tile& t = ht[i & 1];
       const uint32_t resets = m.any ? (uint32_t)__ballot(ch < GS && t.reset[ch < GS ? ch : 0]) : 0;
 #pragma unroll
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       if (item >= items) return;
       int64_t t0, c;
       const int voff = place(item, t0, c);
-      const Rows<T> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
+      const Rows<T, L> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         r.g[i] = gs.load(voff, i * row_bytes);
@@ -640,10 +654,9 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
     };
     auto mark = [&](int item, int i) {
       if (tid < 64 && item < items)
-        mark_tile(a.ax, (int64_t)(a.ntiles - 1 - item / a.nblk) * L, L, marks[i & 3]);
+        mark_tile(a.ax, (int64_t)(a.ntiles - 1 - item / a.nblk) * L, L, rows, marks[i & 3]);
     };
-    auto map = [&](int item, int i, Kept<T>& r) {
-      if (item >= items) return;
+    auto map_ = [&](auto marked, int item, int i, Kept<T>& r) {
       int64_t t0, c;
       place(item, t0, c);
       const bool in = c < a.C;
@@ -651,7 +664,6 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       Gate<GIVEN> gate;
       gate.init(a, in ? c : 0);
       const Marks& m = marks[i & 3];
-      const bool marked = m.any;
       {  // of h
         Tile& t = ht[i & 1];
         float A[4], B[4];
@@ -663,7 +675,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         }
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-          if (marked && m.S[run * R + q] >= 0) {
+          if (marked() && m.S[run * R + q] >= 0) {
             reset = true;
             state4(a.init, m.S[run * R + q], a.C, c, in, B);
           }
@@ -693,8 +705,8 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         }
 #pragma unroll
         for (int q = R - 1; q >= 0; --q) {
-          if (tr + q < rows) {
-            if (marked && m.E[run * R + q] >= 0) {
+          if (!marked() || tr + q < rows) {
+            if (marked() && m.E[run * R + q] >= 0) {
               reset = true;
               state4(a.d_final, m.E[run * R + q], a.C, c, in, Q);
             }
@@ -712,7 +724,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         if (lane == 0) t.reset[run] = reset;
       }
     };
-    auto finish = [&](int item, int i, const Kept<T>& r) {
+    auto map = [&](int item, int i, Kept<T>& r) {
+      if (item >= items) return;
+      if (marks[i & 3].any) map_(std::true_type{}, item, i, r);
+      else map_(std::false_type{}, item, i, r);
+    };
+    auto finish_ = [&](auto marked, int item, int i, const Kept<T>& r) {
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const bool in = c < a.C;
@@ -720,13 +737,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       Gate<GIVEN> gate;
       gate.init(a, in ? c : 0);
       const Marks& m = marks[i & 3];
-      const bool marked = m.any;
       float h[4], e[4], hp[R][4], dsum[4], zsum[4];
       load_f4(&ht[i & 1].A[run][lane * 4], h);
       load_f4(&et[i & 1].A[run][lane * 4], e);
 #pragma unroll
       for (int q = 0; q < R; ++q) {
-        if (marked && m.S[run * R + q] >= 0) state4(a.init, m.S[run * R + q], a.C, c, in, h);
+        if (marked() && m.S[run * R + q] >= 0) state4(a.init, m.S[run * R + q], a.C, c, in, h);
         float xv[4], gv[4];
         widen4(r.x[q], xv);
         widen4(r.g[q], gv);
@@ -738,11 +754,11 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) dsum[j] = zsum[j] = 0.f;
-      const Rows<T> dxs(a.out, t0, rows, a.C), dgs(a.dg, t0, rows, a.C);
+      const Rows<T, L> dxs(a.out, t0, rows, a.C), dgs(a.dg, t0, rows, a.C);
 #pragma unroll
       for (int q = R - 1; q >= 0; --q) {
-        if (tr + q < rows) {
-          if (marked && m.E[run * R + q] >= 0) state4(a.d_final, m.E[run * R + q], a.C, c, in, e);
+        if (!marked() || tr + q < rows) {
+          if (marked() && m.E[run * R + q] >= 0) state4(a.d_final, m.E[run * R + q], a.C, c, in, e);
           float dv[4], gv[4], dx[4], dg[4];
           widen4(r.d[q], dv);
           widen4(r.g[q], gv);
@@ -767,7 +783,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
           }
           dxs.store(voff, q * row_bytes, dx);
           dgs.store(voff, q * row_bytes, dg);
-          if (marked && a.d_init && in && m.S[run * R + q] >= 0)
+          if (marked() && a.d_init && in && m.S[run * R + q] >= 0)
             store4(a.d_init + (int64_t)m.S[run * R + q] * a.C + c, e);
         } else if (in && a.zero_rest && tr + q < a.ax.total) {
           store_zero4(static_cast<T*>(a.out) + (tr + q) * a.C + c);
@@ -779,7 +795,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         store4(&zsums[i & 1][run][lane * 4], zsum);
       }
     };
-    Kept<T> r0, r1;
+    auto finish = [&](int item, int i, const Kept<T>& r) {
+      if (marks[i & 3].any) finish_(std::true_type{}, item, i, r);
+      else finish_(std::false_type{}, item, i, r);
+    };
+    // tile i is ready in `now`; tile i + 1 is made in `then`; `now` takes tile i + AHEAD
+    constexpr int AHEAD = sizeof(T) == 2 ? 3 : 2;
     auto turn = [&](int i, Kept<T>& now, Kept<T>& then) {
       const int item = slot[i & 7];
       if (item >= items) return false;
@@ -791,17 +812,27 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       }
       __syncthreads();  // what enters tile i, the maps of tile i + 1
       finish(item, i, now);
-      fetch(slot[(i + 2) & 7], now);
+      fetch(slot[(i + AHEAD) & 7], now);
       return true;
     };
+    Kept<T> r0, r1;
     mark(slot[0], 0);
     mark(slot[1], 1);
     fetch(slot[0], r0);
     fetch(slot[1], r1);
-    __syncthreads();  // marks
-    map(slot[0], 0, r0);
-    __syncthreads();  // the maps of the first tile
-    for (int i = 0; turn(i, r0, r1) && turn(i + 1, r1, r0); i += 2) {}
+    if constexpr (AHEAD == 3) {
+      Kept<T> r2;
+      fetch(slot[2], r2);
+      __syncthreads();  // marks
+      map(slot[0], 0, r0);
+      __syncthreads();  // the maps of the first tile
+      for (int i = 0; turn(i, r0, r1) && turn(i + 1, r1, r2) && turn(i + 2, r2, r0); i += 3) {}
+    } else {
+      __syncthreads();  // marks
+      map(slot[0], 0, r0);
+      __syncthreads();  // the maps of the first tile
+      for (int i = 0; turn(i, r0, r1) && turn(i + 1, r1, r0); i += 2) {}
+    }
     __syncthreads();  // the sums of the last tile
   }
   if (a.d_init) {
@@ -879,7 +910,7 @@ struct GlrLayout {
   size_t faults, tickets, enter, maps, part, total;
 };
 GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
-  const size_t tiles = (size_t)((T_total + GL<float> - 1) / GL<float>);  // of the shorter kind
+  const size_t tiles = (size_t)((T_total + BL - 1) / BL);  // of the shorter kind
   const size_t w = tiles * (size_t)C;
   GlrLayout l;
   l.faults = 4;
@@ -898,7 +929,7 @@ bool glr_sizes_ok(int64_t T_total, int64_t H, int64_t K) {
 // Checks shared by the entry points; fills the sizes and the gate.
 kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, float lower_bound,
                          const int32_t* cu_seqlens, int64_t B, int64_t T, int64_t H, int64_t K, int64_t N,
-                         int dtype, unsigned flags, bool step = false) {
+                         int dtype, unsigned flags, bool bwd, bool step = false) {
   if (B < 1 || T < 0 || H < 1 || K < 1 || N < 1) return KDA_ERR_INVALID;
   if (flags & ~(unsigned)(FLAG_GATE_GIVEN | FLAG_COMPLEMENT | (step ? 0 : FLAG_ZERO_REST))) return KDA_ERR_INVALID;
   if (cu_seqlens ? B != 1 : N != B) return KDA_ERR_INVALID;
@@ -909,7 +940,7 @@ kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, f
   if (N > (int64_t)1 << 30 || !fits(N, H * K, kMaxElements)) return KDA_ERR_INVALID;
   if (cu_seqlens && T > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   if (!(flags & FLAG_GATE_GIVEN) && !aligned(dt_bias, 16)) return KDA_ERR_INVALID;
-  const int64_t L = tile_rows(dtype), tiles = (B * T + L - 1) / L, nblk = (H * K + GC - 1) / GC;
+  const int64_t L = bwd || dtype == KDA_DTYPE_FP32 ? BL : L_MAX, tiles = (B * T + L - 1) / L, nblk = (H * K + GC - 1) / GC;
   if (!fits(tiles, nblk, (int64_t)1 << 30)) return KDA_ERR_INVALID;  // tile numbers are 32-bit
   a = GlrArgs{};
   a.A_log = A_log;
@@ -986,7 +1017,7 @@ extern "C" {
 
 size_t kda_glr_states_size(int64_t T_total, int64_t H, int64_t K) {
   if (!glr_sizes_ok(T_total, H, K)) return 0;
-  return align256((size_t)((T_total + GL<float> - 1) / GL<float>) * (size_t)(H * K) * sizeof(float)) + 256;
+  return align256((size_t)((T_total + L_MAX - 1) / L_MAX * 2) * (size_t)(H * K) * sizeof(float)) + 256;
 }
 
 size_t kda_glr_workspace_size(int64_t T_total, int64_t H, int64_t K) {
@@ -1002,7 +1033,7 @@ kda_status_t kda_glr_fwd(const void* x, const void* raw_gate, void* out, void* w
                          float* final_state, float* states, const int32_t* cu_seqlens, int64_t B, int64_t T,
                          int64_t H, int64_t K, int64_t N, int dtype, unsigned flags, void* stream) {
   GlrArgs a;
-  const kda_status_t s = glr_prepare(a, A_log, dt_bias, lower_bound, cu_seqlens, B, T, H, K, N, dtype, flags);
+  const kda_status_t s = glr_prepare(a, A_log, dt_bias, lower_bound, cu_seqlens, B, T, H, K, N, dtype, flags, false);
   if (s != KDA_SUCCESS) return s;
   if (a.ax.total > 0 && (!x || !raw_gate || !out)) return KDA_ERR_INVALID;
   if (!aligned_all(4 * dtype_bytes(dtype), {x, raw_gate, out}) ||
@@ -1028,7 +1059,7 @@ kda_status_t kda_glr_bwd(const void* x, const void* raw_gate, const float* state
                          const int32_t* cu_seqlens, int64_t B, int64_t T, int64_t H, int64_t K, int64_t N,
                          int dtype, unsigned flags, void* stream) {
   GlrArgs a;
-  const kda_status_t s = glr_prepare(a, A_log, dt_bias, lower_bound, cu_seqlens, B, T, H, K, N, dtype, flags);
+  const kda_status_t s = glr_prepare(a, A_log, dt_bias, lower_bound, cu_seqlens, B, T, H, K, N, dtype, flags, true);
   if (s != KDA_SUCCESS) return s;
   if (a.ax.total > 0 && (!x || !raw_gate || !states || !d_out || !dx || !d_raw_gate)) return KDA_ERR_INVALID;
   if (!(flags & FLAG_GATE_GIVEN) && (!dA_log || !d_dt_bias)) return KDA_ERR_INVALID;
@@ -1058,7 +1089,7 @@ kda_status_t kda_glr_step(const void* x, const void* raw_gate, void* out, const 
                           float lower_bound, const float* initial_state, float* final_state, int64_t B, int64_t T,
                           int64_t H, int64_t K, int dtype, unsigned flags, void* stream) {
   GlrArgs a;
-  const kda_status_t s = glr_prepare(a, A_log, dt_bias, lower_bound, nullptr, B, T, H, K, B, dtype, flags, true);
+  const kda_status_t s = glr_prepare(a, A_log, dt_bias, lower_bound, nullptr, B, T, H, K, B, dtype, flags, false, true);
   if (s != KDA_SUCCESS) return s;
   if (a.ax.total > 0 && (!x || !raw_gate || !out)) return KDA_ERR_INVALID;
   if (!aligned_all(4 * dtype_bytes(dtype), {x, raw_gate, out}) || !aligned_all(16, {initial_state, final_state}))
