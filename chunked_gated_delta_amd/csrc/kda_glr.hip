@@ -132,6 +132,10 @@ struct Marks {
 __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_len, int64_t rows, Marks& m) {
   const int lane = threadIdx.x & 63;
   const int64_t t1 = t0 + tile_len;
+  if (!ax.cu && ax.N == 1 && t0 > 0 && t1 < rows) {  // inside the one sequence
+    if (lane == 0) m.any = 0;
+    return;
+  }
   // n0, n1: first sequences that start at t0, t1 or behind
   const int64_t n0 = axis_lower(ax, t0);
   int64_t n1 = n0;
@@ -324,6 +328,8 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps,
   }
 }
 
+constexpr int ASKS = 64;  // the thread that asks for tickets: of another wave than the one that makes marks
+
 // Tiles are handed out in order by counters.  One counter serves a tile each
 // 13 ns at best (measured: every pass ran at that pace, whatever it computed),
 // less than memory allows, so the columns are split into up to eight sets of
@@ -335,22 +341,32 @@ constexpr int SETS = 8;
 constexpr int TICKET_LINE = 64;  // ints: counters on lines of their own
 struct Drawer {
   int set, left;  // the set drawn from, sets not used up
-  __device__ __forceinline__ Drawer(const GlrArgs& a) : set(blockIdx.x % a.sets), left(a.sets) {}
-  // A ticket is asked for by ask() and turned into a tile's number, tile * nblk
-  // + column block, or INT_MAX, by answer(), later: the round trip lies between.
-  // By one thread.
+  int first, n;   // its columns
+  double per;     // 1 / n
+  __device__ __forceinline__ Drawer(const GlrArgs& a) : set(blockIdx.x % a.sets), left(a.sets) { enter(a); }
+  __device__ __forceinline__ void enter(const GlrArgs& a) {
+    first = (int)((int64_t)a.nblk * set / a.sets);
+    n = (int)((int64_t)a.nblk * (set + 1) / a.sets) - first;
+    per = 1.0 / n;
+  }
+  // A ticket is asked for by ask() and turned into a tile (x: its number in the
+  // pass's order, ntiles for none; y: its column block) by answer(), later: the
+  // round trip lies between.  By one thread.
   __device__ __forceinline__ int ask(const GlrArgs& a) const {
     return __hip_atomic_fetch_add(a.tickets + set * TICKET_LINE, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __device__ __forceinline__ int answer(const GlrArgs& a, int t) {
+  __device__ __forceinline__ int2 answer(const GlrArgs& a, int t) {
     while (left > 0) {
-      const int first = (int)((int64_t)a.nblk * set / a.sets), n = (int)((int64_t)a.nblk * (set + 1) / a.sets) - first;
-      if (t / n < a.ntiles) return t / n * a.nblk + first + t % n;
+      int q = (int)(t * per);  // t / n, off by one at most
+      q -= q * n > t;
+      q += (q + 1) * n <= t;
+      if (q < a.ntiles) return make_int2(q, first + t - q * n);
       if (--left == 0) break;
       set = set + 1 < a.sets ? set + 1 : 0;
+      enter(a);
       t = ask(a);
     }
-    return INT_MAX;
+    return make_int2(a.ntiles, 0);
   }
 };
 
@@ -393,13 +409,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
   __shared__ Tile tiles[2];
   __shared__ Maps maps;
   __shared__ Marks marks[4];
-  __shared__ int slot[8];  // tickets, by turns
+  __shared__ int2 slot[8];  // tiles, by turns
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
-  const int items = a.ntiles * a.nblk;
   Drawer drawer(a);
   int asked = 0;
-  if (tid == 0) {
+  if (tid == ASKS) {
     for (int i = 0; i < 4; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
     asked = drawer.ask(a);
   }
@@ -410,23 +425,23 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
     __syncthreads();  // marks
     __syncthreads();  // the maps of the first tile
     for (int i = 0;; ++i) {
-      const int item = slot[i & 7];
-      if (item >= items) break;
+      const int2 item = slot[i & 7];
+      if (item.x >= a.ntiles) break;
       const Marks& m = marks[i & 3];
-      const int k = item / a.nblk, blk = item % a.nblk;
+      const int k = item.x, blk = item.y;
       if (m.any) join_runs<false, true, FR<T> / BR>(a, tiles[i & 1], maps, k, blk, m.S[0] >= 0);
       else join_runs<false, false, FR<T> / BR>(a, tiles[i & 1], maps, k, blk, false);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
     }
   } else {
     const int row_bytes = (int)(a.C * sizeof(T));
-    auto place = [&](int item, int64_t& t0, int64_t& c) {
-      t0 = (int64_t)(item / a.nblk) * L;
-      c = (int64_t)(item % a.nblk) * GC + lane * 4;
+    auto place = [&](int2 item, int64_t& t0, int64_t& c) {
+      t0 = (int64_t)item.x * L;
+      c = (int64_t)item.y * GC + lane * 4;
       return c < a.C ? run * R * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
     };
-    auto fetch = [&](int item, Raw<T>& w) {
-      if (item >= items) return;
+    auto fetch = [&](int2 item, Raw<T>& w) {
+      if (item.x >= a.ntiles) return;
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const Rows<T, L> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C);
@@ -437,11 +452,11 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       }
     };
     // the marks of tile i, by the first wave, before anybody needs them
-    auto mark = [&](int item, int i) {
-      if (tid < 64 && item < items) mark_tile(a.ax, (int64_t)(item / a.nblk) * L, L, rows, marks[i & 3]);
+    auto mark = [&](int2 item, int i) {
+      if (tid < 64 && item.x < a.ntiles) mark_tile(a.ax, (int64_t)item.x * L, L, rows, marks[i & 3]);
     };
     // the maps of tile i, from rows that were asked for
-    auto map_ = [&](auto marked, int item, int i, const Raw<T>& w, Run<T>& r) {
+    auto map_ = [&](auto marked, int2 item, int i, const Raw<T>& w, Run<T>& r) {
       int64_t t0, c;
       place(item, t0, c);
       const bool in = c < a.C;
@@ -484,13 +499,13 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       store4(&t.B[run][lane * 4], B);
       if (lane == 0) t.reset[run] = reset;
     };
-    auto map = [&](int item, int i, const Raw<T>& w, Run<T>& r) {
-      if (item >= items) return;
+    auto map = [&](int2 item, int i, const Raw<T>& w, Run<T>& r) {
+      if (item.x >= a.ntiles) return;
       if (marks[i & 3].any) map_(std::true_type{}, item, i, w, r);
       else map_(std::false_type{}, item, i, w, r);
     };
     // the outputs of tile i
-    auto finish_ = [&](auto marked, int item, int i, const Run<T>& r) {
+    auto finish_ = [&](auto marked, int2 item, int i, const Run<T>& r) {
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const bool in = c < a.C;
@@ -513,7 +528,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
         }
       }
     };
-    auto finish = [&](int item, int i, const Run<T>& r) {
+    auto finish = [&](int2 item, int i, const Run<T>& r) {
       if (marks[i & 3].any) finish_(std::true_type{}, item, i, r);
       else finish_(std::false_type{}, item, i, r);
     };
@@ -521,11 +536,11 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
     Raw<T> w0, w1;
     // tile i: its run `now` is ready; tile i + 1 is made from `w`, which then takes tile i + 3
     auto turn = [&](int i, Run<T>& now, Run<T>& then, Raw<T>& w) {
-      const int item = slot[i & 7];
-      if (item >= items) return false;
+      const int2 item = slot[i & 7];
+      if (item.x >= a.ntiles) return false;
       mark(slot[(i + 2) & 7], i + 2);
       map(slot[(i + 1) & 7], i + 1, w, then);
-      if (tid == 0) {  // the ticket that was asked for a tile ago
+      if (tid == ASKS) {  // the ticket that was asked for a tile ago
         slot[(i + 4) & 7] = drawer.answer(a, asked);
         asked = drawer.ask(a);
       }
@@ -569,13 +584,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
   __shared__ float dsums[GIVEN ? 1 : 2][GS][GC], zsums[GIVEN ? 1 : 2][GS][GC];
   __shared__ Maps maps;
   __shared__ Marks marks[4];
-  __shared__ int slot[8];
+  __shared__ int2 slot[8];
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
-  const int items = a.ntiles * a.nblk;
   Drawer drawer(a);
   int asked = 0;
-  if (tid == 0) {
+  if (tid == ASKS) {
     for (int i = 0; i < 3; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
     asked = drawer.ask(a);
   }
@@ -583,13 +597,13 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
   if (tid >= GD) {
     __builtin_amdgcn_s_setprio(3);
     const int ch = tid - GD;
-    auto state_of = [&](int item) {  // h entering the tile
-      const int64_t c = (int64_t)(item % a.nblk) * GC + ch;
-      return item < items && c < a.C ? a.states[(int64_t)(a.ntiles - 1 - item / a.nblk) * a.C + c] : 0.f;
+    auto state_of = [&](int2 item) {  // h entering the tile
+      const int64_t c = (int64_t)item.y * GC + ch;
+      return item.x < a.ntiles && c < a.C ? a.states[(int64_t)(a.ntiles - 1 - item.x) * a.C + c] : 0.f;
     };
     // d_raw and dz z over the tile, from the runs' sums of tile i, a tile behind
-    auto add_up = [&](int item, int i) {
-      const int64_t c = (int64_t)(item % a.nblk) * GC + ch;
+    auto add_up = [&](int2 item, int i) {
+      const int64_t c = (int64_t)item.y * GC + ch;
       if (c >= a.C) return;
       float d = 0.f, z = 0.f;
 #pragma unroll
@@ -597,17 +611,17 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         d += dsums[i & (GIVEN ? 0 : 1)][q][ch];
         z += zsums[i & (GIVEN ? 0 : 1)][q][ch];
       }
-      a.part[(int64_t)(a.ntiles - 1 - item / a.nblk) * a.C + c] = make_float2(d, z);
+      a.part[(int64_t)(a.ntiles - 1 - item.x) * a.C + c] = make_float2(d, z);
     };
     float s = state_of(slot[0]);
     int last = -1;
     __syncthreads();  // marks
     __syncthreads();  // the maps of the first tile
     for (int i = 0;; ++i) {
-      const int item = slot[i & 7];
-      if (item >= items) break;
+      const int2 item = slot[i & 7];
+      if (item.x >= a.ntiles) break;
       const Marks& m = marks[i & 3];
-      const int k = item / a.nblk, blk = item % a.nblk;
+      const int k = item.x, blk = item.y;
       if (m.any) join_runs<true, true, 0>(a, et[i & 1], maps, k, blk, m.E[L - 1] >= 0);
       else join_runs<true, false, 0>(a, et[i & 1], maps, k, blk, false);
       Tile& t = ht[i & 1];
@@ -635,13 +649,13 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
     if (!GIVEN && last >= 0) add_up(slot[last & 7], last);
   } else {
     const int row_bytes = (int)(a.C * sizeof(T));
-    auto place = [&](int item, int64_t& t0, int64_t& c) {
-      t0 = (int64_t)(a.ntiles - 1 - item / a.nblk) * L;
-      c = (int64_t)(item % a.nblk) * GC + lane * 4;
+    auto place = [&](int2 item, int64_t& t0, int64_t& c) {
+      t0 = (int64_t)(a.ntiles - 1 - item.x) * L;
+      c = (int64_t)item.y * GC + lane * 4;
       return c < a.C ? run * R * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
     };
-    auto fetch = [&](int item, Kept<T>& r) {
-      if (item >= items) return;
+    auto fetch = [&](int2 item, Kept<T>& r) {
+      if (item.x >= a.ntiles) return;
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const Rows<T, L> xs(a.x, t0, rows, a.C), gs(a.g, t0, rows, a.C), ds(a.d_out, t0, rows, a.C);
@@ -652,11 +666,11 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         r.x[i] = xs.load(voff, i * row_bytes);
       }
     };
-    auto mark = [&](int item, int i) {
-      if (tid < 64 && item < items)
-        mark_tile(a.ax, (int64_t)(a.ntiles - 1 - item / a.nblk) * L, L, rows, marks[i & 3]);
+    auto mark = [&](int2 item, int i) {
+      if (tid < 64 && item.x < a.ntiles)
+        mark_tile(a.ax, (int64_t)(a.ntiles - 1 - item.x) * L, L, rows, marks[i & 3]);
     };
-    auto map_ = [&](auto marked, int item, int i, Kept<T>& r) {
+    auto map_ = [&](auto marked, int2 item, int i, Kept<T>& r) {
       int64_t t0, c;
       place(item, t0, c);
       const bool in = c < a.C;
@@ -724,12 +738,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         if (lane == 0) t.reset[run] = reset;
       }
     };
-    auto map = [&](int item, int i, Kept<T>& r) {
-      if (item >= items) return;
+    auto map = [&](int2 item, int i, Kept<T>& r) {
+      if (item.x >= a.ntiles) return;
       if (marks[i & 3].any) map_(std::true_type{}, item, i, r);
       else map_(std::false_type{}, item, i, r);
     };
-    auto finish_ = [&](auto marked, int item, int i, const Kept<T>& r) {
+    auto finish_ = [&](auto marked, int2 item, int i, const Kept<T>& r) {
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const bool in = c < a.C;
@@ -795,18 +809,18 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         store4(&zsums[i & 1][run][lane * 4], zsum);
       }
     };
-    auto finish = [&](int item, int i, const Kept<T>& r) {
+    auto finish = [&](int2 item, int i, const Kept<T>& r) {
       if (marks[i & 3].any) finish_(std::true_type{}, item, i, r);
       else finish_(std::false_type{}, item, i, r);
     };
     // tile i is ready in `now`; tile i + 1 is made in `then`; `now` takes tile i + AHEAD
     constexpr int AHEAD = sizeof(T) == 2 ? 3 : 2;
     auto turn = [&](int i, Kept<T>& now, Kept<T>& then) {
-      const int item = slot[i & 7];
-      if (item >= items) return false;
+      const int2 item = slot[i & 7];
+      if (item.x >= a.ntiles) return false;
       mark(slot[(i + 2) & 7], i + 2);
       map(slot[(i + 1) & 7], i + 1, then);
-      if (tid == 0) {
+      if (tid == ASKS) {
         slot[(i + 3) & 7] = drawer.answer(a, asked);
         asked = drawer.ask(a);
       }
