@@ -165,7 +165,7 @@ __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_l
 // Loads and stores of a tile by 32-bit offsets from its first row.  The
 // descriptor ends behind the last row that belongs to a sequence: rows behind
 // it load as zeros and are not stored, and so does an offset of OUTSIDE.
-constexpr int OUTSIDE = 0x7ffffff0;
+constexpr int OUTSIDE = 0x40000000;  // past any tile, also with a row's offset added
 template <typename T, int L>
 struct Rows {
   __amdgpu_buffer_rsrc_t r;
@@ -180,15 +180,19 @@ struct Rows {
       return __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
     }
   }
-  __device__ __forceinline__ void store(int voff, int soff, const float (&d)[4]) const {
+  // The row's offset goes into the lane's: a 16-byte store with an offset in a
+  // scalar register reads its data late, and the compiler, which keeps the next
+  // write of those registers away from a store without one, does not do so
+  // there (seen as single wrong elements of fp32 outputs).
+  __device__ __forceinline__ void store(int voff, int off, const float (&d)[4]) const {
     if constexpr (sizeof(T) == 2) {
       bf16x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = (__bf16)d[i];
-      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), r, voff, soff, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), r, voff + off, 0, 0);
     } else {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, make_float4(d[0], d[1], d[2], d[3])), r, voff,
-                                             soff, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, make_float4(d[0], d[1], d[2], d[3])), r,
+                                             voff + off, 0, 0);
     }
   }
 };
