@@ -111,6 +111,7 @@ _lib.kda_workspace_faults.restype = ctypes.c_int
 _lib.kda_fwd_noalloc.argtypes = [_P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, ctypes.c_float, _P, _P, _P,
                                  _I64, _I64, _I64, _I64, _I64, _I64, _P]
 _lib.kda_fwd_noalloc.restype = ctypes.c_int
+_FN = {}
 _I, _U, _F, _SZ = ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
 for _name, _args in {
     "kda_glr_fwd": [_P] * 4 + [_SZ, _P, _P, _F, _P, _P, _P, _P] + [_I64] * 5 + [_I, _U, _P],
@@ -124,6 +125,7 @@ for _name, _args in {
 }.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = _I
+    _FN[_name] = getattr(_lib, _name)
 for _name, _n in {"kda_glr_workspace_size": 3, "kda_glr_states_size": 3, "kda_glr_bwd_workspace_size": 3,
                   "kda_conv_bwd_workspace_size": 3, "kda_qk_rope_bwd_workspace_size": 4}.items():
     getattr(_lib, _name).argtypes = [_I64] * _n
@@ -355,13 +357,16 @@ _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 class _Call:
     """The checks and the stream of one call: tensors on one GPU, of a type, contiguous, of a shape."""
 
+    __slots__ = ("device", "index")
+
     def __init__(self, first, name):
         if not first.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
         self.device = first.device
+        self.index = self.device.index
 
     def token(self, t, name, dtype, shape=None, contiguous=True):
-        if t.device != self.device or t.dtype != dtype or (contiguous and not t.is_contiguous()):
+        if t.dtype is not dtype or t.device != self.device or (contiguous and not t.is_contiguous()):
             raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor on {self.device}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}")
@@ -372,12 +377,13 @@ class _Call:
 
     def run(self, what, stream, *args):
         if stream is None:
-            stream = torch.cuda.current_stream(self.device).cuda_stream
-        if torch.cuda.current_device() == self.device.index:
-            rc = getattr(_lib, what)(*args, int(stream))
+            stream = torch._C._cuda_getCurrentRawStream(self.index)
+        fn = _FN[what]
+        if torch._C._cuda_getDevice() == self.index:
+            rc = fn(*args, stream)
         else:  # a launch goes to the current device
-            with torch.cuda.device(self.device):
-                rc = getattr(_lib, what)(*args, int(stream))
+            with torch.cuda.device(self.index):
+                rc = fn(*args, stream)
         if rc != 0:
             raise KdaError(rc, what)
 

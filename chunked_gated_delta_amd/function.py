@@ -107,19 +107,24 @@ def _count(x, cu_seqlens):
     return x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
 
 
+def _glr_forward(x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens, flags, train):
+    B, T, H, K = x.shape
+    out = torch.empty_like(x)
+    final = torch.empty(_count(x, cu_seqlens), H, K, dtype=torch.float32, device=x.device)
+    states = _scratch(kda_glr_states_size(B * T, H, K), x) if train else None
+    kda_glr_fwd(x, raw_gate, out, _scratch(kda_glr_workspace_size(B * T, H, K), x), A_log, dt_bias, lower_bound,
+                initial_state, final, states, cu_seqlens, flags)
+    return out, final, states
+
+
 class _Glr(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens, flags, train):
-        B, T, H, K = x.shape
-        out = torch.empty_like(x)
-        final = torch.empty(_count(x, cu_seqlens), H, K, dtype=torch.float32, device=x.device)
-        states = _scratch(kda_glr_states_size(B * T, H, K), x) if train else None
-        kda_glr_fwd(x, raw_gate, out, _scratch(kda_glr_workspace_size(B * T, H, K), x), A_log, dt_bias, lower_bound,
-                    initial_state, final, states, cu_seqlens, flags)
-        if train:
-            ctx.save_for_backward(x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens)
-            ctx.states, ctx.lower_bound, ctx.flags = states, lower_bound, flags
-            ctx.set_materialize_grads(False)
+    def forward(ctx, x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens, flags):
+        out, final, ctx.states = _glr_forward(x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens,
+                                              flags, True)
+        ctx.save_for_backward(x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens)
+        ctx.lower_bound, ctx.flags = lower_bound, flags
+        ctx.set_materialize_grads(False)
         return out, final
 
     @staticmethod
@@ -135,7 +140,7 @@ class _Glr(torch.autograd.Function):
         kda_glr_bwd(x, raw_gate, ctx.states, d_out, dx, dg, dA, dd,
                     _scratch(kda_glr_bwd_workspace_size(B * T, H, K), x), A_log, dt_bias, ctx.lower_bound,
                     initial_state, d_final, di, cu_seqlens, ctx.flags)
-        return dx, dg, dA, dd, di, None, None, None, None
+        return dx, dg, dA, dd, di, None, None, None
 
 
 def _wants_grad(*tensors):
@@ -156,21 +161,26 @@ def kda_glr(x, raw_gate, A_log=None, dt_bias=None, *, lower_bound=-5.0, initial_
     if gate_given and (A_log is not None or dt_bias is not None):
         raise ValueError("with gate_given there is no A_log and no dt_bias")
     flags = (FLAG_GATE_GIVEN if gate_given else 0) | (FLAG_COMPLEMENT if complement else 0) | FLAG_ZERO_REST
-    return _Glr.apply(x, raw_gate, A_log, dt_bias, initial_state, float(lower_bound), cu_seqlens, flags,
-                      _wants_grad(x, raw_gate, A_log, dt_bias, initial_state))
+    args = (x, raw_gate, A_log, dt_bias, initial_state, float(lower_bound), cu_seqlens, flags)
+    if _wants_grad(x, raw_gate, A_log, dt_bias, initial_state):
+        return _Glr.apply(*args)
+    return _glr_forward(*args, False)[:2]
+
+
+def _conv_forward(x, weight, bias, initial_state, cu_seqlens, flags):
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    final = torch.empty(_count(x, cu_seqlens), weight.shape[1] - 1, x.shape[2], dtype=x.dtype, device=x.device)
+    kda_conv_fwd(x, weight, out, bias, initial_state, final, cu_seqlens, flags)
+    return out, final
 
 
 class _Conv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, initial_state, cu_seqlens, flags):
-        N, W = _count(x, cu_seqlens), weight.shape[1]
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        final = torch.empty(N, W - 1, x.shape[2], dtype=x.dtype, device=x.device)
-        kda_conv_fwd(x, weight, out, bias, initial_state, final, cu_seqlens, flags)
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
         ctx.flags = flags
         ctx.set_materialize_grads(False)
-        return out, final
+        return _conv_forward(x, weight, bias, initial_state, cu_seqlens, flags)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -196,18 +206,24 @@ def kda_short_conv(x, weight, bias=None, *, silu=True, initial_state=None, cu_se
     B = 1) or None; rows behind the last sequence come back as zeros.  The final state is the next
     call's initial state.
     """
-    return _Conv.apply(x, weight, bias, initial_state, cu_seqlens, (FLAG_SILU if silu else 0) | FLAG_ZERO_REST)
+    args = (x, weight, bias, initial_state, cu_seqlens, (FLAG_SILU if silu else 0) | FLAG_ZERO_REST)
+    return _Conv.apply(*args) if _wants_grad(x, weight, bias, initial_state) else _conv_forward(*args)
+
+
+def _qk_forward(q, k, q_weight, k_weight, positions, inv_freq, eps, flags):
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    kda_qk_rope_fwd(q, k, q_out, k_out, positions, inv_freq, eps, q_weight, k_weight, flags)
+    return q_out, k_out
 
 
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, flags):
-        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-        kda_qk_rope_fwd(q, k, q_out, k_out, positions, inv_freq, eps, q_weight, k_weight, flags)
         ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
         ctx.eps, ctx.flags = eps, flags
         ctx.set_materialize_grads(False)
-        return q_out, k_out
+        return _qk_forward(q, k, q_weight, k_weight, positions, inv_freq, eps, flags)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -241,5 +257,6 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     """
     if norm not in _NORM:
         raise ValueError(f"norm must be one of {sorted(_NORM)}")
-    return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, float(eps),
-                             _NORM[norm] | (FLAG_INTERLEAVED if interleaved else 0))
+    args = (q, k, q_weight, k_weight, positions, inv_freq, float(eps),
+            _NORM[norm] | (FLAG_INTERLEAVED if interleaved else 0))
+    return _QkNormRope.apply(*args) if _wants_grad(q, k, q_weight, k_weight) else _qk_forward(*args)
