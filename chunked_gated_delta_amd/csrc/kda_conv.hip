@@ -348,8 +348,19 @@ __global__ void __launch_bounds__(CRED) kda_conv_reduce_kernel(ConvArgs a, int W
   const int64_t c = (int64_t)(blockIdx.x / (W + 1)) * 64 + (tid & 63);
   if (j == W && !a.dbias) return;
   double s = 0.0;
-  if (c < a.C)
-    for (int64_t t = tid >> 6; t < a.ntiles; t += CRED / 64) s += a.part[(t * (W + 1) + j) * a.C + c];
+  if (c < a.C) {
+    constexpr int U = 8;  // rows asked for at once
+    for (int64_t t0 = tid >> 6; t0 < a.ntiles; t0 += U * (CRED / 64)) {
+      float p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * (CRED / 64);
+        p[u] = t < a.ntiles ? a.part[(t * (W + 1) + j) * a.C + c] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += p[u];
+    }
+  }
   sm[tid] = s;
   __syncthreads();
   if (tid < 64 && c < a.C) {

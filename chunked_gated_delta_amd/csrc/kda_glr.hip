@@ -332,47 +332,59 @@ __device__ __forceinline__ void join_runs(const GlrArgs& a, Tile& t, Maps& maps,
   }
 }
 
-constexpr int ASKS = 64;  // the thread that asks for tickets: of another wave than the one that makes marks
+constexpr int ASKS = 64;  // the thread that asks for tickets (wave 0 makes the marks)
 
 // Tiles are handed out in order by counters.  One counter serves a tile each
-// 13 ns at best (measured: every pass ran at that pace, whatever it computed),
-// less than memory allows, so the columns are split into up to eight sets of
-// neighbours, each with its counter.  A workgroup takes from its own set first,
-// and from the others when that is used up.  Whatever it waits for was drawn
-// before its own ticket, by a workgroup that works on its tickets in the order
-// it drew them: so no two can wait for each other.
+// 13 ns at best (measured), which is near what memory allows, so columns are
+// split into equal sets of neighbours where their number is even (two, four or
+// eight), each with its counter and its share of the workgroups.  A tile waits
+// only for tiles of its own column with lower tickets, which running workgroups
+// drew and work on in the order they drew them: the lowest unfinished ticket is
+// always being worked on.
 constexpr int SETS = 8;
 constexpr int TICKET_LINE = 64;  // ints: counters on lines of their own
 struct Drawer {
-  int set, left;  // the set drawn from, sets not used up
-  int first, n;   // its columns
-  double per;     // 1 / n
-  __device__ __forceinline__ Drawer(const GlrArgs& a) : set(blockIdx.x % a.sets), left(a.sets) { enter(a); }
-  __device__ __forceinline__ void enter(const GlrArgs& a) {
-    first = (int)((int64_t)a.nblk * set / a.sets);
-    n = (int)((int64_t)a.nblk * (set + 1) / a.sets) - first;
+  int* counter;
+  int first, n;  // columns of the set
+  double per;    // 1 / n
+  __device__ __forceinline__ Drawer(const GlrArgs& a) {
+    const int set = blockIdx.x % a.sets;
+    counter = a.tickets + set * TICKET_LINE;
+    n = a.nblk / a.sets;
+    first = n * set;
     per = 1.0 / n;
   }
   // A ticket is asked for by ask() and turned into a tile (x: its number in the
-  // pass's order, ntiles for none; y: its column block) by answer(), later: the
-  // round trip lies between.  By one thread.
-  __device__ __forceinline__ int ask(const GlrArgs& a) const {
-    return __hip_atomic_fetch_add(a.tickets + set * TICKET_LINE, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // pass's order, at least ntiles for none; y: its column block) by answer(),
+  // later: the round trip lies between.
+  __device__ __forceinline__ int ask() const {
+    return __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __device__ __forceinline__ int2 answer(const GlrArgs& a, int t) {
-    while (left > 0) {
-      int q = (int)(t * per);  // t / n, off by one at most
-      q -= q * n > t;
-      q += (q + 1) * n <= t;
-      if (q < a.ntiles) return make_int2(q, first + t - q * n);
-      if (--left == 0) break;
-      set = set + 1 < a.sets ? set + 1 : 0;
-      enter(a);
-      t = ask(a);
-    }
-    return make_int2(a.ntiles, 0);
+  __device__ __forceinline__ int2 answer(int t) const {
+    int q = (int)(t * per);  // t / n, off by one at most
+    q -= q * n > t;
+    q += (q + 1) * n <= t;
+    return make_int2(q, first + t - q * n);
   }
 };
+
+// The first N tiles and the ticket after them, asked for at once, by one thread.
+// With one tile a column nothing waits for anything: there is a workgroup for
+// every column, and no counter.
+template <int N>
+__device__ __forceinline__ int draw_first(const GlrArgs& a, const Drawer& d, int2* slot) {
+  if (a.ntiles == 1) {
+    for (int i = 0; i < N; ++i) slot[i] = make_int2(i, blockIdx.x);
+    return INT_MAX / 2;
+  }
+  int t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = d.ask();
+  const int asked = d.ask();
+#pragma unroll
+  for (int i = 0; i < N; ++i) slot[i] = d.answer(t[i]);
+  return asked;
+}
 
 // Clears the fault word, the counters and the words that other workgroups wait
 // for (a kernel rather than a memset, so that a captured graph
@@ -418,10 +430,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
   const int64_t rows = axis_rows(a.ax);
   Drawer drawer(a);
   int asked = 0;
-  if (tid == ASKS) {
-    for (int i = 0; i < 4; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
-    asked = drawer.ask(a);
-  }
+  if (tid == ASKS) asked = draw_first<4>(a, drawer, slot);
   __syncthreads();  // tickets
   if (tid >= GD) {
     // everything else waits for this wave: its instructions go first
@@ -545,8 +554,8 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       mark(slot[(i + 2) & 7], i + 2);
       map(slot[(i + 1) & 7], i + 1, w, then);
       if (tid == ASKS) {  // the ticket that was asked for a tile ago
-        slot[(i + 4) & 7] = drawer.answer(a, asked);
-        asked = drawer.ask(a);
+        slot[(i + 4) & 7] = drawer.answer(asked);
+        asked = drawer.ask();
       }
       fetch(slot[(i + 3) & 7], w);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
@@ -593,10 +602,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
   const int64_t rows = axis_rows(a.ax);
   Drawer drawer(a);
   int asked = 0;
-  if (tid == ASKS) {
-    for (int i = 0; i < 3; ++i) slot[i] = drawer.answer(a, drawer.ask(a));
-    asked = drawer.ask(a);
-  }
+  if (tid == ASKS) asked = draw_first<3>(a, drawer, slot);
   __syncthreads();  // tickets
   if (tid >= GD) {
     __builtin_amdgcn_s_setprio(3);
@@ -825,8 +831,8 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       mark(slot[(i + 2) & 7], i + 2);
       map(slot[(i + 1) & 7], i + 1, then);
       if (tid == ASKS) {
-        slot[(i + 3) & 7] = drawer.answer(a, asked);
-        asked = drawer.ask(a);
+        slot[(i + 3) & 7] = drawer.answer(asked);
+        asked = drawer.ask();
       }
       __syncthreads();  // what enters tile i, the maps of tile i + 1
       finish(item, i, now);
@@ -871,12 +877,22 @@ __global__ void __launch_bounds__(GRED) kda_glr_reduce_kernel(GlrArgs a) {
   for (int k0 = 0; k0 < a.K; k0 += 64) {
     const int k = k0 + (tid & 63), row = tid >> 6;  // 16 rows of 64 channels
     double d = 0.0, z = 0.0;
-    if (k < a.K)
-      for (int t = row; t < a.ntiles; t += GRED / 64) {
-        const float2 p = a.part[(int64_t)t * a.C + (int64_t)h * a.K + k];
-        d += p.x;
-        z += p.y;
+    if (k < a.K) {
+      constexpr int U = 8;  // rows asked for at once
+      for (int t0 = row; t0 < a.ntiles; t0 += U * (GRED / 64)) {
+        float2 p[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int t = t0 + u * (GRED / 64);
+          p[u] = t < a.ntiles ? a.part[(int64_t)t * a.C + (int64_t)h * a.K + k] : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          d += p[u].x;
+          z += p[u].y;
+        }
       }
+    }
     sd[tid] = d;
     sz[tid] = z;
     __syncthreads();
@@ -969,7 +985,7 @@ kda_status_t glr_prepare(GlrArgs& a, const float* A_log, const float* dt_bias, f
   a.K = (int)K;
   a.nblk = (int)nblk;
   a.ntiles = (int)tiles;
-  a.sets = nblk < SETS ? (int)nblk : SETS;
+  a.sets = nblk % 8 == 0 ? 8 : nblk % 4 == 0 ? 4 : nblk % 2 == 0 ? 2 : 1;
   a.lb = lower_bound;
   a.zero_rest = flags & FLAG_ZERO_REST ? 1 : 0;
   return KDA_SUCCESS;
@@ -987,7 +1003,7 @@ kda_status_t by_variant(int dtype, unsigned flags, P... p) {
 
 // Workgroups of a pass: as many as run at once, one on a CU.
 int64_t pass_grid(const GlrArgs& a) {
-  const int64_t items = (int64_t)a.ntiles * a.nblk, most = 256;
+  const int64_t items = (int64_t)a.ntiles * a.nblk, most = a.ntiles == 1 ? a.nblk : 256;  // (draw_first)
   return items < 1 ? 1 : items < most ? items : most;
 }
 kda_status_t clear(const GlrArgs& a, hipStream_t st) {

@@ -72,15 +72,12 @@ __device__ __forceinline__ Place place(const QkArgs& a, int slot) {
   return p;
 }
 
+// A lane's 8 channels of a row, as loaded: rows that wait for their turn take
+// half the registers in bf16.
 template <typename T>
-__device__ __forceinline__ void load_row(const T* row, const Place& p, float (&v)[8]) {
-  float f[4];
-  widen4(*reinterpret_cast<const raw4<T>*>(row + p.c0), f);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = f[j];
-  widen4(*reinterpret_cast<const raw4<T>*>(row + p.c1), f);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[4 + j] = f[j];
+__device__ __forceinline__ void load_row(const T* row, const Place& p, RawN<T, 8>& r) {
+  r.v[0] = *reinterpret_cast<const raw4<T>*>(row + p.c0);
+  r.v[1] = *reinterpret_cast<const raw4<T>*>(row + p.c1);
 }
 template <typename T>
 __device__ __forceinline__ void store_row(T* row, const Place& p, const float (&v)[8]) {
@@ -148,16 +145,15 @@ __global__ void __launch_bounds__(QT) kda_qk_fwd_kernel(QkArgs a) {
   if (item >= a.items) return;  // whole groups leave; sums stay within a group
   const int64_t t = item / a.chunks;
   const int h0 = (int)(item % a.chunks) * HC, H = a.Hq + a.Hk;
-  float v[HC][8];
+  RawN<T, 8> raw[HC];
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
     const int h = h0 + i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    zero_raw(raw[i]);
     if (p.in && h < H) {
       const T* row = h < a.Hq ? static_cast<const T*>(a.q) + t * a.qs + h * a.qh
                               : static_cast<const T*>(a.k) + t * a.ks + (h - a.Hq) * a.kh;
-      load_row(row, p, v[i]);
+      load_row(row, p, raw[i]);
     }
   }
   float s[4], c[4];
@@ -171,23 +167,24 @@ __global__ void __launch_bounds__(QT) kda_qk_fwd_kernel(QkArgs a) {
   for (int i = 0; i < HC; ++i) {
     const int h = h0 + i;
     if (h >= H) break;
-    float r = 1.0f;
+    float v[8], r = 1.0f;
+    widen(raw[i], v);
     if (a.norm) {
       float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+      for (int j = 0; j < 8; ++j) ss += v[j] * v[j];
       r = __builtin_amdgcn_rsqf(group_sum(ss, a.lanes) * a.inv_count + a.eps);
     }
     const float* wp = h < a.Hq ? a.qw : a.kw;
     float w[8];
     load_weight(wp, p, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * w[j];
-    if (p.turned) turn(v[i], s, c, INTER, 1.0f);
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
+    if (p.turned) turn(v, s, c, INTER, 1.0f);
     if (p.in) {
       T* row = h < a.Hq ? static_cast<T*>(a.q_out) + t * a.qos + h * a.qoh
                         : static_cast<T*>(a.k_out) + t * a.kos + (h - a.Hq) * a.koh;
-      store_row(row, p, v[i]);
+      store_row(row, p, v);
     }
   }
 }
@@ -195,7 +192,7 @@ __global__ void __launch_bounds__(QT) kda_qk_fwd_kernel(QkArgs a) {
 // A persistent grid, so that the weights' sums stay in registers: every thread
 // strides over items with the same slot.
 template <typename T, int HC, bool INTER>
-__global__ void __launch_bounds__(QT) kda_qk_bwd_kernel(QkArgs a) {
+__global__ void __launch_bounds__(QT, 4) kda_qk_bwd_kernel(QkArgs a) {
   __shared__ float sm[QT][8];
   const int slot = threadIdx.x & (a.lanes - 1), per = QT / a.lanes;
   const Place p = place(a, slot);
@@ -212,18 +209,18 @@ __global__ void __launch_bounds__(QT) kda_qk_bwd_kernel(QkArgs a) {
        item += (int64_t)gridDim.x * per) {
     const int64_t t = item / a.chunks;
     const int h0 = (int)(item % a.chunks) * HC;
-    float v[HC][8], d[HC][8];
+    RawN<T, 8> vr[HC], dr[HC];
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
       const int h = h0 + i;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = d[i][j] = 0.f;
+      zero_raw(vr[i]);
+      zero_raw(dr[i]);
       if (p.in && h < H) {
         const bool isq = h < a.Hq;
         load_row(isq ? static_cast<const T*>(a.q) + t * a.qs + h * a.qh
-                     : static_cast<const T*>(a.k) + t * a.ks + (h - a.Hq) * a.kh, p, v[i]);
+                     : static_cast<const T*>(a.k) + t * a.ks + (h - a.Hq) * a.kh, p, vr[i]);
         load_row(isq ? static_cast<const T*>(a.dq_out) + (t * a.Hq + h) * a.D
-                     : static_cast<const T*>(a.dk_out) + (t * a.Hk + h - a.Hq) * a.D, p, d[i]);
+                     : static_cast<const T*>(a.dk_out) + (t * a.Hk + h - a.Hq) * a.D, p, dr[i]);
       }
     }
     float s[4], c[4];
@@ -233,31 +230,34 @@ __global__ void __launch_bounds__(QT) kda_qk_bwd_kernel(QkArgs a) {
       const int h = h0 + i;
       if (h >= H) break;
       const bool isq = h < a.Hq;
-      if (p.turned) turn(d[i], s, c, INTER, -1.0f);
+      float v[8], d[8];
+      widen(vr[i], v);
+      widen(dr[i], d);
+      if (p.turned) turn(d, s, c, INTER, -1.0f);
       float r = 1.0f;
       if (a.norm) {
         float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+        for (int j = 0; j < 8; ++j) ss += v[j] * v[j];
         r = __builtin_amdgcn_rsqf(group_sum(ss, a.lanes) * a.inv_count + a.eps);
       }
       float dot = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[i][j] *= r;  // n
-        if (isq) sq[j] += d[i][j] * v[i][j];
-        else sk[j] += d[i][j] * v[i][j];
-        d[i][j] *= isq ? qw[j] : kw[j];
-        dot += d[i][j] * v[i][j];
+        v[j] *= r;  // n
+        if (isq) sq[j] += d[j] * v[j];
+        else sk[j] += d[j] * v[j];
+        d[j] *= isq ? qw[j] : kw[j];
+        dot += d[j] * v[j];
       }
       if (a.norm) {
         dot = group_sum(dot, a.lanes) * a.inv_count;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] = r * (d[i][j] - v[i][j] * dot);
+        for (int j = 0; j < 8; ++j) d[j] = r * (d[j] - v[j] * dot);
       }
       if (p.in)
         store_row(isq ? static_cast<T*>(a.q_out) + (t * a.Hq + h) * a.D
-                      : static_cast<T*>(a.k_out) + (t * a.Hk + h - a.Hq) * a.D, p, d[i]);
+                      : static_cast<T*>(a.k_out) + (t * a.Hk + h - a.Hq) * a.D, p, d);
     }
   }
   if (!a.part) return;
@@ -286,8 +286,19 @@ __global__ void __launch_bounds__(QRED) kda_qk_reduce_kernel(QkArgs a, int block
   float* to = which ? a.dkw : a.dqw;
   if (!to) return;
   double s = 0.0;
-  if (c < a.D)
-    for (int b = tid >> 6; b < blocks; b += QRED / 64) s += a.part[((int64_t)b * 2 + which) * a.D + c];
+  if (c < a.D) {
+    constexpr int U = 8;  // rows asked for at once
+    for (int b0 = tid >> 6; b0 < blocks; b0 += U * (QRED / 64)) {
+      float p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + u * (QRED / 64);
+        p[u] = b < blocks ? a.part[((int64_t)b * 2 + which) * a.D + c] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += p[u];
+    }
+  }
   sm[tid] = s;
   __syncthreads();
   if (tid < 64 && c < a.D) {
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(QRED) kda_qk_reduce_kernel(QkArgs a, int block
 }
 
 constexpr int HC = 4;
-constexpr int64_t kQkBlocks = 2048;  // of the backward's grid
+constexpr int64_t kQkBlocks = 1024;  // of the backward's grid: four workgroups a CU
 
 bool strides_ok(int64_t tokens, int64_t H, int64_t D, int64_t ts, int64_t hs) {
   return ts >= 0 && hs >= 0 && ts % 4 == 0 && hs % 4 == 0 && fits(tokens, ts, kMaxElements) && fits(H, hs, kMaxElements) &&
