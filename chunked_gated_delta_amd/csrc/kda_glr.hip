@@ -5,28 +5,43 @@
 //
 // A run of tokens maps the state that enters it to h -> A h + B (A the product
 // of its decays, B its result from zero), and such maps compose.  The packed
-// token axis is cut into tiles of 64 rows by 128 channels, whatever the
-// sequences: a tile that holds the first row of a sequence has a map that does
-// not depend on the entering state (it is reset: the composition selects, it
-// does not multiply by zero, so that a sequence's NaN or infinity stays in it).
-// A tile is 512 threads: 32 lanes of 4 channels by 16 runs of 4 rows, each run
-// in one thread's registers, the runs joined through LDS in order.
+// token axis is cut into tiles of rows by 64 channels, whatever the sequences: a
+// tile that holds the first row of a sequence has a map that does not depend on
+// the entering state (it is reset: the composition selects, it does not multiply
+// by zero, so that a sequence's NaN or infinity stays in it).  A tile is 512
+// threads, one workgroup a CU: seven waves hold 28 runs of 8 rows (bf16; 4 in
+// fp32 and in the backward) in registers, 16 lanes of 4 channels each, and one
+// wave joins the runs, a lane a channel.
 //
 // One pass over the data: a workgroup takes the tiles in order from a counter,
-// loads its tile once, publishes the tile's map, finds the state that enters
-// it and writes the outputs from registers.  To find that state, it looks back
-// over the flags of up to 64 tiles before it for the nearest one whose leaving
-// state is known, and applies the maps of the tiles in between, in order.  The
-// leaving state of a tile is always its map applied to its entering state, so
-// the result has the same bits however far back the search ends.  A tile waits
-// only for tiles that running workgroups took before it; the wait is bounded
-// all the same, and one that gives up sets the workspace's fault word.
+// loads its tile once, publishes the tile's map, finds the state that enters it
+// and writes the outputs from registers.  To find that state it looks for the
+// nearest of the 32 tiles before it whose entering state is known and applies
+// the maps of the tiles in between, in order.  The leaving state of a tile is
+// always its map applied to its entering state, so the result has the same bits
+// however far back the search ends.  A tile waits only for tiles that running
+// workgroups took before it; the wait is bounded all the same, and one that
+// gives up sets the workspace's fault word.
+//
+// What bounds it: memory, where there are many columns.  At 32768 rows x 12288
+// channels of bf16 the pass takes 0.48 ms, 5.0 TB/s of its 6 bytes an element (a
+// copy reaches 5.2 on the same card); reading the inputs twice, with the states
+// folded between two launches, took 1.20 ms.  With few columns every column has
+// more tiles in flight than its entering states can travel through, at two or
+// three round trips of about 1 us a hop: 262144 x 1024 takes 0.42 ms (3.8 TB/s).
+// Measured on the way there: 64-row tiles with two workgroups a CU 0.72 ms; all
+// tickets from one counter 13 ns a tile, whatever it did; the joining wave at
+// default priority 0.65 ms; rows that ask for marks one by one 0.57 ms.
 //
 // Backward, with dh_t = d_out_t + a_{t+1} dh_{t+1} (d_final joins at the last
 // row) and e_t = a_t dh_t, the gradient that row t hands to the row before:
 //     dx_t = b_t dh_t,   dg_t = a_t dh_t (h_{t-1} [- x_t if b = 1 - a])
 // the same pass runs over e from the right; h_{t-1} is recomputed from the
-// states entering every tile, which the forward leaves.
+// states entering every 112 rows, which the forward leaves.  At 69141 x 4096 it
+// takes 0.85 ms, 3.3 TB/s of its 10 bytes an element: per 112-row tile the seven
+// waves need about 9000 cycles of arithmetic (three exponentials and two
+// reciprocals an element) and the joining wave as long for two sets of runs and
+// its waits.
 //
 // All arithmetic is fp32.
 
@@ -80,6 +95,7 @@ struct GlrArgs {
   int sets;
   unsigned* faults;
   float2* part;   // [tiles][C] sums over the tile of d_raw and of dz z
+  double* zsum;   // [C] sums of dz z
   float* dA_log;
   float* d_dt_bias;
   Axis ax;
@@ -215,8 +231,8 @@ __device__ __forceinline__ void post(W* p, W v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Rounds before a wait gives up (about a second: each is a round trip to memory).
-constexpr int kPolls = 1 << 19;
+// Rounds before a wait gives up (more than a second: each is a round trip to memory).
+constexpr int kPolls = 1 << 21;
 
 // What enters tile k (tiles counted in the pass's order) at channel c: its own
 // word, or the word of a tile up to REACH before it with the maps in between
@@ -868,48 +884,50 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
 }
 
 // Sums of the tiles' partial sums, in a fixed order and in fp64 (a long
-// sequence has thousands of them): d_dt_bias per channel, dA_log per head.
-constexpr int GRED = 1024;
+// sequence has thousands of them): d_dt_bias per channel, and per channel what
+// dA_log adds up per head.  A workgroup has 16 channels, a line of each row, by
+// 64 rows at a time: few channels still make enough workgroups to be done in a
+// few round trips (64 channels by 16 rows took 37 us at 618 tiles of 4096
+// channels).
+constexpr int GRED = 1024, RC = 16, RR = GRED / RC;
 __global__ void __launch_bounds__(GRED) kda_glr_reduce_kernel(GlrArgs a) {
-  __shared__ double sd[GRED], sz[GRED];
-  const int tid = threadIdx.x, h = blockIdx.x;
-  double head = 0.0;
-  for (int k0 = 0; k0 < a.K; k0 += 64) {
-    const int k = k0 + (tid & 63), row = tid >> 6;  // 16 rows of 64 channels
-    double d = 0.0, z = 0.0;
-    if (k < a.K) {
-      constexpr int U = 8;  // rows asked for at once
-      for (int t0 = row; t0 < a.ntiles; t0 += U * (GRED / 64)) {
-        float2 p[U];
+  __shared__ double sd[RR][RC], sz[RR][RC];
+  const int ch = threadIdx.x % RC, row = threadIdx.x / RC;
+  const int64_t c = (int64_t)blockIdx.x * RC + ch;
+  double d = 0.0, z = 0.0;
+  if (c < a.C) {
+    constexpr int U = 4;  // rows asked for at once
+    for (int t0 = row; t0 < a.ntiles; t0 += U * RR) {
+      float2 p[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = t0 + u * (GRED / 64);
-          p[u] = t < a.ntiles ? a.part[(int64_t)t * a.C + (int64_t)h * a.K + k] : make_float2(0.f, 0.f);
-        }
+      for (int u = 0; u < U; ++u)
+        p[u] = t0 + u * RR < a.ntiles ? a.part[(int64_t)(t0 + u * RR) * a.C + c] : make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          d += p[u].x;
-          z += p[u].y;
-        }
+      for (int u = 0; u < U; ++u) {
+        d += p[u].x;
+        z += p[u].y;
       }
     }
-    sd[tid] = d;
-    sz[tid] = z;
+  }
+  sd[row][ch] = d;
+  sz[row][ch] = z;
+  for (int r = RR / 2; r >= 1; r >>= 1) {
     __syncthreads();
-    if (tid < 64 && k < a.K) {
-      for (int r = 1; r < GRED / 64; ++r) {
-        d += sd[r * 64 + tid];
-        z += sz[r * 64 + tid];
-      }
-      a.d_dt_bias[(int64_t)h * a.K + k] = (float)d;
-      head += z;
+    if (row < r) {
+      sd[row][ch] += sd[row + r][ch];
+      sz[row][ch] += sz[row + r][ch];
     }
-    __syncthreads();
   }
-  if (tid < 64) {
-    for (int m = 32; m >= 1; m >>= 1) head += __shfl_xor(head, m);
-    if (tid == 0) a.dA_log[h] = (float)head;
+  if (row == 0 && c < a.C) {
+    a.d_dt_bias[c] = (float)sd[0][ch];
+    a.zsum[c] = sz[0][ch];
   }
+}
+__global__ void __launch_bounds__(64) kda_glr_head_kernel(GlrArgs a) {
+  double z = 0.0;
+  for (int k = threadIdx.x; k < a.K; k += 64) z += a.zsum[(int64_t)blockIdx.x * a.K + k];
+  for (int m = 32; m >= 1; m >>= 1) z += __shfl_xor(z, m);
+  if (threadIdx.x == 0) a.dA_log[blockIdx.x] = (float)z;
 }
 
 // One thread per 4 channels of a sequence, its T tokens in order.
@@ -941,7 +959,7 @@ __global__ void __launch_bounds__(GST) kda_glr_step_kernel(GlrArgs a) {
 // The fault word comes where kda_workspace_faults looks for it, then what is
 // cleared: the counters and the words that tiles hand each other.
 struct GlrLayout {
-  size_t faults, tickets, enter, maps, part, total;
+  size_t faults, tickets, enter, maps, part, zsum, total;
 };
 GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
   const size_t tiles = (size_t)((T_total + BL - 1) / BL);  // of the shorter kind
@@ -952,7 +970,8 @@ GlrLayout glr_layout(int64_t T_total, int64_t C, bool bwd) {
   l.enter = l.tickets + SETS * TICKET_LINE * sizeof(int);
   l.maps = l.enter + align256(w * sizeof(uint64_t));
   l.part = l.maps + align256(w * sizeof(uint64_t));
-  l.total = l.part + (bwd ? align256(w * sizeof(float2)) : 0);
+  l.zsum = l.part + (bwd ? align256(w * sizeof(float2)) : 0);
+  l.total = l.zsum + (bwd ? align256((size_t)C * sizeof(double)) : 0);
   return l;
 }
 
@@ -1025,7 +1044,8 @@ struct RunBwd {
     kda_status_t s = clear(a, st);
     if (s == KDA_SUCCESS) s = launch(&kda_glr_bwd_kernel<T, GIVEN, COMPL>, pass_grid(a), GT, st, "glr backward", a);
     if (s != KDA_SUCCESS || GIVEN) return s;
-    return launch(&kda_glr_reduce_kernel, a.H, GRED, st, "glr reduce", a);
+    s = launch(&kda_glr_reduce_kernel, (a.C + RC - 1) / RC, GRED, st, "glr reduce", a);
+    return s != KDA_SUCCESS ? s : launch(&kda_glr_head_kernel, a.H, 64, st, "glr heads", a);
   }
 };
 template <typename T, bool GIVEN, bool COMPL>
@@ -1116,6 +1136,7 @@ kda_status_t kda_glr_bwd(const void* x, const void* raw_gate, const float* state
   carve(a, ws, l);
   a.states = states;
   a.part = reinterpret_cast<float2*>(ws + l.part);
+  a.zsum = reinterpret_cast<double*>(ws + l.zsum);
   return by_variant<RunBwd>(dtype, flags, a, reinterpret_cast<hipStream_t>(stream));
 }
 

@@ -346,7 +346,7 @@ kda_status_t kda_bwd_ex(const void* q, const void* k, const void* v, const void*
 
 /*
  * Faults the kernels of a kda_fwd / kda_fwd_ex / kda_shard_affine / kda_bwd /
- * kda_bwd_ex call detect on the device, where no status can be returned.
+ * kda_bwd_ex / kda_glr_fwd / kda_glr_bwd call detect on the device, where no status can be returned.
  * Each such call clears the fault word of its workspace when it starts and
  * ORs these bits into it:
  *   KDA_FAULT_WAIT_TIMEOUT  a bounded wait between waves or workgroups gave
@@ -464,9 +464,12 @@ typedef enum {
  *                 following kda_glr_bwd with the same inputs; NULL where none
  *                 follows.  (The states entering every tile of rows; the
  *                 layout is the library's own.)
- *   K             a multiple of 4; H, N, B >= 1, T >= 0
+ *   K             a multiple of 4, H * K at most 2^21; H, N, B >= 1, T >= 0
  *   flags         KDA_FLAG_GATE_GIVEN, KDA_FLAG_COMPLEMENT, KDA_FLAG_ZERO_REST
- * A NaN or infinity stays within its own sequence and channel.
+ * A NaN or infinity stays within its own sequence and channel.  Workgroups of
+ * the call hand states to each other; a bounded wait that gives up sets
+ * KDA_FAULT_WAIT_TIMEOUT in the workspace's fault word (kda_workspace_faults
+ * reads it after kda_glr_fwd and kda_glr_bwd too).
  */
 size_t kda_glr_workspace_size(int64_t T_total, int64_t H, int64_t K);
 size_t kda_glr_states_size(int64_t T_total, int64_t H, int64_t K);

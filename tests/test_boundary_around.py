@@ -66,7 +66,7 @@ REFUSED = [
     *[(f, o, INVALID) for f in (glr_fwd, glr_bwd) for o in
       (dict(B=0), dict(T=-1), dict(H=0), dict(K=0), dict(N=0), dict(N=2), dict(B=2, N=2, cu=P), dict(flags=2),
        dict(flags=4096), dict(T=1 << 45), dict(B=1 << 40, N=1 << 40, T=1 << 40), dict(H=1 << 40), dict(T=1 << 31, cu=P),
-       dict(x=P + 2), dict(dt=P + 4), dict(init=P + 4), dict(states=P + 8))],
+       dict(H=1 << 15, K=128), dict(x=P + 2), dict(dt=P + 4), dict(init=P + 4), dict(states=P + 8))],
     *[(f, o, UNSUPPORTED) for f in (glr_fwd, glr_bwd, glr_step) for o in
       (dict(K=6), dict(ty=2), dict(ty=-1), dict(lb=-5.5), dict(lb=0.5), dict(lb=NAN))],
     *[(f, o, WORKSPACE) for f in (glr_fwd, glr_bwd) for o in (dict(ws=None), dict(size=256))],
@@ -76,7 +76,7 @@ REFUSED = [
     *[(conv_step, {f: None}, INVALID) for f in ("x", "w", "out")],
     *[(f, o, INVALID) for f in (conv_fwd, conv_bwd) for o in
       (dict(B=0), dict(T=-1), dict(C=0), dict(N=0), dict(N=2), dict(B=2, N=2, cu=P), dict(flags=128), dict(xs=8),
-       dict(xs=18), dict(x=P + 2), dict(init=P + 2), dict(T=1 << 50), dict(T=1 << 31, cu=P))],
+       dict(xs=18), dict(x=P + 2), dict(init=P + 2), dict(w=P + 8), dict(b=P + 4), dict(T=1 << 50), dict(T=1 << 31, cu=P))],
     *[(f, o, UNSUPPORTED) for f in (conv_fwd, conv_bwd, conv_step) for o in
       (dict(C=12), dict(W=5), dict(W=1), dict(ty=7))],
     (conv_bwd, dict(ws=None), WORKSPACE), (conv_bwd, dict(size=16), WORKSPACE), (conv_step, dict(flags=2048), INVALID),
