@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(CT) kda_conv_bwd_kernel(ConvArgs a) {
 }
 
 // dw [C][W] and dbias [C] from the tiles' sums, in a fixed order and in fp64: a
-// workgroup has one tap of 16 channels by 64 rows at a time.
-constexpr int CRED = 1024, RC = 16, RR = CRED / RC;
+// workgroup has one tap of 32 channels, a line of each row, by 32 rows at a time.
+constexpr int CRED = 1024, RC = 32, RR = CRED / RC;
 __global__ void __launch_bounds__(CRED) kda_conv_reduce_kernel(ConvArgs a, int W) {
   __shared__ double sm[RR][RC];
   const int ch = threadIdx.x % RC, row = threadIdx.x / RC;
