@@ -16,6 +16,7 @@ importing this module fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 # torch first: its bundled HIP runtime carries the same SONAME
@@ -357,17 +358,16 @@ _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 class _Call:
     """The checks and the stream of one call: tensors on one GPU, of a type, contiguous, of a shape."""
 
-    __slots__ = ("device", "index")
+    __slots__ = ("index",)
 
     def __init__(self, first, name):
-        if not first.is_cuda:
+        self.index = first.get_device()
+        if self.index < 0:
             raise ValueError(f"{name} must be a device tensor")
-        self.device = first.device
-        self.index = self.device.index
 
     def token(self, t, name, dtype, shape=None, contiguous=True):
-        if t.dtype is not dtype or t.device != self.device or (contiguous and not t.is_contiguous()):
-            raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor on {self.device}")
+        if t.dtype is not dtype or t.get_device() != self.index or (contiguous and not t.is_contiguous()):
+            raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor on cuda:{self.index}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}")
         return t.data_ptr()
@@ -401,9 +401,9 @@ def _sequences(cu_seqlens, c, B):
 
 
 def _bytes(c, workspace):
-    if workspace.device != c.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {c.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != c.index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{c.index}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def kda_glr_workspace_size(T: int, H: int, K: int) -> int:
@@ -492,13 +492,12 @@ def kda_glr_step(x, raw_gate, out, A_log, dt_bias, lower_bound, initial_state=No
 def _row_stride(t, name):
     """Elements between tokens of a [B, T, ...] tensor whose rows lie evenly: a slice of a wider one."""
     B, T = t.shape[:2]
-    row = 1
-    for n in t.shape[2:]:
-        row *= n
-    s = t.stride(1) if T > 1 else t.stride(0) if B > 1 else row
-    if B > 1 and T > 1 and t.stride(0) != T * s:
-        raise ValueError(f"{name}: the tokens of all sequences must lie evenly apart")
-    return s
+    st = t.stride()
+    if T > 1:
+        if B > 1 and st[0] != T * st[1]:
+            raise ValueError(f"{name}: the tokens of all sequences must lie evenly apart")
+        return st[1]
+    return st[0] if B > 1 else math.prod(t.shape[2:])
 
 
 def _conv(x, weight, bias, flags):
