@@ -129,15 +129,18 @@ __device__ __forceinline__ int64_t axis_div(const Axis& ax, int64_t t) {
   n += (n + 1) * ax.T <= t;
   return n;
 }
-// Rows that belong to sequences.  Held to the array, and the first offset to 0,
-// so that offsets that break the contract cannot lead outside the arrays.
+// Rows that belong to sequences.  Held to the array, the first offset to 0 and
+// every other to 0 or more, so that offsets that break the contract cannot lead
+// outside the arrays.
 __device__ __forceinline__ int64_t axis_rows(const Axis& ax) {
   if (!ax.cu) return ax.total;
   const int64_t r = ax.cu[ax.N];
   return r < 0 ? 0 : r < ax.total ? r : ax.total;
 }
 __device__ __forceinline__ int64_t axis_start(const Axis& ax, int64_t n) {
-  return ax.cu ? (n > 0 ? (int64_t)ax.cu[n] : 0) : n * ax.T;
+  if (!ax.cu) return n * ax.T;
+  const int32_t s = n > 0 ? ax.cu[n] : 0;
+  return s > 0 ? s : 0;
 }
 
 // Smallest n in [0, N] with start(n) >= t (N + 1 if there is none), found by a

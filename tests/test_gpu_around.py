@@ -744,3 +744,43 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for s, w in zip((a, b), want):
             assert all(torch.equal(t, w[n]) for n, t in s[2].items())
+
+
+@pytest.mark.parametrize("cu", [[0, -5, 40], [0, 30, 10, 40], [0, 12, 100], [7, 20, 40], [0, -1, -2], [40, 0, 0]])
+def test_offsets_that_break_the_contract_stay_inside(cu):
+    """Their results are not specified, but rows in front of and behind the arrays are neither used nor written."""
+    T, C, W, pad, r = 40, 64, 4, 8, Rand(60)
+    N = len(cu) - 1
+
+    def framed(t, fill=float("nan")):
+        whole = torch.full((t.shape[0] + 2 * pad, *t.shape[1:]), fill, dtype=t.dtype, device=DEV)
+        whole[pad:-pad] = t.to(DEV)
+        return whole, whole[pad:-pad]
+
+    x, g, d_out = (framed(r(T, C, dtype=torch.bfloat16))[1] for _ in range(3))
+    outs = {n: framed(torch.zeros(T, C, dtype=torch.bfloat16), 7.0) for n in ("h", "dx", "dg", "y", "dy")}
+    states = {n: framed(torch.zeros(N, C), 7.0) for n in ("fin", "di")}
+    rows = {n: framed(torch.zeros(N, W - 1, C, dtype=torch.bfloat16), 7.0) for n in ("cf", "cd")}
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    al, dt, w, init = dev(r(1)), dev(r(1, C)), dev(r(C, W)), dev(r(N, W - 1, C, dtype=torch.bfloat16))
+    four, o = lambda t: t.view(1, T, 1, C), lambda n: outs[n][1]  # noqa: E731
+    ws = torch.empty(max(kda.kda_glr_bwd_workspace_size(T, 1, C), kda.kda_conv_bwd_workspace_size(T, C, W)),
+                     dtype=torch.uint8, device=DEV)
+    kept = torch.empty(kda.kda_glr_states_size(T, 1, C), dtype=torch.uint8, device=DEV)
+    dA, dd, dw = torch.empty(1, device=DEV), torch.empty(1, C, device=DEV), torch.empty(C, W, device=DEV)
+    say("glr", cu.tolist())
+    kda.kda_glr_fwd(four(x), four(g), four(o("h")), ws, al, dt, -5.0, None, states["fin"][1].view(N, 1, C), kept, cu)
+    torch.cuda.synchronize()
+    assert kda.kda_workspace_faults(ws) == 0
+    kda.kda_glr_bwd(four(x), four(g), kept, four(d_out), four(o("dx")), four(o("dg")), dA, dd, ws, al, dt, -5.0, None, None,
+                    states["di"][1].view(N, 1, C), cu)
+    torch.cuda.synchronize()
+    assert kda.kda_workspace_faults(ws) == 0
+    say("conv", cu.tolist())
+    kda.kda_conv_fwd(x[None], w, o("y")[None], None, init, rows["cf"][1], cu, kda.FLAG_SILU)
+    kda.kda_conv_bwd(x[None], w, d_out[None], o("dy")[None], dw, ws, None, None, init, None, rows["cd"][1], cu, kda.FLAG_SILU)
+    torch.cuda.synchronize()
+    for n, (whole, inner) in (outs | states | rows).items():
+        assert torch.isfinite(inner).all(), n
+        assert (whole[:pad] == 7).all() and (whole[-pad:] == 7).all(), n
+    assert all(torch.isfinite(t).all() for t in (dA, dd, dw))
