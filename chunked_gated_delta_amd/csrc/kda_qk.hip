@@ -316,6 +316,12 @@ bool strides_ok(int64_t tokens, int64_t H, int64_t D, int64_t ts, int64_t hs) {
          (H <= 1 || hs >= D) && (tokens <= 1 || ts >= D);
 }
 
+// Whether no two rows of D elements share any: heads within a token's span, or
+// tokens within a head's.
+bool rows_apart(int64_t tokens, int64_t H, int64_t D, int64_t ts, int64_t hs) {
+  return H == 0 || tokens <= 1 || ts >= (H - 1) * hs + D || (H > 1 && hs >= (tokens - 1) * ts + D);
+}
+
 kda_status_t qk_prepare(QkArgs& a, const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
                         int64_t k_stride, int64_t k_head_stride, const float* q_weight, const float* k_weight,
                         const int32_t* positions, const double* inv_freq, float eps, int64_t tokens, int64_t Hq,
@@ -402,6 +408,9 @@ kda_status_t kda_qk_rope_fwd(const void* q, int64_t q_stride, int64_t q_head_str
   a.q_out = q_out;
   a.k_out = k_out;
   const bool qin = q_out == q, kin = k_out == k;  // in place: the input's strides
+  if ((qin && !rows_apart(tokens, Hq, D, q_stride, q_head_stride)) ||
+      (kin && !rows_apart(tokens, Hk, D, k_stride, k_head_stride)))
+    return KDA_ERR_INVALID;
   a.qos = qin ? a.qs : Hq * D;
   a.qoh = qin ? a.qh : D;
   a.kos = kin ? a.ks : Hk * D;

@@ -87,6 +87,7 @@ REFUSED = [
        dict(flags=4 | 512), dict(qs=8), dict(qs=34), dict(qh=8), dict(ks=-16), dict(q=P + 2), dict(k=P + 4),
        dict(n=1 << 60))],
     *[(f, o, UNSUPPORTED) for f in (rope_fwd, rope_bwd) for o in (dict(D=20), dict(D=520, qh=520, qs=1040, ks=520, kh=520), dict(R=4), dict(ty=3))],
+    (rope_fwd, dict(qs=16), INVALID), (rope_fwd, dict(Hk=2, ks=16), INVALID),  # in place over rows that overlap
     (rope_bwd, dict(dqw=P), WORKSPACE), (rope_bwd, dict(dkw=P, ws=P, size=64), WORKSPACE),
 ]
 
