@@ -6,6 +6,11 @@ norm and rotation of queries and keys.  Each allocates its outputs and
 workspaces with PyTorch and calls the library's entry points for both
 directions; without a gradient to compute they are the inference calls too.
 
+A backward pass can be captured into a graph as any of PyTorch's: after warm-up
+passes on a side stream, and with no eager graph over the same parameters still
+alive (an output of an earlier pass that is kept holds one), since PyTorch would
+add the captured gradients up on that graph's stream.
+
 ``kda_chunk`` allocates the outputs and workspaces with PyTorch and calls the
 library's ``kda_fwd`` in the forward and ``kda_bwd`` in the backward; it adds
 no arithmetic of its own.  Gradients flow to q, k, v, raw_gate, raw_beta,

@@ -455,9 +455,11 @@ typedef enum {
  *   out           [B, T, H, K] written
  *   workspace     scratch of >= kda_glr_workspace_size(B * T, H, K) bytes
  *   A_log, dt_bias, lower_bound   as for kda_fwd.  With KDA_FLAG_GATE_GIVEN
- *                 raw_gate holds g itself, any value (minus infinity: the
- *                 state is dropped), these three are unused, and A_log and
- *                 dt_bias may be NULL.
+ *                 raw_gate holds g itself (minus infinity: the state is
+ *                 dropped; values above 0 only as long as a stretch of 224
+ *                 rows sums to less than 88, since decays are multiplied
+ *                 before they meet a state), these three are unused, and
+ *                 A_log and dt_bias may be NULL.
  *   initial_state fp32 [N, H, K] or NULL for zeros
  *   final_state   fp32 [N, H, K] written, or NULL
  *   states        >= kda_glr_states_size(B * T, H, K) bytes, written for a
@@ -567,7 +569,7 @@ kda_status_t kda_conv_step(const void* x, int64_t x_stride, const float* weight,
  *                 elements (multiples of 4): slices of one projection's output
  *                 will do.  Hq or Hk may be 0.
  *   q_out, k_out  contiguous, or equal to q and k: then in place, with their
- *                 strides
+ *                 strides, under which no two rows may overlap
  *   q_weight, k_weight  fp32 [D] or NULL
  *   positions     int32 [tokens], any value; inv_freq fp64 [R / 2], radians per
  *                 position (angles are formed and reduced in fp64).  Both may

@@ -784,3 +784,50 @@ def test_offsets_that_break_the_contract_stay_inside(cu):
         assert torch.isfinite(inner).all(), n
         assert (whole[:pad] == 7).all() and (whole[-pad:] == 7).all(), n
     assert all(torch.isfinite(t).all() for t in (dA, dd, dw))
+
+
+def test_captured_training_pass():
+    """Forward and backward through autograd in one captured graph, replayed with new inputs; the eager
+    passes between the replays have leaves of their own."""
+    H, K, T = 2, 64, 300
+    cu = torch.tensor([0, 120, 120, 290], dtype=torch.int32, device=DEV)
+    pos, f = torch.arange(T, dtype=torch.int32, device=DEV)[None], torch.full((16,), 0.3, dtype=torch.float64, device=DEV)
+
+    def inputs(seed):
+        r = Rand(seed)
+        leaves = [r(1, T, H * K, dtype=torch.bfloat16), r(H * K, 4, std=0.5), r(H * K), 1 + r(K, std=0.1), r(1, T, H, K, dtype=torch.bfloat16),
+                  r(H, std=0.5), r(H, K, std=0.1), r(3, H, K)]
+        return [t.to(DEV).requires_grad_(True) for t in leaves], [dev(r(1, T, H, K, dtype=torch.bfloat16)), dev(r(3, H, K))]
+
+    def step(leaves, d):
+        x, w, b, nw, g, al, dt, init = leaves
+        y = kda_short_conv(x, w, b, cu_seqlens=cu)[0].view(1, T, H, K)
+        y, z = kda_qk_norm_rope(y, y, pos, f, q_weight=nw)
+        h, fin = kda_glr(y, g, al, dt, initial_state=init, cu_seqlens=cu, complement=True)
+        h2, _ = kda_glr(z, g, al, dt, cu_seqlens=cu)
+        return torch.autograd.grad((h, fin, h2), leaves, (d[0], d[1], d[0]))
+
+    leaves, d = inputs(70)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(leaves, d)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    say("capture")
+    with torch.cuda.graph(graph):
+        grads = step(leaves, d)
+    torch.cuda.synchronize()
+    for i in range(4):
+        eager, de = inputs(71 + i)
+        with torch.no_grad():
+            for to, by in zip(leaves + d, eager + de):
+                to.copy_(by)
+        say("replay", i)
+        graph.replay()
+        want = step(eager, de)
+        torch.cuda.synchronize()
+        for n, (got, w) in enumerate(zip(grads, want)):
+            assert torch.equal(got, w), (i, n)
