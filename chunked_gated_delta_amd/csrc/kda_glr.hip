@@ -37,11 +37,12 @@
 // row) and e_t = a_t dh_t, the gradient that row t hands to the row before:
 //     dx_t = b_t dh_t,   dg_t = a_t dh_t (h_{t-1} [- x_t if b = 1 - a])
 // the same pass runs over e from the right; h_{t-1} is recomputed from the
-// states entering every 112 rows, which the forward leaves.  At 69141 x 4096 it
-// takes 0.85 ms, 3.3 TB/s of its 10 bytes an element: per 112-row tile the seven
-// waves need about 9000 cycles of arithmetic (three exponentials and two
-// reciprocals an element) and the joining wave as long for two sets of runs and
-// its waits.
+// states entering every 112 rows, which the forward leaves.  At 32768 x 12288 it
+// takes 0.94 ms, 4.3 TB/s of its 10 bytes an element (1.03 ms with the slopes of
+// the gates formed twice and the gates' parameters loaded by every wave); at
+// 69141 x 4096, with four tiles of a column at work, 0.84 ms, 3.4 TB/s: 0.73 of
+// them without the waits for entering states, 0.53 if rows and results also
+// stayed in the caches.
 //
 // All arithmetic is fp32.
 
@@ -107,6 +108,29 @@ struct GlrArgs {
   float lb;
 };
 
+// The gates of a tile's columns, by the wave that joins: asked for a tile ahead
+// of their use, and written where the seven waves find them.
+template <bool STAGED>
+struct Gates {
+  int blk = -1;  // the column block that is in hand: a workgroup's tiles are often of one
+  float al, dt;
+  __device__ __forceinline__ void ask(const GlrArgs& a, int2 item, int ch) {
+    if (!STAGED || item.x >= a.ntiles || item.y == blk) return;
+    blk = item.y;
+    const uint32_t c = (uint32_t)blk * GC + ch;
+    const bool in = c < (uint32_t)a.C;
+    al = in ? a.A_log[c / (uint32_t)a.K] : 0.f;
+    dt = in ? a.dt_bias[c] : 0.f;
+  }
+  __device__ __forceinline__ void put(float (&gate)[2][GC], int ch) const {
+    if constexpr (STAGED) {
+      const float na = -expf(al) * LOG2E;
+      gate[0][ch] = na;
+      gate[1][ch] = na * dt;
+    }
+  }
+};
+
 // The gate of 4 channels.  With z = exp(A_log) (raw + dt_bias), na and nb hold
 // -exp(A_log) log2(e) and na dt_bias, so that -z log2(e) = na raw + nb.
 template <bool GIVEN>
@@ -121,10 +145,32 @@ struct Gate {
       lb2 = a.lb * LOG2E;
     }
   }
+  // The same out of LDS, where the wave that joins has put it: a load here
+  // would come back behind every row that the wave has asked for.
+  __device__ __forceinline__ void init(const GlrArgs& a, const float (&gate)[2][GC], int at) {
+    if constexpr (!GIVEN) {
+      na = gate[0][at];
+      load_f4(&gate[1][at], nb);
+      lb2 = a.lb * LOG2E;
+    }
+  }
   // g log2(e)
   __device__ __forceinline__ float g2(float raw, int j) const {
     if constexpr (GIVEN) return raw * LOG2E;
     return lb2 * __builtin_amdgcn_rcpf(1.0f + fexp2(raw * na + nb[j]));
+  }
+  // and s (1 - s) = w s^2, with s = sigmoid(z) and w = exp(-z), its slope but
+  // for constants.  The w outside of s is kept finite so that w s does not
+  // become infinity times zero (a NaN is in s as well).
+  __device__ __forceinline__ float g2(float raw, int j, float& slope) const {
+    const float w = fexp2(raw * na + nb[j]), s = __builtin_amdgcn_rcpf(1.0f + w);
+    slope = fminf(w, 0x1p126f) * s * s;
+    return lb2 * s;
+  }
+  // the slope alone, from -z log2(e) (held finite by a comparison: NaN stays)
+  __device__ __forceinline__ float slope(float mz) const {
+    const float w = fexp2(mz > 126.f ? 126.f : mz), s = __builtin_amdgcn_rcpf(1.0f + w);
+    return s * (w * s);
   }
 };
 
@@ -372,9 +418,14 @@ struct Drawer {
   }
   // A ticket is asked for by ask() and turned into a tile (x: its number in the
   // pass's order, at least ntiles for none; y: its column block) by answer(),
-  // later: the round trip lies between.
-  __device__ __forceinline__ int ask() const {
-    return __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // later: the round trip lies between.  The address is given in a vector
+  // register: at one that is known to be the wave's the compiler adds up over
+  // lanes first and so takes the answer at once.  `after` is an answer that has
+  // to be there before.
+  __device__ __forceinline__ int ask(int after = 0) const {
+    int zero = 0;
+    asm("" : "+v"(zero) : "v"(after));
+    return __hip_atomic_fetch_add(counter + zero, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __device__ __forceinline__ int2 answer(int t) const {
     int q = (int)(t * per);  // t / n, off by one at most
@@ -384,7 +435,10 @@ struct Drawer {
   }
 };
 
-// The first N tiles and the ticket after them, asked for at once, by one thread.
+// The first N tiles and the ticket after them, by one thread.  One at a time, so
+// that the workgroups' first tiles come first, then their second ones: asked for
+// at once, a workgroup holds neighbours, and the next waits for its last
+// (262144 x 1024 680 us instead of 430).
 // With one tile a column nothing waits for anything: there is a workgroup for
 // every column, and no counter.
 template <int N>
@@ -395,8 +449,8 @@ __device__ __forceinline__ int draw_first(const GlrArgs& a, const Drawer& d, int
   }
   int t[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) t[i] = d.ask();
-  const int asked = d.ask();
+  for (int i = 0; i < N; ++i) t[i] = d.ask(i > 0 ? t[i - 1] : 0);
+  const int asked = d.ask(t[N - 1]);
 #pragma unroll
   for (int i = 0; i < N; ++i) slot[i] = d.answer(t[i]);
   return asked;
@@ -438,9 +492,14 @@ struct Raw {
 template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
   constexpr int R = FR<T>, L = FL<T>;
+  // Gates out of LDS (see Gates), where a tile has many rows: 32768 x 12288 of
+  // bf16 takes 480 us so and 490 to 515 with loads; fp32, whose tiles have half
+  // as many, 540 us and 475 at 32768 x 6144.
+  constexpr bool STAGED = sizeof(T) == 2 && !GIVEN;
   __shared__ Tile tiles[2];
   __shared__ Maps maps;
   __shared__ Marks marks[4];
+  __shared__ float gates[4][2][GC];
   __shared__ int2 slot[8];  // tiles, by turns
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
@@ -451,6 +510,12 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
   if (tid >= GD) {
     // everything else waits for this wave: its instructions go first
     __builtin_amdgcn_s_setprio(3);
+    const int ch = tid - GD;
+    Gates<STAGED> gate;
+    for (int i = 0; i < 2; ++i) {
+      gate.ask(a, slot[i], ch);
+      gate.put(gates[i], ch);
+    }
     __syncthreads();  // marks
     __syncthreads();  // the maps of the first tile
     for (int i = 0;; ++i) {
@@ -458,8 +523,10 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       if (item.x >= a.ntiles) break;
       const Marks& m = marks[i & 3];
       const int k = item.x, blk = item.y;
+      gate.ask(a, slot[(i + 2) & 7], ch);
       if (m.any) join_runs<false, true, FR<T> / BR>(a, tiles[i & 1], maps, k, blk, m.S[0] >= 0);
       else join_runs<false, false, FR<T> / BR>(a, tiles[i & 1], maps, k, blk, false);
+      gate.put(gates[(i + 2) & 3], ch);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
     }
   } else {
@@ -490,7 +557,8 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
       place(item, t0, c);
       const bool in = c < a.C;
       Gate<GIVEN> gate;
-      gate.init(a, in ? c : 0);
+      if constexpr (STAGED) gate.init(a, gates[i & 3], lane * 4);
+      else gate.init(a, in ? c : 0);
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         float xv[4], gv[4];
@@ -596,10 +664,11 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_fwd_kernel(GlrArgs a) {
   }
 }
 
-// The backward's run keeps its rows as loaded: they are needed again.
-template <typename T>
+// The backward's run keeps its rows as loaded, its decays and (SLOPE) the slopes
+// of its gates: they are needed again.
+template <typename T, bool SLOPE>
 struct Kept {
-  float a[BR][4];
+  float a[BR][4], slope[SLOPE ? BR : 1][4];
   raw4<T> x[BR], g[BR], d[BR];
 };
 
@@ -609,10 +678,13 @@ struct Kept {
 template <typename T, bool GIVEN, bool COMPL>
 __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
   constexpr int R = BR, L = BL;
+  // With b = 1 - a the registers do not hold the slopes too: they are formed again.
+  constexpr bool SLOPE = !GIVEN && !COMPL;
   __shared__ Tile et[2], ht[2];  // maps of e, from the right, and of h
   __shared__ float dsums[GIVEN ? 1 : 2][GS][GC], zsums[GIVEN ? 1 : 2][GS][GC];
   __shared__ Maps maps;
   __shared__ Marks marks[4];
+  __shared__ float gates[4][2][GC];
   __shared__ int2 slot[8];
   const int tid = threadIdx.x, lane = tid % GW, run = tid / GW;
   const int64_t rows = axis_rows(a.ax);
@@ -640,6 +712,11 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       a.part[(int64_t)(a.ntiles - 1 - item.x) * a.C + c] = make_float2(d, z);
     };
     float s = state_of(slot[0]);
+    Gates<!GIVEN> gate;
+    for (int i = 0; i < 2; ++i) {
+      gate.ask(a, slot[i], ch);
+      gate.put(gates[i], ch);
+    }
     int last = -1;
     __syncthreads();  // marks
     __syncthreads();  // the maps of the first tile
@@ -648,6 +725,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       if (item.x >= a.ntiles) break;
       const Marks& m = marks[i & 3];
       const int k = item.x, blk = item.y;
+      gate.ask(a, slot[(i + 2) & 7], ch);
       if (m.any) join_runs<true, true, 0>(a, et[i & 1], maps, k, blk, m.E[L - 1] >= 0);
       else join_runs<true, false, 0>(a, et[i & 1], maps, k, blk, false);
       Tile& t = ht[i & 1];
@@ -667,6 +745,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         }
       }
       s = state_of(slot[(i + 1) & 7]);
+      gate.put(gates[(i + 2) & 3], ch);
       __syncthreads();  // what enters tile i, the maps of tile i + 1
       if (!GIVEN && i > 0) add_up(slot[(i - 1) & 7], i - 1);
       last = i;
@@ -680,7 +759,7 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       c = (int64_t)item.y * GC + lane * 4;
       return c < a.C ? run * R * row_bytes + (int)(c * sizeof(T)) : OUTSIDE;
     };
-    auto fetch = [&](int2 item, Kept<T>& r) {
+    auto fetch = [&](int2 item, Kept<T, SLOPE>& r) {
       if (item.x >= a.ntiles) return;
       int64_t t0, c;
       const int voff = place(item, t0, c);
@@ -696,13 +775,13 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       if (tid < 64 && item.x < a.ntiles)
         mark_tile(a.ax, (int64_t)(a.ntiles - 1 - item.x) * L, L, rows, marks[i & 3]);
     };
-    auto map_ = [&](auto marked, int2 item, int i, Kept<T>& r) {
+    auto map_ = [&](auto marked, int2 item, int i, Kept<T, SLOPE>& r) {
       int64_t t0, c;
       place(item, t0, c);
       const bool in = c < a.C;
       const int64_t tr = t0 + run * R;
       Gate<GIVEN> gate;
-      gate.init(a, in ? c : 0);
+      gate.init(a, gates[i & 3], lane * 4);
       const Marks& m = marks[i & 3];
       {  // of h
         Tile& t = ht[i & 1];
@@ -724,7 +803,9 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
           widen4(r.g[q], gv);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float g2 = gate.g2(gv[j], j);
+            float g2;
+            if constexpr (SLOPE) g2 = gate.g2(gv[j], j, r.slope[q][j]);
+            else g2 = gate.g2(gv[j], j);
             r.a[q][j] = fexp2(g2);
             A[j] *= r.a[q][j];
             B[j] = r.a[q][j] * B[j] + (COMPL ? one_minus(g2, r.a[q][j]) * xv[j] : xv[j]);
@@ -764,19 +845,20 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         if (lane == 0) t.reset[run] = reset;
       }
     };
-    auto map = [&](int2 item, int i, Kept<T>& r) {
+    auto map = [&](int2 item, int i, Kept<T, SLOPE>& r) {
       if (item.x >= a.ntiles) return;
       if (marks[i & 3].any) map_(std::true_type{}, item, i, r);
       else map_(std::false_type{}, item, i, r);
     };
-    auto finish_ = [&](auto marked, int2 item, int i, const Kept<T>& r) {
+    auto finish_ = [&](auto marked, int2 item, int i, const Kept<T, SLOPE>& r) {
       int64_t t0, c;
       const int voff = place(item, t0, c);
       const bool in = c < a.C;
       const int64_t tr = t0 + run * R;
       Gate<GIVEN> gate;
-      gate.init(a, in ? c : 0);
+      gate.init(a, gates[i & 3], lane * 4);
       const Marks& m = marks[i & 3];
+      const float to_raw = GIVEN ? 1.f : a.lb * (gate.na * -0.6931471805599453f);
       float h[4], e[4], hp[R][4], dsum[4], zsum[4];
       load_f4(&ht[i & 1].A[run][lane * 4], h);
       load_f4(&et[i & 1].A[run][lane * 4], e);
@@ -809,15 +891,14 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
             dx[j] = COMPL ? one_minus(gate.g2(gv[j], j), r.a[q][j]) * dh : dh;
             dg[j] = e[j] * hp[q][j];
             if constexpr (!GIVEN) {
-              // dg/dz = lb s (1 - s), s = 1 / (1 + w), w = exp(-z).  w is kept
-              // finite (a comparison, so that NaN stays) so that w s does not
-              // become infinity times zero.
+              // dg/dz = lb slope, dz/draw = exp(A_log)
               const float mz = gv[j] * gate.na + gate.nb[j];  // -z log2(e)
-              const float w = fexp2(mz > 126.f ? 126.f : mz);
-              const float s = __builtin_amdgcn_rcpf(1.0f + w);
-              const float dz = dg[j] * (a.lb * s * (w * s));
-              zsum[j] += dz * (mz * -0.6931471805599453f);
-              dg[j] = dz * (gate.na * -0.6931471805599453f);  // dz/draw = exp(A_log)
+              float slope;
+              if constexpr (SLOPE) slope = r.slope[q][j];
+              else slope = gate.slope(mz);
+              const float dz = dg[j] * slope;  // (the constants come behind)
+              zsum[j] += dz * mz;
+              dg[j] = dz * to_raw;
               dsum[j] += dg[j];
             }
           }
@@ -831,17 +912,19 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
         }
       }
       if constexpr (!GIVEN) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) zsum[j] *= a.lb * -0.6931471805599453f;
         store4(&dsums[i & 1][run][lane * 4], dsum);
         store4(&zsums[i & 1][run][lane * 4], zsum);
       }
     };
-    auto finish = [&](int2 item, int i, const Kept<T>& r) {
+    auto finish = [&](int2 item, int i, const Kept<T, SLOPE>& r) {
       if (marks[i & 3].any) finish_(std::true_type{}, item, i, r);
       else finish_(std::false_type{}, item, i, r);
     };
     // tile i is ready in `now`; tile i + 1 is made in `then`; `now` takes tile i + AHEAD
     constexpr int AHEAD = sizeof(T) == 2 ? 3 : 2;
-    auto turn = [&](int i, Kept<T>& now, Kept<T>& then) {
+    auto turn = [&](int i, Kept<T, SLOPE>& now, Kept<T, SLOPE>& then) {
       const int2 item = slot[i & 7];
       if (item.x >= a.ntiles) return false;
       mark(slot[(i + 2) & 7], i + 2);
@@ -855,13 +938,13 @@ __global__ void __launch_bounds__(GT, 2) kda_glr_bwd_kernel(GlrArgs a) {
       fetch(slot[(i + AHEAD) & 7], now);
       return true;
     };
-    Kept<T> r0, r1;
+    Kept<T, SLOPE> r0, r1;
     mark(slot[0], 0);
     mark(slot[1], 1);
     fetch(slot[0], r0);
     fetch(slot[1], r1);
     if constexpr (AHEAD == 3) {
-      Kept<T> r2;
+      Kept<T, SLOPE> r2;
       fetch(slot[2], r2);
       __syncthreads();  // marks
       map(slot[0], 0, r0);
