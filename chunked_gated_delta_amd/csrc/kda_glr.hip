@@ -226,7 +226,11 @@ __device__ __forceinline__ void mark_tile(const Axis& ax, int64_t t0, int tile_l
 
 // Loads and stores of a tile by 32-bit offsets from its first row.  The
 // descriptor ends behind the last row that belongs to a sequence: rows behind
-// it load as zeros and are not stored, and so does an offset of OUTSIDE.
+// it load as zeros and are not stored, and so does an offset of OUTSIDE.  All of
+// an offset is in the lane's register: the intrinsics leave the scalar offset
+// out of the check against the descriptor's end, so that with a row's offset
+// there the last tile read rows behind the array.  (No slower: 32704 x 12288 of
+// bf16 472 us forward and 936 backward, 470 and 940 with scalar offsets.)
 constexpr int OUTSIDE = 0x40000000;  // past any tile, also with a row's offset added
 template <typename T, int L>
 struct Rows {
@@ -235,11 +239,11 @@ struct Rows {
     const int64_t left = rows - t0 < L ? rows - t0 : L;
     r = buf(static_cast<const T*>(base) + t0 * C, (uint32_t)((left > 0 ? left : 0) * C * sizeof(T)));
   }
-  __device__ __forceinline__ raw4<T> load(int voff, int soff) const {
+  __device__ __forceinline__ raw4<T> load(int voff, int off) const {
     if constexpr (sizeof(T) == 2) {
-      return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0));
+      return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, voff + off, 0, 0));
     } else {
-      return __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+      return __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, voff + off, 0, 0));
     }
   }
   // The row's offset goes into the lane's: a 16-byte store with an offset in a
