@@ -20,6 +20,7 @@ A_log, dt_bias and initial_state from the output and from the final state.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import (FLAG_COMPLEMENT, FLAG_GATE_GIVEN, FLAG_INTERLEAVED, FLAG_KEEP_RECORDS, FLAG_NO_QK_NORM,
                FLAG_REUSE_RECORDS, FLAG_RMS_NORM, FLAG_SILU, FLAG_ZERO_REST, kda_bwd_ex, kda_bwd_workspace_size, kda_conv_bwd,
@@ -148,8 +149,13 @@ class _Glr(torch.autograd.Function):
         return dx, dg, dA, dd, di, None, None, None
 
 
-def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+def _wants_derivative(*tensors):
+    """Whether the call has to be seen by autograd: an input requires a gradient, or carries a tangent
+    (forward mode, which these operators do not have: autograd says so)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def kda_glr(x, raw_gate, A_log=None, dt_bias=None, *, lower_bound=-5.0, initial_state=None, cu_seqlens=None,
@@ -167,7 +173,7 @@ def kda_glr(x, raw_gate, A_log=None, dt_bias=None, *, lower_bound=-5.0, initial_
         raise ValueError("with gate_given there is no A_log and no dt_bias")
     flags = (FLAG_GATE_GIVEN if gate_given else 0) | (FLAG_COMPLEMENT if complement else 0) | FLAG_ZERO_REST
     args = (x, raw_gate, A_log, dt_bias, initial_state, float(lower_bound), cu_seqlens, flags)
-    if _wants_grad(x, raw_gate, A_log, dt_bias, initial_state):
+    if _wants_derivative(x, raw_gate, A_log, dt_bias, initial_state):
         return _Glr.apply(*args)
     return _glr_forward(*args, False)[:2]
 
@@ -212,7 +218,7 @@ def kda_short_conv(x, weight, bias=None, *, silu=True, initial_state=None, cu_se
     call's initial state.
     """
     args = (x, weight, bias, initial_state, cu_seqlens, (FLAG_SILU if silu else 0) | FLAG_ZERO_REST)
-    return _Conv.apply(*args) if _wants_grad(x, weight, bias, initial_state) else _conv_forward(*args)
+    return _Conv.apply(*args) if _wants_derivative(x, weight, bias, initial_state) else _conv_forward(*args)
 
 
 def _qk_forward(q, k, q_weight, k_weight, positions, inv_freq, eps, flags):
@@ -264,4 +270,4 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
         raise ValueError(f"norm must be one of {sorted(_NORM)}")
     args = (q, k, q_weight, k_weight, positions, inv_freq, float(eps),
             _NORM[norm] | (FLAG_INTERLEAVED if interleaved else 0))
-    return _QkNormRope.apply(*args) if _wants_grad(q, k, q_weight, k_weight) else _qk_forward(*args)
+    return _QkNormRope.apply(*args) if _wants_derivative(q, k, q_weight, k_weight) else _qk_forward(*args)

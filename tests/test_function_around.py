@@ -1,0 +1,53 @@
+"""The differentiable wrappers of the operators around the core, on the CPU: what they hand to the
+library's calls, which are replaced here, and what autograd sees of them."""
+
+import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
+
+from chunked_gated_delta_amd import function as F
+
+CALLS = ("kda_glr_fwd", "kda_glr_bwd", "kda_conv_fwd", "kda_conv_bwd", "kda_qk_rope_fwd", "kda_qk_rope_bwd")
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """The arguments of every call, by its name; nothing is computed."""
+    seen = {}
+    for name in CALLS:
+        monkeypatch.setattr(F, name, lambda *a, _name=name, **k: seen.setdefault(_name, []).append(a))
+    return seen
+
+
+def inputs(ty=torch.bfloat16):
+    """Per operator: the call, and its inputs that may be differentiated, by name."""
+    x = torch.randn(1, 6, 2, 8, dtype=ty)
+    pos, f = torch.zeros(1, 6, dtype=torch.int32), torch.ones(4, dtype=torch.float64)
+    return {
+        "glr": (lambda x, raw_gate, A_log, dt_bias, initial_state: F.kda_glr(x, raw_gate, A_log, dt_bias,
+                                                                             initial_state=initial_state),
+                dict(x=x, raw_gate=torch.randn(1, 6, 2, 8, dtype=ty), A_log=torch.randn(2), dt_bias=torch.randn(2, 8),
+                     initial_state=torch.randn(1, 2, 8))),
+        "conv": (lambda x, weight, bias, initial_state: F.kda_short_conv(x, weight, bias, initial_state=initial_state),
+                 dict(x=torch.randn(1, 6, 16, dtype=ty), weight=torch.randn(16, 4), bias=torch.randn(16),
+                      initial_state=torch.randn(1, 3, 16, dtype=ty))),
+        "qk": (lambda q, k, q_weight, k_weight: F.kda_qk_norm_rope(q, k, pos, f, q_weight=q_weight, k_weight=k_weight),
+               dict(q=x, k=torch.randn(1, 6, 1, 8, dtype=ty), q_weight=torch.randn(8), k_weight=torch.randn(8))),
+    }
+
+
+NAMES = [(op, n) for op, (_, t) in inputs().items() for n in t]
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("op,name", NAMES)
+def test_a_tangent_is_refused_not_dropped(op, name, grad, library):
+    """These operators have no forward-mode derivative: an input with a tangent is an error, with and
+    without a graph to record, and a call without one inside the same level is not."""
+    call, t = inputs()[op]
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        call(**t)
+        t[name] = forward_ad.make_dual(t[name], torch.ones_like(t[name]))
+        with pytest.raises(NotImplementedError, match="jvp"):
+            call(**t)
+    assert not any(o.requires_grad for o in call(**inputs()[op][1]))
