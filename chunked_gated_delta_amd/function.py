@@ -38,6 +38,13 @@ def _sizes(q, v, cu_seqlens):
     return B, T, H, K, V, N
 
 
+def _as_taken(g, dtype):
+    """A gradient as the kernels load it: of their type, contiguous and on a 16-byte boundary (a
+    contiguous one need not be: the gradient of a piece of a ``cat`` is a view at the piece's offset)."""
+    g = g.to(dtype).contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _KdaChunk(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, raw_gate, raw_beta, A_log, dt_bias, initial_state, scale, lower_bound,
@@ -60,8 +67,8 @@ class _KdaChunk(torch.autograd.Function):
     def backward(ctx, d_out, d_final):
         q, k, v, raw_gate, raw_beta, A_log, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
         B, T, H, K, V, N = _sizes(q, v, cu_seqlens)
-        d_out = torch.zeros_like(v) if d_out is None else d_out.to(torch.bfloat16).contiguous()
-        d_final = None if d_final is None else d_final.to(torch.float32).contiguous()
+        d_out = torch.zeros_like(v) if d_out is None else _as_taken(d_out, torch.bfloat16)
+        d_final = None if d_final is None else _as_taken(d_final, torch.float32)
         dq, dk, draw_gate = torch.empty_like(q), torch.empty_like(k), torch.empty_like(raw_gate)
         dv, draw_beta = torch.empty_like(v), torch.empty_like(raw_beta)
         dA_log, ddt_bias = torch.empty_like(A_log), torch.empty_like(dt_bias)
@@ -105,8 +112,8 @@ def _scratch(size, like):
 
 
 def _grad(g, like):
-    """A gradient as the library takes it: the output's type, contiguous, zeros where there is none."""
-    return torch.zeros_like(like, memory_format=torch.contiguous_format) if g is None else g.to(like.dtype).contiguous()
+    """The gradient of an output of ``like``'s shape and type, zeros where there is none."""
+    return torch.zeros_like(like, memory_format=torch.contiguous_format) if g is None else _as_taken(g, like.dtype)
 
 
 def _count(x, cu_seqlens):
@@ -139,7 +146,7 @@ class _Glr(torch.autograd.Function):
         x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
         B, T, H, K = x.shape
         d_out = _grad(d_out, x)
-        d_final = None if d_final is None else d_final.to(torch.float32).contiguous()
+        d_final = None if d_final is None else _as_taken(d_final, torch.float32)
         dx, dg = torch.empty_like(x), torch.empty_like(raw_gate)
         dA, dd = (None if t is None else torch.empty_like(t) for t in (A_log, dt_bias))
         di = None if initial_state is None else torch.empty_like(initial_state)
@@ -167,7 +174,9 @@ def kda_glr(x, raw_gate, A_log=None, dt_bias=None, *, lower_bound=-5.0, initial_
     itself with ``gate_given`` (A_log and dt_bias must then be None); b_t = 1, or 1 - a_t with ``complement``.  x and
     raw_gate bf16 or fp32 [B,T,H,K]; A_log fp32 [H]; dt_bias fp32 [H,K]; initial_state fp32
     [N,H,K] or None; cu_seqlens int32 [N+1] (with B = 1) or None; rows behind the last sequence
-    come back as zeros.  All tensors contiguous, on one GPU, and unchanged until the backward.
+    come back as zeros.  All tensors contiguous, on one GPU, and unchanged until the backward; x and
+    raw_gate on a boundary of 4 elements, dt_bias and initial_state of 16 bytes, as PyTorch allocates
+    (a view into a flat buffer may start elsewhere; the call then raises KdaError).
     """
     if gate_given and (A_log is not None or dt_bias is not None):
         raise ValueError("with gate_given there is no A_log and no dt_bias")
@@ -198,7 +207,7 @@ class _Conv(torch.autograd.Function):
     def backward(ctx, d_out, d_final):
         x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
         d_out = _grad(d_out, x)
-        d_final = None if d_final is None else d_final.to(x.dtype).contiguous()
+        d_final = None if d_final is None else _as_taken(d_final, x.dtype)
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dw = torch.empty_like(weight)
         db, di = (None if t is None else torch.empty_like(t) for t in (bias, initial_state))
@@ -215,7 +224,8 @@ def kda_short_conv(x, weight, bias=None, *, silu=True, initial_state=None, cu_se
     do); weight fp32 [C,W], W 2 to 4; bias fp32 [C] or None; initial_state [N,W-1,C] of x's type
     (the inputs before the first token, in order) or None for zeros; cu_seqlens int32 [N+1] (with
     B = 1) or None; rows behind the last sequence come back as zeros.  The final state is the next
-    call's initial state.
+    call's initial state.  x and initial_state start on a boundary of 4 elements, weight and bias of 16
+    bytes (a view into a flat buffer that does not makes the call raise KdaError).
     """
     args = (x, weight, bias, initial_state, cu_seqlens, (FLAG_SILU if silu else 0) | FLAG_ZERO_REST)
     return _Conv.apply(*args) if _wants_derivative(x, weight, bias, initial_state) else _conv_forward(*args)
@@ -264,7 +274,8 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     (x / sqrt(mean x^2 + eps)) or "none"; q_weight, k_weight fp32 [D] or None; positions int32
     [B,T] and inv_freq fp64 [R/2] (radians per position) turn the pairs (i, i + R/2) of the first
     R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them.  With "l2" and no weights
-    the results are unit rows, as ``kda_fwd_ex`` takes them with FLAG_NO_QK_NORM.
+    the results are unit rows, as ``kda_fwd_ex`` takes them with FLAG_NO_QK_NORM.  q and k start on a
+    boundary of 4 elements, and so do their rows.
     """
     if norm not in _NORM:
         raise ValueError(f"norm must be one of {sorted(_NORM)}")

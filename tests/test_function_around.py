@@ -51,3 +51,42 @@ def test_a_tangent_is_refused_not_dropped(op, name, grad, library):
         with pytest.raises(NotImplementedError, match="jvp"):
             call(**t)
     assert not any(o.requires_grad for o in call(**inputs()[op][1]))
+
+
+def at_odd_place(t):
+    """The same values, contiguous, one element behind an aligned address."""
+    flat = torch.cat([t.new_zeros(1), t.flatten()])
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("op,ty", [(op, ty) for op in ("glr", "conv", "qk") for ty in (torch.bfloat16, torch.float32)])
+def test_gradients_may_arrive_at_any_address(op, ty, library):
+    """The gradient of a piece of a cat is a view at the piece's offset: contiguous and not aligned.
+    The kernels' loads are of up to 16 bytes."""
+    call, t = inputs(ty)[op]
+    outs = call(**{n: v.requires_grad_() for n, v in t.items()})
+    grads = [torch.randn_like(o) for o in outs]
+    torch.autograd.backward(outs, [at_odd_place(g) for g in grads])
+    name = {"glr": "kda_glr_bwd", "conv": "kda_conv_bwd", "qk": "kda_qk_rope_bwd"}[op]
+    (args,) = library[name]
+    given = [a for a in args if torch.is_tensor(a) and any(a.shape == g.shape and torch.equal(a, g) for g in grads)]
+    assert len(given) == 2 and all(a.data_ptr() % 16 == 0 and a.is_contiguous() for a in given)
+    # as autograd itself hands them out
+    library.clear()
+    out = call(**t)[0]
+    torch.cat([out.new_zeros(1), out.flatten()]).sum().backward()
+    (args,) = library[name]
+    ones = [a for a in args if torch.is_tensor(a) and a.shape == out.shape and (a == 1).all()]
+    assert len(ones) == 1 and ones[0].data_ptr() % 16 == 0
+
+
+def test_gradients_of_the_core_may_arrive_at_any_address(monkeypatch):
+    seen = []
+    monkeypatch.setattr(F, "kda_fwd_ex", lambda *a, **k: None)
+    monkeypatch.setattr(F, "kda_bwd_ex", lambda *a, **k: seen.append((a[6], k["d_final"])))
+    q, k, v, g = (torch.randn(1, 64, 1, 64, dtype=torch.bfloat16).requires_grad_() for _ in range(4))
+    outs = F.kda_chunk(q, k, v, g, torch.randn(1, 64, 1, dtype=torch.bfloat16), torch.zeros(1), torch.zeros(1, 64))
+    grads = [torch.randn_like(o) for o in outs]
+    torch.autograd.backward(outs, [at_odd_place(d) for d in grads])
+    for got, want in zip(seen[0], grads):
+        assert got.data_ptr() % 16 == 0 and torch.equal(got, want)
