@@ -133,9 +133,9 @@ def _glr_forward(x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seq
 class _Glr(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens, flags):
-        out, final, ctx.states = _glr_forward(x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens,
-                                              flags, True)
-        ctx.save_for_backward(x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens)
+        out, final, states = _glr_forward(x, raw_gate, A_log, dt_bias, initial_state, lower_bound, cu_seqlens, flags,
+                                          True)
+        ctx.save_for_backward(x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens, states)
         ctx.lower_bound, ctx.flags = lower_bound, flags
         ctx.set_materialize_grads(False)
         return out, final
@@ -143,14 +143,14 @@ class _Glr(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_out, d_final):
-        x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
+        x, raw_gate, A_log, dt_bias, initial_state, cu_seqlens, states = ctx.saved_tensors
         B, T, H, K = x.shape
         d_out = _grad(d_out, x)
         d_final = None if d_final is None else _as_taken(d_final, torch.float32)
         dx, dg = torch.empty_like(x), torch.empty_like(raw_gate)
         dA, dd = (None if t is None else torch.empty_like(t) for t in (A_log, dt_bias))
         di = None if initial_state is None else torch.empty_like(initial_state)
-        kda_glr_bwd(x, raw_gate, ctx.states, d_out, dx, dg, dA, dd,
+        kda_glr_bwd(x, raw_gate, states, d_out, dx, dg, dA, dd,
                     _scratch(kda_glr_bwd_workspace_size(B * T, H, K), x), A_log, dt_bias, ctx.lower_bound,
                     initial_state, d_final, di, cu_seqlens, ctx.flags)
         return dx, dg, dA, dd, di, None, None, None

@@ -1,6 +1,8 @@
 """The differentiable wrappers of the operators around the core, on the CPU: what they hand to the
 library's calls, which are replaced here, and what autograd sees of them."""
 
+import weakref
+
 import pytest
 import torch
 import torch.autograd.forward_ad as forward_ad
@@ -90,3 +92,29 @@ def test_gradients_of_the_core_may_arrive_at_any_address(monkeypatch):
     torch.autograd.backward(outs, [at_odd_place(d) for d in grads])
     for got, want in zip(seen[0], grads):
         assert got.data_ptr() % 16 == 0 and torch.equal(got, want)
+
+
+def test_the_recurrences_states_are_saved_tensors(library):
+    """What the forward leaves for the backward is seen by saved-tensor hooks and freed with the graph,
+    also while an output is still held."""
+    call, t = inputs()["glr"]
+    size = F.kda_glr_states_size(6, 2, 8)
+    packed = []
+
+    def pack(v):
+        packed.append(v)
+        return v
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda v: v):
+        outs = call(**{n: v.requires_grad_() for n, v in t.items()})
+    assert [v.numel() for v in packed if v.dtype is torch.uint8] == [size]
+    packed.clear()
+    outs = call(**t)
+    (_, states), _ = library["kda_glr_fwd"][-1][8:10], library.clear()
+    ref = weakref.ref(states.untyped_storage())
+    outs[0].float().sum().backward()
+    (args,) = library["kda_glr_bwd"]
+    assert args[2].data_ptr() == states.data_ptr()
+    del states, args
+    library.clear()
+    assert ref() is None and outs[0] is not None
