@@ -273,12 +273,15 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     projection's output will do); ``norm`` "l2" (x / sqrt(sum x^2 + eps), the core's), "rms"
     (x / sqrt(mean x^2 + eps)) or "none"; q_weight, k_weight fp32 [D] or None; positions int32
     [B,T] and inv_freq fp64 [R/2] (radians per position) turn the pairs (i, i + R/2) of the first
-    R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them.  With "l2" and no weights
+    R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them (inv_freq is not differentiated:
+    one that requires a gradient is refused).  With "l2" and no weights
     the results are unit rows, as ``kda_fwd_ex`` takes them with FLAG_NO_QK_NORM.  q and k start on a
     boundary of 4 elements, and so do their rows.
     """
     if norm not in _NORM:
         raise ValueError(f"norm must be one of {sorted(_NORM)}")
+    if inv_freq is not None and inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("inv_freq has no gradient here: pass inv_freq.detach()")
     args = (q, k, q_weight, k_weight, positions, inv_freq, float(eps),
             _NORM[norm] | (FLAG_INTERLEAVED if interleaved else 0))
-    return _QkNormRope.apply(*args) if _wants_derivative(q, k, q_weight, k_weight) else _qk_forward(*args)
+    return _QkNormRope.apply(*args) if _wants_derivative(q, k, q_weight, k_weight, inv_freq) else _qk_forward(*args)

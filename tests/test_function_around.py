@@ -118,3 +118,14 @@ def test_the_recurrences_states_are_saved_tensors(library):
     del states, args
     library.clear()
     assert ref() is None and outs[0] is not None
+
+
+def test_frequencies_that_want_a_derivative_are_refused(library):
+    """The rotation's frequencies have no gradient: asked for one, the call fails rather than leave it out."""
+    q, f, pos = torch.randn(1, 6, 2, 8, dtype=torch.bfloat16), torch.ones(4, dtype=torch.float64), torch.zeros(1, 6).int()
+    with pytest.raises(ValueError, match="inv_freq"):
+        F.kda_qk_norm_rope(q, q, pos, f.clone().requires_grad_())
+    with torch.no_grad():
+        F.kda_qk_norm_rope(q, q, pos, f.clone().requires_grad_())
+    with forward_ad.dual_level(), pytest.raises(NotImplementedError, match="jvp"):
+        F.kda_qk_norm_rope(q, q, pos, forward_ad.make_dual(f, f))
