@@ -21,7 +21,7 @@
 // always its map applied to its entering state, so the result has the same bits
 // however far back the search ends.  A tile waits only for tiles that running
 // workgroups took before it; the wait is bounded all the same, and one that
-// gives up sets the workspace's fault word.
+// gives up sets the workspace's fault word and takes NaN for the state.
 //
 // What bounds it: memory, where there are many columns.  At 32768 rows x 12288
 // channels of bf16 the pass takes 0.47 ms, 5.1 TB/s of its 6 bytes an element (a
@@ -341,8 +341,10 @@ __device__ __forceinline__ float look_back(const GlrArgs& a, Maps& maps, int k, 
       return s;
     }
   }
+  // Not a state that could be taken for one: the fault word is in a workspace
+  // that the caller may have let go of, a NaN stays to the sequence's end.
   if (ch == 0) atomicOr(a.faults, FAULT_WAIT_TIMEOUT);
-  return 0.f;
+  return __builtin_nanf("");
 }
 
 struct Tile {

@@ -471,7 +471,9 @@ typedef enum {
  * A NaN or infinity stays within its own sequence and channel.  Workgroups of
  * the call hand states to each other; a bounded wait that gives up sets
  * KDA_FAULT_WAIT_TIMEOUT in the workspace's fault word (kda_workspace_faults
- * reads it after kda_glr_fwd and kda_glr_bwd too).
+ * reads it after kda_glr_fwd and kda_glr_bwd too), and what would have needed
+ * the state is NaN from there to the end of its sequence (in the backward: to
+ * its start), so that the failure shows without the fault word.
  */
 size_t kda_glr_workspace_size(int64_t T_total, int64_t H, int64_t K);
 size_t kda_glr_states_size(int64_t T_total, int64_t H, int64_t K);

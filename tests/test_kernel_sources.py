@@ -39,3 +39,12 @@ def test_checked_accesses_have_no_scalar_offset(name, soffset):
             assert args[at] == "0", (name, kind, args)
             seen += 1
     assert seen == 4
+
+
+def test_a_wait_that_gives_up_leaves_no_number():
+    """The search for an entering state is bounded.  Where it ends without one it sets the fault word and
+    returns NaN: a zero would be taken for a state."""
+    with open(os.path.join(CSRC, "kda_glr.hip")) as f:
+        body = re.search(r"float look_back\(.*?\n}\n", f.read(), re.S).group(0)
+    fault = body.index("atomicOr(a.faults, FAULT_WAIT_TIMEOUT)")
+    assert re.findall(r"return (.*?);", body[fault:]) == ['__builtin_nanf("")']
