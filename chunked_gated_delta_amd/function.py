@@ -48,16 +48,16 @@ def _as_taken(g, dtype):
 class _KdaChunk(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, raw_gate, raw_beta, A_log, dt_bias, initial_state, scale, lower_bound,
-                cu_seqlens, reuse_records):
+                cu_seqlens, reuse_records, variant):
         B, T, H, K, V, N = _sizes(q, v, cu_seqlens)
         out = torch.empty_like(v)
         final_state = torch.empty(N, H, K, V, dtype=torch.float32, device=q.device)
         size = kda_bwd_workspace_size(B * T, H, N) if reuse_records else kda_workspace_size(B * T, H, N)
         ws = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
         kda_fwd_ex(q, k, v, raw_gate, raw_beta, scale, out, ws, A_log, dt_bias, lower_bound, initial_state,
-                   final_state, cu_seqlens, flags=FLAG_KEEP_RECORDS if reuse_records else 0)
+                   final_state, cu_seqlens, flags=variant | (FLAG_KEEP_RECORDS if reuse_records else 0))
         ctx.save_for_backward(q, k, v, raw_gate, raw_beta, A_log, dt_bias, initial_state, cu_seqlens)
-        ctx.scale, ctx.lower_bound = scale, lower_bound
+        ctx.scale, ctx.lower_bound, ctx.variant = scale, lower_bound, variant
         # the backward workspace starts with the forward's layout: keep it, records included
         ctx.ws = ws if reuse_records else None
         ctx.set_materialize_grads(False)
@@ -80,13 +80,13 @@ class _KdaChunk(torch.autograd.Function):
                                     device=q.device), 0
         kda_bwd_ex(q, k, v, raw_gate, raw_beta, ctx.scale, d_out, dq, dk, dv, draw_gate, draw_beta, dA_log,
                    ddt_bias, ws, A_log, dt_bias, ctx.lower_bound, initial_state=initial_state, d_final=d_final,
-                   d_initial_state=dinit, cu_seqlens=cu_seqlens, flags=flags)
+                   d_initial_state=dinit, cu_seqlens=cu_seqlens, flags=flags | ctx.variant)
         ctx.ws = None
-        return dq, dk, dv, draw_gate, draw_beta, dA_log, ddt_bias, dinit, None, None, None, None
+        return dq, dk, dv, draw_gate, draw_beta, dA_log, ddt_bias, dinit, None, None, None, None, None
 
 
 def kda_chunk(q, k, v, raw_gate, raw_beta, A_log, dt_bias, *, scale=None, lower_bound=-5.0,
-              initial_state=None, cu_seqlens=None, reuse_records=False):
+              initial_state=None, cu_seqlens=None, reuse_records=False, qk_normalized=False):
     """Differentiable KDA forward; returns (out bf16 [B,T,H,V], final_state fp32 [N,H,K,V]).
 
     Inputs as for ``kda_fwd``: q, k, v, raw_gate bf16 [B,T,H,*]; raw_beta bf16 [B,T,H];
@@ -100,11 +100,16 @@ def kda_chunk(q, k, v, raw_gate, raw_beta, A_log, dt_bias, *, scale=None, lower_
     It trades memory for time: the workspace (about 0.35 MB per chunk and head, 17 GB at
     T = 32768, H = 96) stays allocated from the forward to the backward, which uses the
     records up (a second backward would need the forward again).
+
+    ``qk_normalized`` takes q and k as they are (KDA_FLAG_NO_QK_NORM), for rows that already have
+    norm 1, as ``kda_qk_norm_rope`` makes with "l2" and no weights.  Without it each row is
+    normed here, also one that was scaled before, whose scale is lost.
     """
     if scale is None:
         scale = q.shape[-1] ** -0.5
     return _KdaChunk.apply(q, k, v, raw_gate, raw_beta, A_log, dt_bias, initial_state, float(scale),
-                           float(lower_bound), cu_seqlens, bool(reuse_records))
+                           float(lower_bound), cu_seqlens, bool(reuse_records),
+                           FLAG_NO_QK_NORM if qk_normalized else 0)
 
 
 def _scratch(size, like):
@@ -275,7 +280,9 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     [B,T] and inv_freq fp64 [R/2] (radians per position) turn the pairs (i, i + R/2) of the first
     R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them (inv_freq is not differentiated:
     one that requires a gradient is refused).  With "l2" and no weights
-    the results are unit rows, as ``kda_fwd_ex`` takes them with FLAG_NO_QK_NORM.  q and k start on a
+    the results are unit rows, as ``kda_chunk`` takes them with ``qk_normalized`` and ``kda_fwd_ex``
+    with FLAG_NO_QK_NORM; rows with weights or of "rms" are for layers without a norm of their own
+    (the core's takes their scale off again).  q and k start on a
     boundary of 4 elements, and so do their rows.
     """
     if norm not in _NORM:

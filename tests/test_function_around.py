@@ -129,3 +129,17 @@ def test_frequencies_that_want_a_derivative_are_refused(library):
         F.kda_qk_norm_rope(q, q, pos, f.clone().requires_grad_())
     with forward_ad.dual_level(), pytest.raises(NotImplementedError, match="jvp"):
         F.kda_qk_norm_rope(q, q, pos, forward_ad.make_dual(f, f))
+
+
+@pytest.mark.parametrize("reuse", [False, True])
+def test_the_core_takes_rows_that_are_normed_already(reuse, monkeypatch):
+    """qk_normalized is the library's flag in both directions, beside those of the records."""
+    flags = []
+    monkeypatch.setattr(F, "kda_fwd_ex", lambda *a, **k: flags.append(k["flags"]))
+    monkeypatch.setattr(F, "kda_bwd_ex", lambda *a, **k: flags.append(k["flags"]))
+    q, k, v, g = (torch.randn(1, 64, 1, 64, dtype=torch.bfloat16).requires_grad_() for _ in range(4))
+    rest = (torch.randn(1, 64, 1, dtype=torch.bfloat16), torch.zeros(1), torch.zeros(1, 64))
+    for normed, bit in ((False, 0), (True, F.FLAG_NO_QK_NORM)):
+        flags.clear()
+        F.kda_chunk(q, k, v, g, *rest, reuse_records=reuse, qk_normalized=normed)[0].float().sum().backward()
+        assert flags == [bit | (F.FLAG_KEEP_RECORDS if reuse else 0), bit | (F.FLAG_REUSE_RECORDS if reuse else 0)]
