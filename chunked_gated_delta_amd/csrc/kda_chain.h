@@ -162,6 +162,9 @@ __device__ __forceinline__ void store_vt_quarter(__bf16* sVt, const VTile<NQ>& v
 // place a compile-time or wave-uniform offset.  The lane offsets are
 // re-derived from an opaque thread id, so none of them stays live across the
 // chunk loop.  A null pointer leaves zeros (load) or writes nothing (store).
+// The 16-byte stores have a scalar offset, and the compiler then puts no wait
+// between them and a next write of their data.  S is not written after them:
+// they are a chain's last use of it, and the workgroup ends.
 template <bool STORE, int NQ>
 __device__ __forceinline__ void state_io(f32x4 (&S)[2][2 * NQ], const float* p, int vk, int seq, int h, int H,
                                          int vs) {

@@ -246,10 +246,14 @@ struct Rows {
       return __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, voff + off, 0, 0));
     }
   }
-  // The row's offset goes into the lane's: a 16-byte store with an offset in a
-  // scalar register reads its data late, and the compiler, which keeps the next
-  // write of those registers away from a store without one, does not do so
-  // there (seen as single wrong elements of fp32 outputs).
+  // With the row's offset in a scalar register, one build of the 16-byte store
+  // gave single wrong fp32 outputs: the first element of a lane's four.  The
+  // assembly of that build wrote the store's first data register in the very
+  // next instruction.  The compiler keeps such writes away from stores of more
+  // than 8 bytes, except from those with a scalar offset, which the public ISA
+  // guides exempt; that the exemption does not hold here is inferred from this
+  // one build and not otherwise established.  Without a scalar offset the
+  // question does not arise.
   __device__ __forceinline__ void store(int voff, int off, const float (&d)[4]) const {
     if constexpr (sizeof(T) == 2) {
       bf16x4 v;
