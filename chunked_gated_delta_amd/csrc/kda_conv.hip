@@ -14,9 +14,10 @@
 // then over tiles in a fixed order.
 //
 // All arithmetic is fp32.  The forward is bound by memory, 4 bytes an element in
-// bf16: 0.31 ms at 32768 rows x 12288 channels, 5.2 TB/s, a plain copy's rate.
-// The backward's 6 bytes an element come with 31 operations and two
-// transcendentals: 0.38 ms at 69141 x 4096, 4.4 TB/s.
+// bf16: 0.31 ms at 32768 rows x 12288 channels, 5.2 TB/s, a plain copy's rate
+// (fp32 0.62 ms, the same rate).  The backward's 6 bytes an element come with 31
+// operations and two transcendentals: 0.41 ms at 69141 x 4096, 4.1 TB/s (fp32
+// 0.92 ms, 3.7 TB/s).
 
 #include "../../include/kda.h"
 #include "kda_host.h"

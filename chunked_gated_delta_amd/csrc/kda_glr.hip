@@ -44,6 +44,14 @@
 // them without the waits for entering states, 0.53 if rows and results also
 // stayed in the caches.
 //
+// In fp32: forward 32768 x 6144 0.48 ms and 69141 x 4096 0.72 ms (4.8 TB/s),
+// backward there 1.10 ms (5.1 TB/s).
+//
+// Registers: the data waves' rows fill them.  The compiler spills two in the
+// bf16 forwards with formed gates, five and six in the fp32 backwards with
+// formed gates, none in the others; 50 to 97 scalar registers a kernel live in
+// lanes of a vector register instead of memory.
+//
 // All arithmetic is fp32.
 
 #include <limits.h>

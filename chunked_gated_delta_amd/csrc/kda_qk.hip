@@ -17,8 +17,11 @@
 // partners, so that a pair never leaves its lane.  A lane does up to HC heads
 // of one token with the same 4 sines and cosines.  The work is bound by
 // memory: 4 bytes an element forward in bf16, 0.57 ms at 32768 tokens x 192 heads
-// of 128 (5.7 TB/s), and 6 backward, 54 us at 8194 tokens x 40 heads (4.7 TB/s;
-// 95 us with the waiting rows held as fp32, which left three waves a SIMD).
+// of 128 (5.6 TB/s; fp32 1.15 ms, the same rate), and 6 backward, 53 us at 8194
+// tokens x 40 heads (4.7 TB/s; 95 us with the waiting rows held as fp32, which
+// left three waves a SIMD).  In fp32 four waves a SIMD leave the backward too few
+// registers: the compiler spills 43, and it takes 147 us there (3.4 TB/s) and
+// 1.10 ms at 16384 tokens x 192 heads (4.4 TB/s).
 
 #include "../../include/kda.h"
 #include "kda_host.h"
