@@ -102,8 +102,9 @@ def kda_chunk(q, k, v, raw_gate, raw_beta, A_log, dt_bias, *, scale=None, lower_
     records up (a second backward would need the forward again).
 
     ``qk_normalized`` takes q and k as they are (KDA_FLAG_NO_QK_NORM), for rows that already have
-    norm 1, as ``kda_qk_norm_rope`` makes with "l2" and no weights.  Without it each row is
-    normed here, also one that was scaled before, whose scale is lost.
+    norm 1, as ``kda_qk_norm_rope`` makes with "l2" and no weights.  That they do is not checked here
+    (``kda_fwd_ex`` records it in its workspace's fault word); longer rows give wrong results.
+    Without it each row is normed here, also one that was scaled before, whose scale is lost.
     """
     if scale is None:
         scale = q.shape[-1] ** -0.5
@@ -278,12 +279,13 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     projection's output will do); ``norm`` "l2" (x / sqrt(sum x^2 + eps), the core's), "rms"
     (x / sqrt(mean x^2 + eps)) or "none"; q_weight, k_weight fp32 [D] or None; positions int32
     [B,T] and inv_freq fp64 [R/2] (radians per position) turn the pairs (i, i + R/2) of the first
-    R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them (inv_freq is not differentiated:
-    one that requires a gradient is refused).  With "l2" and no weights
-    the results are unit rows, as ``kda_chunk`` takes them with ``qk_normalized`` and ``kda_fwd_ex``
-    with FLAG_NO_QK_NORM; rows with weights or of "rms" are for layers without a norm of their own
-    (the core's takes their scale off again).  q and k start on a
-    boundary of 4 elements, and so do their rows.
+    R channels, or (2i, 2i + 1) with ``interleaved``; None leaves them.  inv_freq is not
+    differentiated: one that requires a gradient is refused.  q and k start on a boundary of 4
+    elements, and so do their rows.
+
+    With "l2" and no weights the results are unit rows, as ``kda_chunk`` takes them with
+    ``qk_normalized`` and ``kda_fwd_ex`` with FLAG_NO_QK_NORM.  Rows with weights or of "rms" are for
+    layers without a norm of their own: the core's takes their scale off again.
     """
     if norm not in _NORM:
         raise ValueError(f"norm must be one of {sorted(_NORM)}")
