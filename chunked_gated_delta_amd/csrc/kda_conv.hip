@@ -516,6 +516,8 @@ kda_status_t kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, 
   if (a.ax.total > 0 && (!x || !out)) return KDA_ERR_INVALID;
   const size_t al = 4 * dtype_bytes(dtype);
   if (!aligned_all(al, {out, final_state})) return KDA_ERR_INVALID;
+  // (rows before a tile are another thread's to write, states another tile's)
+  if (same(out, x) || same(final_state, initial_state)) return KDA_ERR_INVALID;
   a.y = out;
   a.fin = final_state;
   return by_type<RunFwd>(dtype, W, a, reinterpret_cast<hipStream_t>(stream));
@@ -555,6 +557,8 @@ kda_status_t kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, 
   if (!aligned_all(al, {d_out, d_final, dx, d_initial_state}) || !aligned(workspace, 16))
     return KDA_ERR_INVALID;
   if (!workspace || workspace_bytes < kda_conv_bwd_workspace_size(a.ax.total, C, W)) return KDA_ERR_WORKSPACE;
+  if (same(dx, x) || same(dx, d_out) || same(d_initial_state, d_final) || same(d_initial_state, initial_state))
+    return KDA_ERR_INVALID;
   a.dy = d_out;
   a.d_final = d_final;
   a.y = dx;

@@ -1196,6 +1196,8 @@ kda_status_t kda_glr_fwd(const void* x, const void* raw_gate, void* out, void* w
     return KDA_ERR_INVALID;
   const GlrLayout l = glr_layout(a.ax.total, a.C, false);
   if (!workspace || workspace_bytes < l.total) return KDA_ERR_WORKSPACE;
+  // (a sequence's last tile may be written before its first reads the state again)
+  if (same(final_state, initial_state)) return KDA_ERR_INVALID;
   char* ws = static_cast<char*>(workspace);
   a.x = x;
   a.g = raw_gate;
@@ -1223,6 +1225,7 @@ kda_status_t kda_glr_bwd(const void* x, const void* raw_gate, const float* state
     return KDA_ERR_INVALID;
   const GlrLayout l = glr_layout(a.ax.total, a.C, true);
   if (!workspace || workspace_bytes < l.total) return KDA_ERR_WORKSPACE;
+  if (same(d_initial_state, d_final) || same(d_initial_state, initial_state)) return KDA_ERR_INVALID;
   char* ws = static_cast<char*>(workspace);
   a.x = x;
   a.g = raw_gate;

@@ -191,6 +191,10 @@ inline bool aligned_all(size_t bytes, std::initializer_list<const void*> ps) {
   return true;
 }
 
+// Whether two arrays that were given are the same one: an output that another
+// workgroup's reads would still need as an input.
+inline bool same(const void* a, const void* b) { return a && a == b; }
+
 // Bytes that an element of a token array has, 0 for a type that is none.
 inline size_t dtype_bytes(int dtype) { return dtype == 0 ? 2 : dtype == 1 ? 4 : 0; }
 

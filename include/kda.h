@@ -421,7 +421,9 @@ kda_status_t kda_fwd_noalloc(const void* q, const void* k, const void* v, const 
  *                are written as zeros).
  *   alignment    token arrays and states: 4 elements; fp32 parameters,
  *                fp32 states and workspaces: 16 bytes (KDA_ERR_INVALID).
- * Outputs must not overlap inputs or each other except where stated.
+ * Outputs must not overlap inputs or each other except where stated; a state
+ * (or, in the convolution, a token array) given as input and output of one
+ * call that is not a step is refused (KDA_ERR_INVALID).
  */
 typedef enum {
   KDA_DTYPE_BF16 = 0,
