@@ -33,7 +33,8 @@ __all__ = ["kda_fwd", "kda_fwd_ex", "kda_workspace_size", "kda_is_supported", "k
            "FLAG_RMS_NORM", "FLAG_INTERLEAVED", "FLAG_ZERO_REST", "kda_glr_fwd", "kda_glr_bwd", "kda_glr_step",
            "kda_glr_workspace_size", "kda_glr_states_size", "kda_glr_bwd_workspace_size", "kda_conv_fwd",
            "kda_conv_bwd", "kda_conv_step", "kda_conv_bwd_workspace_size", "kda_qk_rope_fwd", "kda_qk_rope_bwd",
-           "kda_qk_rope_bwd_workspace_size"]
+           "kda_qk_rope_bwd_workspace_size", "kda_la_fwd", "kda_la_bwd", "kda_la_step", "kda_la_workspace_size",
+           "kda_la_bwd_workspace_size"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libkda.so")
@@ -46,7 +47,8 @@ exported_symbols = ("kda_fwd", "kda_workspace_size", "kda_is_supported", "kda_st
                     "kda_glr_fwd", "kda_glr_bwd", "kda_glr_step", "kda_glr_workspace_size", "kda_glr_states_size",
                     "kda_glr_bwd_workspace_size", "kda_conv_fwd", "kda_conv_bwd", "kda_conv_step",
                     "kda_conv_bwd_workspace_size", "kda_qk_rope_fwd", "kda_qk_rope_bwd",
-                    "kda_qk_rope_bwd_workspace_size")
+                    "kda_qk_rope_bwd_workspace_size", "kda_la_fwd", "kda_la_bwd", "kda_la_step",
+                    "kda_la_workspace_size", "kda_la_bwd_workspace_size")
 # kda_fwd_ex variant bits (KDA_FLAG_* in include/kda.h)
 FLAG_GATE_GIVEN, FLAG_BETA_GIVEN, FLAG_NO_QK_NORM, FLAG_STATE_VK = 1, 2, 4, 8
 # kda_fwd_ex, kda_bwd_ex: reuse the chunk records the previous call left in the workspace
@@ -123,12 +125,16 @@ for _name, _args in {
     "kda_conv_step": [_P, _I64] + [_P] * 5 + [_I64] * 4 + [_I, _U, _P],
     "kda_qk_rope_fwd": [_P, _I64, _I64] * 2 + [_P] * 6 + [_F] + [_I64] * 5 + [_I, _U, _P],
     "kda_qk_rope_bwd": [_P, _I64, _I64] * 2 + [_P] * 7 + [_SZ] + [_P] * 4 + [_F] + [_I64] * 5 + [_I, _U, _P],
+    "kda_la_fwd": [_P, _I64, _I64] * 3 + [_P, _F, _P, _P, _SZ, _P, _P, _P] + [_I64] * 6 + [_U, _P],
+    "kda_la_bwd": [_P, _I64, _I64] * 3 + [_P, _F] + [_P] * 8 + [_SZ, _P, _P] + [_I64] * 6 + [_U, _P],
+    "kda_la_step": [_P, _I64, _I64] * 3 + [_P, _F, _P, _P, _P] + [_I64] * 5 + [_P],
 }.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = _I
     _FN[_name] = getattr(_lib, _name)
 for _name, _n in {"kda_glr_workspace_size": 3, "kda_glr_states_size": 3, "kda_glr_bwd_workspace_size": 3,
-                  "kda_conv_bwd_workspace_size": 3, "kda_qk_rope_bwd_workspace_size": 4}.items():
+                  "kda_conv_bwd_workspace_size": 3, "kda_qk_rope_bwd_workspace_size": 4,
+                  "kda_la_workspace_size": 4, "kda_la_bwd_workspace_size": 5}.items():
     getattr(_lib, _name).argtypes = [_I64] * _n
     getattr(_lib, _name).restype = _SZ
 
@@ -616,6 +622,83 @@ def kda_qk_rope_bwd(q, k, d_q_out, d_k_out, dq, dk, positions, inv_freq, eps=1e-
           c.token(dk, "dk", q.dtype, k.shape), c.option(d_q_weight, "d_q_weight", torch.float32, (D,)),
           c.option(d_k_weight, "d_k_weight", torch.float32, (D,)), ws, size, pqw, pkw, ppos, pf, float(eps), B * T,
           Hq, Hk, D, R, ty, int(flags))
+
+
+# ---------------------------------------------------------------------------
+# token mixers beside the core
+# ---------------------------------------------------------------------------
+def _heads(c, t, name, shape):
+    """Pointer, token stride and head stride of a bf16 token array [B, T, H, channels] whose tokens and
+    heads lie evenly apart."""
+    p = c.token(t, name, torch.bfloat16, shape, contiguous=False)
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return p, _row_stride(t, name), t.stride(2) if t.shape[2] > 1 else t.shape[3]
+
+
+def _la(q, k, v, log_decay):
+    c = _Call(q, "q")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, H, channels]")
+    B, T, H, K = q.shape
+    V = v.shape[3]
+    return c, B, T, H, K, V, [*_heads(c, q, "q", q.shape), *_heads(c, k, "k", q.shape),
+                              *_heads(c, v, "v", (B, T, H, V)), c.token(log_decay, "log_decay", torch.float32, (H,))]
+
+
+def kda_la_workspace_size(T: int, H: int, K: int, V: int) -> int:
+    """Workspace bytes of kda_la_fwd for T packed tokens and H heads of K and V channels."""
+    return int(_lib.kda_la_workspace_size(T, H, K, V))
+
+
+def kda_la_bwd_workspace_size(T: int, H: int, K: int, V: int, N: int) -> int:
+    """Workspace bytes of kda_la_bwd for T packed tokens, H heads of K and V channels and N sequences."""
+    return int(_lib.kda_la_bwd_workspace_size(T, H, K, V, N))
+
+
+def kda_la_fwd(q, k, v, log_decay, scale, out, workspace, initial_state=None, final_state=None, cu_seqlens=None, flags=0,
+               stream=None):
+    """Enqueue linear attention with a decay for each head, S_t = exp(log_decay) S_{t-1} + k_t v_t^T,
+    out_t = scale S_t^T q_t, on ``stream`` (default: torch's current stream).
+
+    q, k bf16 [B,T,H,K], v bf16 [B,T,H,V], tokens and heads evenly apart; K and V 64 or 128; log_decay
+    fp32 [H], at most 0; out bf16 [B,T,H,V]; workspace >= kda_la_workspace_size(B*T, H, K, V) bytes;
+    initial_state / final_state fp32 [N,H,K,V] or None; cu_seqlens int32 [N+1] or None; flags 0 or
+    FLAG_ZERO_REST."""
+    c, B, T, H, K, V, p = _la(q, k, v, log_decay)
+    N, pcu = _sequences(cu_seqlens, c, B)
+    ws, size = _bytes(c, workspace)
+    st = (N, H, K, V)
+    c.run("kda_la_fwd", stream, *p, float(scale), c.token(out, "out", torch.bfloat16, v.shape), ws, size,
+          c.option(initial_state, "initial_state", torch.float32, st),
+          c.option(final_state, "final_state", torch.float32, st), pcu, B, T, H, K, V, N, int(flags))
+
+
+def kda_la_bwd(q, k, v, log_decay, scale, d_out, dq, dk, dv, workspace, d_log_decay=None, initial_state=None, d_final=None,
+               d_initial_state=None, cu_seqlens=None, flags=0, stream=None):
+    """Enqueue the gradients of a kda_la_fwd call with the same inputs, for d_out bf16 [B,T,H,V] and
+    d_final (fp32 [N,H,K,V], None for zero).  Writes dq, dk, dv (bf16, contiguous) and, if given,
+    d_log_decay (fp32 [H]) and d_initial_state; workspace >= kda_la_bwd_workspace_size(B*T, H, K, V, N)
+    bytes."""
+    c, B, T, H, K, V, p = _la(q, k, v, log_decay)
+    N, pcu = _sequences(cu_seqlens, c, B)
+    ws, size = _bytes(c, workspace)
+    st, bf = (N, H, K, V), torch.bfloat16
+    c.run("kda_la_bwd", stream, *p, float(scale), c.token(d_out, "d_out", bf, v.shape),
+          c.option(d_final, "d_final", torch.float32, st), c.token(dq, "dq", bf, q.shape), c.token(dk, "dk", bf, q.shape),
+          c.token(dv, "dv", bf, v.shape), c.option(d_log_decay, "d_log_decay", torch.float32, (H,)),
+          c.option(d_initial_state, "d_initial_state", torch.float32, st), ws, size,
+          c.option(initial_state, "initial_state", torch.float32, st), pcu, B, T, H, K, V, N, int(flags))
+
+
+def kda_la_step(q, k, v, log_decay, scale, out, initial_state=None, final_state=None, stream=None):
+    """Enqueue linear attention over B sequences of T tokens each (decoding): one launch, no workspace;
+    states fp32 [B,H,K,V], final_state may be initial_state for an in-place update."""
+    c, B, T, H, K, V, p = _la(q, k, v, log_decay)
+    st = (B, H, K, V)
+    c.run("kda_la_step", stream, *p, float(scale), c.token(out, "out", torch.bfloat16, v.shape),
+          c.option(initial_state, "initial_state", torch.float32, st),
+          c.option(final_state, "final_state", torch.float32, st), B, T, H, K, V)
 
 
 def raw_call(*args):

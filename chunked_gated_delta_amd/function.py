@@ -25,10 +25,11 @@ from torch.autograd import forward_ad
 from . import (FLAG_COMPLEMENT, FLAG_GATE_GIVEN, FLAG_INTERLEAVED, FLAG_KEEP_RECORDS, FLAG_NO_QK_NORM,
                FLAG_REUSE_RECORDS, FLAG_RMS_NORM, FLAG_SILU, FLAG_ZERO_REST, kda_bwd_ex, kda_bwd_workspace_size, kda_conv_bwd,
                kda_conv_bwd_workspace_size, kda_conv_fwd, kda_fwd_ex, kda_glr_bwd, kda_glr_bwd_workspace_size,
-               kda_glr_fwd, kda_glr_states_size, kda_glr_workspace_size, kda_qk_rope_bwd,
+               kda_glr_fwd, kda_glr_states_size, kda_glr_workspace_size, kda_la_bwd, kda_la_bwd_workspace_size,
+               kda_la_fwd, kda_la_workspace_size, kda_qk_rope_bwd,
                kda_qk_rope_bwd_workspace_size, kda_qk_rope_fwd, kda_workspace_size)
 
-__all__ = ["kda_chunk", "kda_glr", "kda_short_conv", "kda_qk_norm_rope"]
+__all__ = ["kda_chunk", "kda_glr", "kda_short_conv", "kda_qk_norm_rope", "kda_linear_attn"]
 
 
 def _sizes(q, v, cu_seqlens):
@@ -294,3 +295,52 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     args = (q, k, q_weight, k_weight, positions, inv_freq, float(eps),
             _NORM[norm] | (FLAG_INTERLEAVED if interleaved else 0))
     return _QkNormRope.apply(*args) if _wants_derivative(q, k, q_weight, k_weight, inv_freq) else _qk_forward(*args)
+
+
+def _la_forward(q, k, v, log_decay, initial_state, scale, cu_seqlens):
+    B, T, H, K = q.shape
+    V = v.shape[3]
+    out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    final = torch.empty(_count(q, cu_seqlens), H, K, V, dtype=torch.float32, device=q.device)
+    kda_la_fwd(q, k, v, log_decay, scale, out, _scratch(kda_la_workspace_size(B * T, H, K, V), q), initial_state, final,
+               cu_seqlens, FLAG_ZERO_REST)
+    return out, final
+
+
+class _LinearAttn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, initial_state, scale, cu_seqlens):
+        ctx.save_for_backward(q, k, v, log_decay, initial_state, cu_seqlens)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return _la_forward(q, k, v, log_decay, initial_state, scale, cu_seqlens)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_final):
+        q, k, v, log_decay, initial_state, cu_seqlens = ctx.saved_tensors
+        B, T, H, K = q.shape
+        d_final = None if d_final is None else _as_taken(d_final, torch.float32)
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        dg = torch.empty_like(log_decay) if ctx.needs_input_grad[3] else None
+        di = torch.empty_like(initial_state) if ctx.needs_input_grad[4] else None
+        N = _count(q, cu_seqlens)
+        ws = _scratch(kda_la_bwd_workspace_size(B * T, H, K, v.shape[3], N), q)
+        kda_la_bwd(q, k, v, log_decay, ctx.scale, _grad(d_out, v), dq, dk, dv, ws, dg, initial_state, d_final, di,
+                   cu_seqlens, FLAG_ZERO_REST)
+        return dq, dk, dv, dg, di, None, None
+
+
+def kda_linear_attn(q, k, v, log_decay, *, scale=None, initial_state=None, cu_seqlens=None):
+    """Differentiable linear attention with a decay for each head, S_t = exp(log_decay) S_{t-1} + k_t v_t^T
+    and out_t = scale S_t^T q_t; returns (out bf16 [B,T,H,V], final_state fp32 [N,H,K,V]).
+
+    q, k bf16 [B,T,H,K], v bf16 [B,T,H,V], K and V each 64 or 128, tokens and heads evenly apart (slices
+    of one projection's output, or one head's rows expanded to all, will do); log_decay fp32 [H], at
+    most 0 (minus infinity: nothing is kept), with a gradient if it requires one; ``scale`` defaults to
+    K^-1/2; initial_state fp32 [N,H,K,V] or None for zeros; cu_seqlens int32 [N+1] (with B = 1) or
+    None; rows behind the last sequence come back as zeros.  All tensors on one GPU, unchanged until the
+    backward, and on a boundary of 16 bytes, rows and heads too (KdaError otherwise).
+    """
+    args = (q, k, v, log_decay, initial_state, float(q.shape[-1] ** -0.5 if scale is None else scale), cu_seqlens)
+    return _LinearAttn.apply(*args) if _wants_derivative(q, k, v, log_decay, initial_state) else _la_forward(*args)

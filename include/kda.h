@@ -601,6 +601,71 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
                              const double* inv_freq, float eps, int64_t tokens, int64_t Hq, int64_t Hk, int64_t D,
                              int64_t R, int dtype, unsigned flags, void* stream);
 
+/*
+ * Token mixers beside the KDA core, in the manner of the operators around it:
+ * caller-owned device pointers, nothing allocated or synchronised, no memset
+ * recorded (so capturable), the same bits from run to run, and cu_seqlens that
+ * may end before T (KDA_FLAG_ZERO_REST: rows behind become zeros).
+ *   token arrays  bf16, contiguous where no strides are given.  Strides are in
+ *                 elements, between tokens (the tokens of one sequence after
+ *                 those of the one before) and between heads: multiples of 8
+ *                 from 0 to 2^23, so that slices of one projection's output or
+ *                 one head's rows for all heads will do.
+ *   alignment     16 bytes for token arrays, states and workspaces
+ * A workspace belongs to one call at a time: calls (and graphs) that may
+ * overlap need their own.
+ */
+
+/*
+ * Linear attention with one decay for each head,
+ *     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t.
+ *
+ *   q, k          [B, T, H, K];  v [B, T, H, V];  K, V each 64 or 128
+ *   log_decay     fp32 [H], natural logarithm per token, at most 0 (minus
+ *                 infinity: nothing is kept).  Values above 0 are not refused;
+ *                 the states then grow, and overflow where the formula does.
+ *   out           [B, T, H, V] written, contiguous
+ *   workspace     scratch of >= kda_la_workspace_size(B * T, H, K, V) bytes
+ *   initial_state fp32 [N, H, K, V] or NULL for zeros
+ *   final_state   fp32 [N, H, K, V] written, or NULL; not initial_state
+ *   scale         finite
+ *   flags         0 or KDA_FLAG_ZERO_REST
+ * A NaN or infinity stays within its own sequence and head; it reaches tokens
+ * up to 63 before its own, too (a step's tokens are multiplied together).
+ */
+size_t kda_la_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V);
+kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                        int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                        const float* log_decay, float scale, void* out, void* workspace, size_t workspace_bytes,
+                        const float* initial_state, float* final_state, const int32_t* cu_seqlens, int64_t B, int64_t T,
+                        int64_t H, int64_t K, int64_t V, int64_t N, unsigned flags, void* stream);
+
+/*
+ * Gradients of kda_la_fwd for loss = <d_out, out> + <d_final, final_state>.
+ *   d_out         [B, T, H, V], contiguous;  d_final fp32 [N, H, K, V] or NULL for zero
+ *   dq, dk, dv    [B, T, H, K], [B, T, H, K], [B, T, H, V] written, contiguous
+ *   d_log_decay   fp32 [H] written, or NULL (which saves about a sixth of the time)
+ *   d_initial_state fp32 [N, H, K, V] written, or NULL
+ *   workspace     >= kda_la_bwd_workspace_size(B * T, H, K, V, N) bytes
+ */
+size_t kda_la_bwd_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V, int64_t N);
+kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                        int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                        const float* log_decay, float scale, const void* d_out, const float* d_final, void* dq, void* dk,
+                        void* dv, float* d_log_decay, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                        const float* initial_state, const int32_t* cu_seqlens, int64_t B, int64_t T, int64_t H,
+                        int64_t K, int64_t V, int64_t N, unsigned flags, void* stream);
+
+/*
+ * Linear attention for decoding: B sequences of T tokens each (T small, at most
+ * 2^20), in one launch without a workspace.  States fp32 [B, H, K, V];
+ * final_state may equal initial_state (the in-place update) or be NULL.
+ */
+kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                         int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                         const float* log_decay, float scale, void* out, const float* initial_state, float* final_state,
+                         int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* kda_status_string(kda_status_t status);
 
