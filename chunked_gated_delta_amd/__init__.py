@@ -34,7 +34,8 @@ __all__ = ["kda_fwd", "kda_fwd_ex", "kda_workspace_size", "kda_is_supported", "k
            "kda_glr_workspace_size", "kda_glr_states_size", "kda_glr_bwd_workspace_size", "kda_conv_fwd",
            "kda_conv_bwd", "kda_conv_step", "kda_conv_bwd_workspace_size", "kda_qk_rope_fwd", "kda_qk_rope_bwd",
            "kda_qk_rope_bwd_workspace_size", "kda_la_fwd", "kda_la_bwd", "kda_la_step", "kda_la_workspace_size",
-           "kda_la_bwd_workspace_size"]
+           "kda_la_bwd_workspace_size", "kda_attn_fwd", "kda_attn_bwd", "kda_attn_workspace_size",
+           "kda_attn_bwd_workspace_size"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libkda.so")
@@ -48,7 +49,8 @@ exported_symbols = ("kda_fwd", "kda_workspace_size", "kda_is_supported", "kda_st
                     "kda_glr_bwd_workspace_size", "kda_conv_fwd", "kda_conv_bwd", "kda_conv_step",
                     "kda_conv_bwd_workspace_size", "kda_qk_rope_fwd", "kda_qk_rope_bwd",
                     "kda_qk_rope_bwd_workspace_size", "kda_la_fwd", "kda_la_bwd", "kda_la_step",
-                    "kda_la_workspace_size", "kda_la_bwd_workspace_size")
+                    "kda_la_workspace_size", "kda_la_bwd_workspace_size", "kda_attn_fwd", "kda_attn_bwd",
+                    "kda_attn_workspace_size", "kda_attn_bwd_workspace_size")
 # kda_fwd_ex variant bits (KDA_FLAG_* in include/kda.h)
 FLAG_GATE_GIVEN, FLAG_BETA_GIVEN, FLAG_NO_QK_NORM, FLAG_STATE_VK = 1, 2, 4, 8
 # kda_fwd_ex, kda_bwd_ex: reuse the chunk records the previous call left in the workspace
@@ -128,13 +130,16 @@ for _name, _args in {
     "kda_la_fwd": [_P, _I64, _I64] * 3 + [_P, _F, _P, _P, _SZ, _P, _P, _P] + [_I64] * 6 + [_U, _P],
     "kda_la_bwd": [_P, _I64, _I64] * 3 + [_P, _F] + [_P] * 8 + [_SZ, _P, _P] + [_I64] * 6 + [_U, _P],
     "kda_la_step": [_P, _I64, _I64] * 3 + [_P, _F, _P, _P, _P] + [_I64] * 5 + [_P],
+    "kda_attn_fwd": [_P, _I64, _I64] * 3 + [_F, _P, _P, _P, _P, _SZ, _P, _P] + [_I64] * 7 + [_U, _P],
+    "kda_attn_bwd": [_P, _I64, _I64] * 3 + [_F] + [_P] * 9 + [_SZ, _P, _P] + [_I64] * 7 + [_U, _P],
 }.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = _I
     _FN[_name] = getattr(_lib, _name)
 for _name, _n in {"kda_glr_workspace_size": 3, "kda_glr_states_size": 3, "kda_glr_bwd_workspace_size": 3,
                   "kda_conv_bwd_workspace_size": 3, "kda_qk_rope_bwd_workspace_size": 4,
-                  "kda_la_workspace_size": 4, "kda_la_bwd_workspace_size": 5}.items():
+                  "kda_la_workspace_size": 4, "kda_la_bwd_workspace_size": 5,
+                  "kda_attn_workspace_size": 6, "kda_attn_bwd_workspace_size": 2}.items():
     getattr(_lib, _name).argtypes = [_I64] * _n
     getattr(_lib, _name).restype = _SZ
 
@@ -699,6 +704,62 @@ def kda_la_step(q, k, v, log_decay, scale, out, initial_state=None, final_state=
     c.run("kda_la_step", stream, *p, float(scale), c.token(out, "out", torch.bfloat16, v.shape),
           c.option(initial_state, "initial_state", torch.float32, st),
           c.option(final_state, "final_state", torch.float32, st), B, T, H, K, V)
+
+
+def _attn(q, k, v, cu_seqlens_q, cu_seqlens_k):
+    c = _Call(q, "q")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, H, D]")
+    B, Tq, Hq, D = q.shape
+    Tk, Hk = k.shape[1:3]
+    p = [*_heads(c, q, "q", q.shape), *_heads(c, k, "k", (B, Tk, Hk, D)), *_heads(c, v, "v", (B, Tk, Hk, D))]
+    if (cu_seqlens_q is None) != (cu_seqlens_k is None):
+        raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
+    N, pq = _sequences(cu_seqlens_q, c, B)
+    Nk, pk = _sequences(cu_seqlens_k, c, B)
+    if N != Nk:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+    return c, (B, Tq, Tk, Hq, Hk, D, N), p, pq, pk
+
+
+def kda_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, N: int) -> int:
+    """Workspace bytes of kda_attn_fwd for Tq packed queries and Tk packed keys of N sequences."""
+    return int(_lib.kda_attn_workspace_size(Tq, Tk, Hq, Hk, D, N))
+
+
+def kda_attn_bwd_workspace_size(Tq: int, Hq: int) -> int:
+    """Workspace bytes of kda_attn_bwd for Tq packed queries of Hq heads."""
+    return int(_lib.kda_attn_bwd_workspace_size(Tq, Hq))
+
+
+def kda_attn_fwd(q, k, v, scale, out, lse, workspace, out_lo=None, cu_seqlens_q=None, cu_seqlens_k=None, flags=0,
+                 stream=None):
+    """Enqueue causal softmax attention on ``stream`` (default: torch's current stream): query i of a
+    sequence of nq queries and nk keys sees the keys j <= i + nk - nq.
+
+    q bf16 [B,Tq,Hq,D], k, v bf16 [B,Tk,Hk,D], tokens and heads evenly apart, D 64 or 128, Hq a multiple
+    of Hk; out bf16 [B,Tq,Hq,D]; out_lo the same for kda_attn_bwd (what out's rounding took off), or
+    None; lse fp32 [B,Tq,Hq]; workspace >= kda_attn_workspace_size(B*Tq, B*Tk, Hq,
+    Hk, D, N) bytes; cu_seqlens_q, cu_seqlens_k int32 [N+1] (the same one for prompts without a past)
+    or None; flags 0 or FLAG_ZERO_REST."""
+    c, sizes, p, pq, pk = _attn(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    ws, size = _bytes(c, workspace)
+    c.run("kda_attn_fwd", stream, *p, float(scale), c.token(out, "out", torch.bfloat16, q.shape),
+          c.option(out_lo, "out_lo", torch.bfloat16, q.shape), c.token(lse, "lse", torch.float32, q.shape[:3]), ws, size, pq, pk, *sizes, int(flags))
+
+
+def kda_attn_bwd(q, k, v, scale, out, out_lo, lse, d_out, dq, dk, dv, workspace, d_lse=None, cu_seqlens_q=None,
+                 cu_seqlens_k=None, flags=0, stream=None):
+    """Enqueue the gradients of a kda_attn_fwd call with the same inputs, which wrote out, out_lo and lse,
+    for d_out bf16 [B,Tq,Hq,D] and d_lse (fp32 [B,Tq,Hq], None for zero).  Writes dq, dk and dv (bf16,
+    contiguous); workspace >= kda_attn_bwd_workspace_size(B*Tq, Hq) bytes."""
+    c, sizes, p, pq, pk = _attn(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    ws, size = _bytes(c, workspace)
+    bf, ls = torch.bfloat16, q.shape[:3]
+    c.run("kda_attn_bwd", stream, *p, float(scale), c.token(out, "out", bf, q.shape),
+          c.token(out_lo, "out_lo", bf, q.shape), c.token(lse, "lse", torch.float32, ls), c.token(d_out, "d_out", bf, q.shape),
+          c.option(d_lse, "d_lse", torch.float32, ls), c.token(dq, "dq", bf, q.shape), c.token(dk, "dk", bf, k.shape),
+          c.token(dv, "dv", bf, k.shape), ws, size, pq, pk, *sizes, int(flags))
 
 
 def raw_call(*args):

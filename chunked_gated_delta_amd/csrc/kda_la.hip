@@ -28,7 +28,7 @@
 // Precision: products of bf16 inputs are exact in the fp32 accumulators.  Where
 // an fp32 value has to be an MFMA operand it is split into bf16 parts: z times
 // its decay into three (the states are fp32 results), the pair weights and the
-// entering state into two (2^-17, below the bf16 output's 2^-9; the decay's
+// entering state into two (2^-16, where the bf16 output has 2^-8; the decay's
 // gradient is an fp32 result again, and takes three).  A sum of one bf16 part
 // would add errors as large as the output's own rounding.
 

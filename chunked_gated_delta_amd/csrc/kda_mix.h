@@ -23,8 +23,8 @@ __device__ __forceinline__ bf16x8 join(uint2 a, uint2 b) {
   return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
 }
 
-// The next bf16 part of x, taken off it: two parts leave an error below 2^-17
-// of x, three one below 2^-25.
+// The next bf16 part of x, taken off it: two parts leave an error of at most
+// 2^-16 of x, three one of 2^-24.
 __device__ __forceinline__ bf16x4 cut_part(float (&x)[4]) {
   bf16x4 p;
 #pragma unroll

@@ -23,13 +23,14 @@ import torch
 from torch.autograd import forward_ad
 
 from . import (FLAG_COMPLEMENT, FLAG_GATE_GIVEN, FLAG_INTERLEAVED, FLAG_KEEP_RECORDS, FLAG_NO_QK_NORM,
-               FLAG_REUSE_RECORDS, FLAG_RMS_NORM, FLAG_SILU, FLAG_ZERO_REST, kda_bwd_ex, kda_bwd_workspace_size, kda_conv_bwd,
+               FLAG_REUSE_RECORDS, FLAG_RMS_NORM, FLAG_SILU, FLAG_ZERO_REST, kda_attn_bwd,
+               kda_attn_bwd_workspace_size, kda_attn_fwd, kda_attn_workspace_size, kda_bwd_ex, kda_bwd_workspace_size, kda_conv_bwd,
                kda_conv_bwd_workspace_size, kda_conv_fwd, kda_fwd_ex, kda_glr_bwd, kda_glr_bwd_workspace_size,
                kda_glr_fwd, kda_glr_states_size, kda_glr_workspace_size, kda_la_bwd, kda_la_bwd_workspace_size,
                kda_la_fwd, kda_la_workspace_size, kda_qk_rope_bwd,
                kda_qk_rope_bwd_workspace_size, kda_qk_rope_fwd, kda_workspace_size)
 
-__all__ = ["kda_chunk", "kda_glr", "kda_short_conv", "kda_qk_norm_rope", "kda_linear_attn"]
+__all__ = ["kda_chunk", "kda_glr", "kda_short_conv", "kda_qk_norm_rope", "kda_linear_attn", "kda_attn"]
 
 
 def _sizes(q, v, cu_seqlens):
@@ -344,3 +345,55 @@ def kda_linear_attn(q, k, v, log_decay, *, scale=None, initial_state=None, cu_se
     """
     args = (q, k, v, log_decay, initial_state, float(q.shape[-1] ** -0.5 if scale is None else scale), cu_seqlens)
     return _LinearAttn.apply(*args) if _wants_derivative(q, k, v, log_decay, initial_state) else _la_forward(*args)
+
+
+def _attn_forward(q, k, v, scale, cu_q, cu_k, out_lo=None):
+    B, Tq, Hq, D = q.shape
+    Tk, Hk = k.shape[1:3]
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    ws = _scratch(kda_attn_workspace_size(B * Tq, B * Tk, Hq, Hk, D, _count(q, cu_q)), q)
+    kda_attn_fwd(q, k, v, scale, out, lse, ws, out_lo, cu_q, cu_k, FLAG_ZERO_REST)
+    return out, lse
+
+
+class _Attn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, scale, cu_q, cu_k):
+        out_lo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out, lse = _attn_forward(q, k, v, scale, cu_q, cu_k, out_lo)
+        ctx.save_for_backward(q, k, v, out, out_lo, lse, cu_q, cu_k)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return out, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_lse):
+        q, k, v, out, out_lo, lse, cu_q, cu_k = ctx.saved_tensors
+        d_lse = None if d_lse is None else _as_taken(d_lse, torch.float32)
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        ws = _scratch(kda_attn_bwd_workspace_size(q.shape[0] * q.shape[1], q.shape[2]), q)
+        kda_attn_bwd(q, k, v, ctx.scale, out, out_lo, lse, _grad(d_out, q), dq, dk, dv, ws, d_lse, cu_q, cu_k,
+                     FLAG_ZERO_REST)
+        return dq, dk, dv, None, None, None
+
+
+def kda_attn(q, k, v, *, scale=None, cu_seqlens=None, cu_seqlens_k=None):
+    """Differentiable causal softmax attention, for the full-attention layers between linear ones;
+    returns (out bf16 [B,Tq,Hq,D], lse fp32 [B,Tq,Hq], the natural logarithm of each row's sum).
+
+    q bf16 [B,Tq,Hq,D], k, v bf16 [B,Tk,Hk,D], D 64 or 128, Hq a multiple of Hk (query head h uses key
+    head h Hk / Hq), tokens and heads evenly apart (slices of one projection's output will do); ``scale``
+    defaults to D^-1/2.  The queries are the last ones of their sequence: query i of nq sees the keys
+    j <= i + nk - nq, so that Tk > Tq is a prompt or token behind a past.  cu_seqlens int32 [N+1] (with
+    B = 1) are the offsets of packed queries, and of the keys too unless cu_seqlens_k gives theirs.  A
+    query without keys, and rows behind the last sequence, come back as zeros with lse minus infinity.
+    Gradients flow from both results.  All tensors on one GPU, unchanged until the backward, and on a
+    boundary of 16 bytes, rows and heads too (KdaError otherwise).
+    """
+    if cu_seqlens is None and cu_seqlens_k is not None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    args = (q, k, v, float(q.shape[-1] ** -0.5 if scale is None else scale), cu_seqlens,
+            cu_seqlens if cu_seqlens_k is None else cu_seqlens_k)
+    return _Attn.apply(*args) if _wants_derivative(q, k, v) else _attn_forward(*args)

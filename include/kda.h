@@ -666,6 +666,55 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
                          const float* log_decay, float scale, void* out, const float* initial_state, float* final_state,
                          int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, void* stream);
 
+/*
+ * Causal softmax attention over whole prompts, with grouped heads and packed
+ * sequences: for a sequence of nq queries and nk keys, query i sees the keys
+ * j <= i + nk - nq (the queries are the last ones), and with
+ * s_ij = scale q_i.k_j over those,
+ *     lse_i = log sum_j exp(s_ij),   out_i = sum_j exp(s_ij - lse_i) v_j.
+ * A query that sees no key (nq > nk) gives zeros and lse = minus infinity, and
+ * no gradient.  Decoding is the call with one query a sequence.
+ *
+ *   q, out        [B, Tq, Hq, D];  k, v [B, Tk, Hk, D];  D 64 or 128
+ *   Hq            a multiple of Hk: query head h uses key head h Hk / Hq
+ *   out_lo        as out, or NULL: written with what out's rounding took off,
+ *                 which kda_attn_bwd needs
+ *   lse           fp32 [B, Tq, Hq] written (natural logarithm)
+ *   workspace     scratch of >= kda_attn_workspace_size(B * Tq, B * Tk, Hq,
+ *                 Hk, D, N) bytes
+ *   cu_seqlens_q, cu_seqlens_k  int32 [N + 1] offsets of the queries and the
+ *                 keys with B == 1 (the same array for prompts without a
+ *                 past), or both NULL for N == B
+ *   scale         finite and positive
+ *   flags         0 or KDA_FLAG_ZERO_REST (rows behind the last sequence: lse
+ *                 becomes minus infinity there)
+ * Tq and Tk are below 2^31.  A NaN or infinity stays within its own sequence
+ * and key head; in v it reaches queries up to 63 tokens before its own, too
+ * (a tile's keys are multiplied together, with weight zero).
+ */
+size_t kda_attn_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N);
+kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                          int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride, float scale,
+                          void* out, void* out_lo, float* lse, void* workspace, size_t workspace_bytes, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                          int64_t D, int64_t N, unsigned flags, void* stream);
+
+/*
+ * Gradients of kda_attn_fwd for loss = <d_out, out> + <d_lse, lse>.
+ *   out, out_lo, lse  what the forward with the same inputs wrote
+ *   d_out         [B, Tq, Hq, D], contiguous;  d_lse fp32 [B, Tq, Hq] or NULL for zero
+ *   dq, dk, dv    [B, Tq, Hq, D], [B, Tk, Hk, D] twice, written, contiguous;
+ *                 dk and dv are sums over the query heads of a key head
+ *   workspace     >= kda_attn_bwd_workspace_size(B * Tq, Hq) bytes
+ */
+size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Hq);
+kda_status_t kda_attn_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
+                          int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride, float scale,
+                          const void* out, const void* out_lo, const float* lse, const void* d_out, const float* d_lse, void* dq, void* dk,
+                          void* dv, void* workspace, size_t workspace_bytes, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                          int64_t D, int64_t N, unsigned flags, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* kda_status_string(kda_status_t status);
 

@@ -3,10 +3,10 @@
 Tolerances, with A(x) the same sum over the absolute values of its terms:
 
 * bf16 results: half a step of the value (2^-8), plus 2^-15 A for the pair weights and entering states
-  that are split in two bf16 parts (2^-17 each, pair weights on top of two fp32 roundings), plus the
+  that are split in two bf16 parts (2^-8 2^-8 each), plus the
   roundings of fp32 sums, 2^-24 A each: up to 128 channels, 64 tokens, and, in a state, 64 tokens and
   two products for each of the steps that it was carried over.
-* states and the decay's gradient, fp32 results: three parts (2^-25), and the same sums.
+* states and the decay's gradient, fp32 results: three parts (2^-24), and the same sums.
 """
 
 import numpy as np
