@@ -139,10 +139,8 @@ __device__ __forceinline__ bf16x8 cols_frag(const uint16_t* lds, int row0, int c
 }
 // Registers 8 b .. 8 b + 7 of a 32x32 result, rounded, as the B operand against cols_frag's rows 16 b .. + 15.
 __device__ __forceinline__ bf16x8 result_frag(const f32x16& s, int b) {
-  bf16x8 o;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = (__bf16)s[8 * b + e];
-  return o;
+  const uint2 x = round4(s[8 * b], s[8 * b + 1], s[8 * b + 2], s[8 * b + 3]);
+  return join(x, round4(s[8 * b + 4], s[8 * b + 5], s[8 * b + 6], s[8 * b + 7]));
 }
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;
@@ -153,8 +151,8 @@ __device__ __forceinline__ f32x16 zero16() {
 
 // Four channels of an output row, and what their rounding took off.
 __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t at, float (&v)[4]) {
-  *reinterpret_cast<bf16x4*>(a.out + at) = cut_part(v);
-  if (a.out_lo) *reinterpret_cast<bf16x4*>(a.out_lo + at) = cut_part(v);
+  *reinterpret_cast<uint2*>(a.out + at) = cut_part(v);
+  if (a.out_lo) *reinterpret_cast<uint2*>(a.out_lo + at) = cut_part(v);
 }
 
 // Rows behind the last sequence of an axis: H D elements each become zeros.

@@ -14,8 +14,9 @@
 //     R_t = a (R_{t-1} + S_{t-1}),   dg = sum_t scale q_t.(R_t do_t) + <R_T, dS_T>,
 // carried in the dq sweep as a second state; over a chunk
 //     R_C = a^C (R_0 + C S_0) + sum_j (C-1-j) a^{C-1-j} v_j k_j^T,
-// and its part of o weighs the pair (i, j) by i - j.  No difference of large
-// sums is taken (sum t (q_t.dq_t - k_t.dk_t) would be one).
+// and the pairs within it give sum_{i>j} (i - j) a^{i-j} (do_i.v_j)(q_i.k_j), the
+// fp32 scores of the sweep times those of q and k.  No difference of large sums
+// is taken (sum t (q_t.dq_t - k_t.dk_t) would be one).
 //
 // A workgroup of four waves takes one head, one slice of z's channels and a
 // segment of the packed token axis, 64 tokens a step.  Each wave owns 16 or 32
@@ -38,11 +39,11 @@
 namespace kda {
 namespace {
 
-constexpr int LC = 64;          // tokens of a step
-constexpr int LT = 256;         // threads
-constexpr int64_t kLaWant = 512;   // workgroups to aim for: two per CU
-constexpr int64_t kLaEnough = 160; // chains that fill the chip without being cut into segments
-constexpr int64_t kLaMinSeg = 512; // tokens of a segment at least
+constexpr int LC = 64;  // tokens of a step
+constexpr int LT = 256;  // threads
+constexpr int64_t kLaWant = 512;   // workgroups at a time: two per CU
+constexpr int64_t kLaMost = 2048;  // workgroups that cutting leads to at most
+constexpr int64_t kLaMinSteps = 4; // steps of a segment at least
 
 // One sweep.  State element (d, c) of sequence n and head h is at
 // (n H + h) K V + d sr + c sc.
@@ -99,19 +100,77 @@ struct LaStretch {
   bool starts, ends;  // the sequence starts (ends) here, in the sweep's direction
 };
 
+// Element (row, col) of a tile of W columns in LDS: rows are not padded; their
+// 16-byte pieces are permuted by the row instead, so that 16 rows of one piece
+// (MFMA rows) and 8 rows of two neighbouring ones (transposing reads) each meet
+// all 64 banks once.  Padded rows can have one of the two, and cost half of the
+// LDS time in the other.
+template <int W>
+__device__ __forceinline__ int at_lds(int row, int col) {
+  static_assert(W == 64 || W == 128, "pieces of 16 bytes");
+  const int f = W == 128 ? (row & 7) << 1 | (row >> 3 & 1) : (row >> 1 & 3) << 1 | (row >> 3 & 1);
+  return row * W + (((col >> 3) ^ f) << 3) + (col & 7);
+}
+
+// A step's rows of one array: W channels of 64 tokens, asked for in 16-byte
+// pieces by the workgroup.  Token i of the step is row i behind `p`, or, back in
+// time, row 63 - i, so that every offset is positive; a step moves p by 64 rows.
+template <int W>
+struct LaRows {
+  static constexpr int PR = LT / (W / 8), U = LC / PR;  // rows a load covers, loads
+  uint4 r[U];
+  const uint16_t* p;  // of the step to be fetched next
+  int at, ts;         // this thread's offset in bytes in the first piece; bytes between tokens
+  __device__ __forceinline__ void start(int token_stride, int rev) {
+    const int rt = threadIdx.x / (W / 8);
+    ts = token_stride * 2;
+    at = (rev ? PR - 1 - rt : rt) * ts + (int)(threadIdx.x % (W / 8)) * 16;
+  }
+  __device__ __forceinline__ void seek(const uint16_t* base, int64_t row0, int rev) {
+    p = base + (rev ? row0 - (LC - 1) : row0) * (ts >> 1);
+  }
+  // Rows from len on are zeros: their offset is behind the descriptor's end, so
+  // that no load stands in a branch of its own.
+  __device__ __forceinline__ void load(int len, int rev) {
+    const __amdgpu_buffer_rsrc_t d = buf(p, 0x7fffffffu);
+    const int rt = threadIdx.x / (W / 8);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      r[u] = bload<uint4>(d, rt + PR * u < len ? at : (int)0x80000000, (rev ? U - 1 - u : u) * PR * ts);
+    p += (rev ? -LC : LC) * (int64_t)(ts >> 1);
+  }
+  __device__ __forceinline__ void store(uint16_t* lds) const {
+    const int rt = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+#pragma unroll
+    for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(lds + at_lds<W>(rt + PR * u, c)) = r[u];
+  }
+};
+
+__device__ __forceinline__ bf16x8 cut8(float (&x)[8]) {  // the next bf16 part of eight values
+  const uint32_t a = cut2(x[0], x[1]), b = cut2(x[2], x[3]), c = cut2(x[4], x[5]), d = cut2(x[6], x[7]);
+  return __builtin_bit_cast(bf16x8, make_uint4(a, b, c, d));
+}
+
+constexpr int kWaitLoads = 0x0f70;  // s_waitcnt vmcnt(0) alone
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
+}
+
 template <int DX, int ZW, bool OUT, bool DG>
-__global__ void __launch_bounds__(LT, DG ? 1 : 2) la_sweep_kernel(const LaArgs a) {
-  constexpr int NZ = 4 * ZW, XP = DX + 16, ZP = NZ + 16;  // LDS pitches: rows 8 banks (Z: 40) apart
-  constexpr int NCT = ZW / 16, NDT = DX / 16, NKB = DX / 32;
-  constexpr int NP = DG ? 3 : 2;  // bf16 parts of pair weights and entering states
-  constexpr int XU = LC * DX / 8 / LT, ZU = LC * NZ / 8 / LT;  // 16-byte pieces a thread loads
-  __shared__ __align__(16) uint16_t sX[OUT ? LC * XP : 8], sY[LC * XP], sZ[LC * ZP];
-  __shared__ uint4 sP[OUT ? (DG ? 2 * NP : NP) : 1][OUT ? 8 : 1][64];  // pair weights as B operands (then times i - j)
+__global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const LaArgs a) {
+  constexpr int NZ = 4 * ZW, NCT = ZW / 16, NDT = DX / 16, NKB = DX / 32;
+  constexpr int NP = DG ? 3 : 2;  // bf16 parts of entering states
+  __shared__ __align__(16) uint16_t sX[OUT ? LC * DX : 8], sY[LC * DX], sZ[LC * NZ];
+  __shared__ uint4 sP[OUT ? 2 : 1][OUT ? 8 : 1][64];  // pair weights as B operands, two parts
+  __shared__ __align__(16) uint16_t sQ[OUT && DG ? LC * NZ : 8];  // the rows that the decay's gradient is dotted with
   __shared__ float sLam[LC + 1];
+  __shared__ __align__(16) float sW[LC];  // decays of z's rows up to the step's end, times c3
   __shared__ float sRed[4];
 
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6, l16 = lane & 15, g4 = lane >> 4;
-  const int64_t R = axis_rows(a.ax);
+  const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6), l16 = lane & 15, g4 = lane >> 4;
+  const int64_t R = uniform(axis_rows(a.ax));
 
   // ---- sequences without tokens: what leaves them is what entered
   if ((int64_t)blockIdx.x >= a.main) {
@@ -129,13 +188,13 @@ __global__ void __launch_bounds__(LT, DG ? 1 : 2) la_sweep_kernel(const LaArgs a
 
   // ---- this workgroup's place.  Ids that agree mod 8 run on one XCD: the
   // slices and passes of an item, which read the same rows, are neighbours there.
-  const int64_t id = blockIdx.x;
+  const int id = blockIdx.x;
   const int kinds = a.slices * a.passes;
-  const int64_t item = id / 8 / kinds * 8 + id % 8;
+  const int item = id / 8 / kinds * 8 + id % 8;
   if (item >= a.items) return;
-  const int kind = (int)(id / 8 % kinds), slice = kind % a.slices;
+  const int kind = id / 8 % kinds, slice = kind % a.slices;
   const LaPass& p = a.p[kind / a.slices];
-  const int h = (int)(item % a.H), s = (int)(item / a.H);
+  const int h = item % a.H, s = item / a.H;
   const int DZ = NZ * a.slices;
   const LaSeg sg = la_seg(a, s, R);
   const int rev = p.rev;
@@ -152,213 +211,296 @@ __global__ void __launch_bounds__(LT, DG ? 1 : 2) la_sweep_kernel(const LaArgs a
   if (DG && t == 0) p.part[((int64_t)h * a.nseg + s) * a.slices + slice] = 0.0f;
   if (sg.p0 >= sg.p1) return;
 
-  const float gh = a.g[h];
-  if (t <= LC) sLam[t] = la_pow(gh, t);
-  __syncthreads();
-
   // ---- the first stretch.  OUT: all stretches of the segment in the sweep's
   // order; otherwise the one that goes on beyond the segment's end, if any.
   const bool tail = rev == (OUT ? 0 : 1);  // whether to begin at the segment's first row
   LaStretch c;
   auto place = [&](int n) {
-    const int64_t bos = axis_start(a.ax, n), eos = la_end(a.ax, n, R);
+    const int64_t bos = uniform(axis_start(a.ax, n)), eos = uniform(la_end(a.ax, n, R));
     c.n = n;
     c.a = bos > sg.p0 ? bos : sg.p0;
     c.b = eos < sg.p1 ? eos : sg.p1;
     c.starts = rev ? eos <= sg.p1 : bos >= sg.p0;
     c.ends = rev ? bos >= sg.p0 : eos <= sg.p1;
   };
-  place(axis_owner(a.ax, tail ? sg.p0 : sg.p1 - 1));
+  place(uniform(axis_owner(a.ax, tail ? sg.p0 : sg.p1 - 1)));
   if (!OUT && c.ends) return;
   if (c.a >= c.b) return;  // only where offsets break their contract
-  int64_t done = 0;  // tokens of the stretch before the current step
+  // tokens of the stretch from the current step on; of the one whose rows are asked for
+  int left = (int)(c.b - c.a), ahead = left;
 
-  uint4 rx[OUT ? XU : 1], ry[XU], rz[ZU];
-  auto rows = [&](auto& r, auto width, const uint16_t* base, int64_t ts, int64_t row0, int len) {
-    constexpr int W8 = decltype(width)::value / 8;
-    const uint16_t* q = base + row0 * ts;
-#pragma unroll
-    for (int u = 0; u < (int)(sizeof(r) / 16); ++u) {
-      const int e = t + LT * u, row = e / W8;
-      const int at = (rev ? -row : row) * (int)ts + e % W8 * 8;
-      r[u] = row < len ? *reinterpret_cast<const uint4*>(q + at) : make_uint4(0, 0, 0, 0);
+  LaRows<DX> rx, ry;
+  LaRows<NZ> rz, rq;
+  if constexpr (OUT) rx.start((int)p.xs, rev);
+  ry.start((int)p.ys, rev);
+  rz.start((int)p.zs, rev);
+  if constexpr (OUT && DG) rq.start((int)p.ws, rev);
+  uint16_t* po = nullptr;  // the step's first token in the output
+  const int os = (rev ? -a.H : a.H) * DZ;
+  auto seek = [&]() {
+    const int64_t row0 = rev ? c.b - 1 : c.a;
+    if constexpr (OUT) rx.seek(p.x + h * p.xh, row0, rev);
+    ry.seek(p.y + h * p.yh, row0, rev);
+    rz.seek(p.z + h * p.zh + slice * NZ, row0, rev);
+    if constexpr (OUT && DG) rq.seek(p.w + h * p.wh + slice * NZ, row0, rev);
+  };
+  auto fetch = [&]() {
+    const int len = ahead < LC ? ahead : LC;
+    if constexpr (OUT) rx.load(len, rev);
+    ry.load(len, rev);
+    rz.load(len, rev);
+    if constexpr (OUT && DG) rq.load(len, rev);
+  };
+  int wlen = 0;  // the step length that sW belongs to
+  auto stage = [&]() {  // the rows that have come, and the decays of their step, into LDS
+    if constexpr (OUT) rx.store(sX);
+    ry.store(sY);
+    rz.store(sZ);
+    if constexpr (OUT && DG) rq.store(sQ);
+    const int len = ahead < LC ? ahead : LC;
+    if (len != wlen) {  // seldom: steps are whole but for a stretch's last one
+      wlen = len;
+      const int n = len - t - p.off;  // len - 1 - j + (1 - off)
+      if (t < LC) sW[t] = n >= 0 ? sLam[n] * p.c3 : 0.0f;
     }
   };
-  auto fetch = [&]() {  // the step's rows into registers; time step i is row0 + i, or row0 - i
-    const int64_t row0 = rev ? c.b - 1 - done : c.a + done;
-    const int64_t left = c.b - c.a - done;
-    const int len = (int)(left < LC ? left : LC);
-    if constexpr (OUT) rows(rx, std::integral_constant<int, DX>{}, p.x + h * p.xh, p.xs, row0, len);
-    rows(ry, std::integral_constant<int, DX>{}, p.y + h * p.yh, p.ys, row0, len);
-    rows(rz, std::integral_constant<int, NZ>{}, p.z + h * p.zh + slice * NZ, p.zs, row0, len);
-  };
+
+  seek();
+  fetch();
+  const float gh = a.g[h];
+  if (t <= LC) sLam[t] = la_pow(gh, t);
+  __syncthreads();
 
   f32x4 S[NDT][NCT], Rs[DG ? NDT : 1][DG ? NCT : 1];
   double dg = 0.0;
   const int col = slice * NZ + w * ZW + l16;  // the lane's channel of z (+ 16 ct)
   const int64_t segat = ((int64_t)s * a.H + h) * a.KV;
   const int64_t rat = (int64_t)a.nseg * a.H * a.KV;  // R's segments lie behind S's
-  // a^{i-j} of the wave's 16 rows i against each column tile, 0 above the diagonal
-  float dec[OUT ? 4 : 1][4], lamo[OUT ? 4 : 1];
+  // a^{i-j} of the wave's 16 rows j: against the columns of its own tile, of the
+  // next one, and what is more for a tile further away; a^{i + off}
+  float dec0[4], dec1[4], far[4], lamo[4];
   if constexpr (OUT) {
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = 16 * (w - jt) + l16 - 4 * g4 - r;
-        dec[jt][r] = n >= 0 ? sLam[n] * p.c1 : 0.0f;
-      }
-      lamo[jt] = sLam[16 * jt + l16 + p.off > LC ? LC : 16 * jt + l16 + p.off] * p.c2;
+    for (int r = 0; r < 4; ++r) {
+      const int n = l16 - 4 * g4 - r;
+      dec0[r] = sLam[n >= 0 ? n : 0] * p.c1;
+      dec1[r] = sLam[16 + n] * p.c1;
+      far[r] = sLam[r - w > 1 ? 16 * (r - w - 1) : 0];
+      lamo[r] = sLam[16 * r + l16 + p.off] * p.c2;
     }
   }
+  stage();
+  __syncthreads();
 
-  fetch();
+  LaStretch now = c;
+  bool first = true;
   while (true) {
-    const int64_t left = c.b - c.a - done;
-    const int len = (int)(left < LC ? left : LC);
-    const bool first = done == 0, last = left <= LC;
-    const int64_t row0 = rev ? c.b - 1 - done : c.a + done;
-    const LaStretch now = c;
+    const int len = left < LC ? left : LC;
+    const bool last = left <= LC;
+    if (OUT && first) po = p.out + ((rev ? now.b - 1 : now.a) * a.H + h) * DZ + slice * NZ + w * ZW;
 
-    // ---- tiles into LDS
-#pragma unroll
-    for (int u = 0; u < XU; ++u) {
-      const int e = t + LT * u, at = e / (DX / 8) * XP + e % (DX / 8) * 8;
-      if constexpr (OUT) *reinterpret_cast<uint4*>(sX + at) = rx[u];
-      *reinterpret_cast<uint4*>(sY + at) = ry[u];
-    }
-#pragma unroll
-    for (int u = 0; u < ZU; ++u) {
-      const int e = t + LT * u;
-      *reinterpret_cast<uint4*>(sZ + e / (NZ / 8) * ZP + e % (NZ / 8) * 8) = rz[u];
-    }
-
-    // ---- the state that enters a stretch
-    if (first) {
-      const float* src = now.starts ? p.sin : OUT ? p.seg : nullptr;
-      const int64_t at = now.starts ? ((int64_t)now.n * a.H + h) * a.KV : segat;
-      const int sr = now.starts ? p.sr : DZ, sc = now.starts ? p.sc : 1;
-#pragma unroll
-      for (int dt = 0; dt < NDT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int d = 16 * dt + 4 * g4 + r;
-            S[dt][ct][r] = src ? src[at + d * sr + (col + 16 * ct) * sc] : 0.0f;
-            if constexpr (DG) Rs[dt][ct][r] = !now.starts && OUT ? p.seg[rat + segat + d * DZ + col + 16 * ct] : 0.0f;
-          }
-    }
-
-    // ---- the next step, and its rows while this one runs
+    // ---- the next step
     bool more = true;
-    done += LC;
+    ahead = left - LC;
     if (last) {
-      done = 0;
       more = false;
       if (OUT) {
         int n = now.n;
         while (true) {  // the next sequence with tokens in this segment
           n += rev ? -1 : 1;
           if (n < 0 || n >= a.ax.N) break;
-          if (rev ? la_end(a.ax, n, R) <= sg.p0 : axis_start(a.ax, n) >= sg.p1) break;
+          if (rev ? uniform(la_end(a.ax, n, R)) <= sg.p0 : uniform(axis_start(a.ax, n)) >= sg.p1) break;
           place(n);
           if (c.a < c.b) {
             more = true;
+            ahead = (int)(c.b - c.a);
+            seek();
             break;
           }
         }
       }
     }
-    __syncthreads();
-    if (more) fetch();
 
-    if constexpr (OUT) {
-      // ---- pairs: rows i of this wave, (y x^T)[j][i] with 4 consecutive j a lane
-      bf16x8 xb[NKB];
+    // ---- the state that enters a stretch
+    if (first) {
+      const float* src = now.starts ? p.sin : OUT ? p.seg : nullptr;
 #pragma unroll
-      for (int kb = 0; kb < NKB; ++kb)
-        xb[kb] = *reinterpret_cast<const bf16x8*>(sX + (16 * w + l16) * XP + 32 * kb + 8 * g4);
+      for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        if (jt > (w | 1)) break;
-        float v[4] = {0.f, 0.f, 0.f, 0.f}, vn[4] = {0.f, 0.f, 0.f, 0.f};
-        if (jt <= w) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int kb = 0; kb < NKB; ++kb)
-            acc = mfma_bf16(*reinterpret_cast<const bf16x8*>(sY + (16 * jt + l16) * XP + 32 * kb + 8 * g4), xb[kb], acc);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int n = 16 * (w - jt) + l16 - 4 * g4 - r;
-            v[r] = n >= 0 ? acc[r] * dec[jt][r] : 0.0f;
-            vn[r] = v[r] * (float)n;
-          }
+        for (int ct = 0; ct < NCT; ++ct) {
+          S[dt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if constexpr (DG) Rs[dt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+      if (src) {
+        const float* at = src + (now.starts ? ((int64_t)now.n * a.H + h) * a.KV : segat);
+        const int sr = now.starts ? p.sr : DZ, sc = now.starts ? p.sc : 1;
 #pragma unroll
-        for (int m = 0; m < NP; ++m) {
-          reinterpret_cast<bf16x4*>(&sP[m][2 * w + (jt >> 1)][lane])[jt & 1] = cut_part(v);
-          if constexpr (DG) reinterpret_cast<bf16x4*>(&sP[NP + m][2 * w + (jt >> 1)][lane])[jt & 1] = cut_part(vn);
-        }
+        for (int dt = 0; dt < NDT; ++dt)
+#pragma unroll
+          for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int d = 16 * dt + 4 * g4 + r;
+              S[dt][ct][r] = at[d * sr + (col + 16 * ct) * sc];
+              if constexpr (DG && OUT)
+                if (!now.starts) Rs[dt][ct][r] = at[rat + d * DZ + col + 16 * ct];
+            }
+        // Waited for here: a wait behind the branch would be one for the loads
+        // issued after it, on the usual path without these.
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
       }
     }
+    // Its rows come while this step runs.  Without a next step there are none,
+    // but neither the loads nor what waits for them stands in a branch: where one
+    // ends, registers would be waited for that other loads and stores hold up.
+    if (!more) ahead = 0;
+    fetch();
 
-    // ---- the entering state's part of the outputs: out^T[c][i] = S^T x^T
+    // ---- the entering state's part of the outputs, out^T[c][i] = S^T x^T, and
+    // the pairs, rows j of this wave: (y x^T)[j][i].  Both take x's rows in the
+    // channel order of the state's registers.
     f32x4 O[OUT ? 4 : 1][NCT], On[DG && OUT ? 4 : 1][DG && OUT ? NCT : 1];
     if constexpr (OUT) {
+      f32x4 P[4];
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+      for (int it = 0; it < 4; ++it) {
+        P[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
           O[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
           if constexpr (DG) On[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+      }
+      auto frag = [&](const uint16_t* tile, int row, int kb) {
+        const int ch = 32 * kb + 4 * g4;
+        return join(*reinterpret_cast<const uint2*>(tile + at_lds<DX>(row, ch)),
+                    *reinterpret_cast<const uint2*>(tile + at_lds<DX>(row, ch + 16)));
+      };
+      // Rows and state parts are one block of channels ahead of the products, so
+      // that the parts are cut while products run.
+      constexpr int AHEAD = DG ? 0 : 1;  // two states leave no registers for it
+      bf16x8 xf[1 + AHEAD][4], yf[1 + AHEAD], sp[1 + AHEAD][NCT][NP], rp[1 + AHEAD][DG ? NCT : 1][NP];
+      auto ready = [&](int kb) {
+        const int b = kb & AHEAD;
 #pragma unroll
-      for (int kb = 0; kb < NKB; ++kb) {
-        bf16x8 sp[NCT][NP], rp[DG ? NCT : 1][NP];
+        for (int it = 0; it < 4; ++it) xf[b][it] = frag(sX, 16 * it + l16, kb);
+        yf[b] = frag(sY, 16 * w + l16, kb);
+      };
+      auto parts = [&](int kb) {
         auto cut = [&](f32x4 u, f32x4 v, bf16x8 (&o)[NP]) {
+          float f[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
 #pragma unroll
-          for (int m = 0; m < NP; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              o[m][r] = (__bf16)u[r];
-              u[r] -= (float)o[m][r];
-              o[m][4 + r] = (__bf16)v[r];
-              v[r] -= (float)o[m][4 + r];
-            }
+          for (int m = 0; m < NP; ++m) o[m] = cut8(f);
         };
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-          cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp[ct]);
-          if constexpr (DG) cut(Rs[2 * kb][ct], Rs[2 * kb + 1][ct], rp[ct]);
+          cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp[kb & AHEAD][ct]);
+          if constexpr (DG) cut(Rs[2 * kb][ct], Rs[2 * kb + 1][ct], rp[kb & AHEAD][ct]);
+        }
+      };
+      ready(0);
+      __builtin_amdgcn_sched_barrier(0);
+      parts(0);
+#pragma unroll
+      for (int kb = 0; kb < NKB; ++kb) {
+        const int b = kb & AHEAD;
+        if (kb + AHEAD < NKB && kb + AHEAD > 0) {
+          ready(kb + AHEAD);
+          parts(kb + AHEAD);
         }
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const uint16_t* q = sX + (16 * it + l16) * XP + 32 * kb + 4 * g4;
-          const bf16x8 xf = join(*reinterpret_cast<const uint2*>(q), *reinterpret_cast<const uint2*>(q + 16));
-#pragma unroll
-          for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int m = 0; m < NP; ++m) {
-              O[it][ct] = mfma_bf16(sp[ct][m], xf, O[it][ct]);
-              if constexpr (DG) On[it][ct] = mfma_bf16(rp[ct][m], xf, On[it][ct]);
-            }
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
+        for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf[b], xf[b][it], P[it]);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
+          for (int m = 0; m < NP; ++m)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+              O[it][ct] = mfma_bf16(sp[b][ct][m], xf[b][it], O[it][ct]);
+              if constexpr (DG) On[it][ct] = mfma_bf16(rp[b][ct][m], xf[b][it], On[it][ct]);
+            }
+        if constexpr (!DG) {  // reads first, then products with the cutting between them
+          if (kb + 1 < NKB) __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
+#pragma unroll
+          for (int i = 0; i < 4 + 4 * NCT * NP; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      f32x4 A[DG ? 4 : 1];  // (z q^T)[j][i] over this slice's channels
+      if constexpr (DG) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) A[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < NZ / 32; ++kb) {
+          const bf16x8 zf = *reinterpret_cast<const bf16x8*>(sZ + at_lds<NZ>(16 * w + l16, 32 * kb + 8 * g4));
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            A[it] = mfma_bf16(zf, *reinterpret_cast<const bf16x8*>(sQ + at_lds<NZ>(16 * it + l16, 32 * kb + 8 * g4)), A[it]);
+        }
+      }
+      float pairs = 0.0f;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        if (it < (w & 2)) continue;  // nothing reads those
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int n = 16 * (it - w) + l16 - 4 * g4 - r;
+          v[r] = n >= 0 ? P[it][r] * (it == w ? dec0[r] : dec1[r] * far[it]) : 0.0f;
+          if constexpr (DG) pairs += n > 0 ? (float)n * v[r] * A[it][r] : 0.0f;
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          reinterpret_cast<uint2*>(&sP[m][2 * it + (w >> 1)][lane])[w & 1] = cut_part(v);
+      }
+      if constexpr (DG) dg += pairs;
+      float sum = 0.0f;
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+          float q[4];
+          if constexpr (DG)
+            widen4(*reinterpret_cast<const uint2*>(sQ + at_lds<NZ>(16 * it + l16, w * ZW + 16 * ct + 4 * g4)), q);
+#pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if constexpr (DG) On[it][ct][r] = (On[it][ct][r] + O[it][ct][r] * (float)(16 * it + l16 + 1)) * lamo[it];
+            if constexpr (DG) sum += (On[it][ct][r] + O[it][ct][r] * (float)(16 * it + l16 + 1)) * lamo[it] * q[r];
             O[it][ct][r] *= lamo[it];
           }
+        }
+      if constexpr (DG) dg += sum;
     }
 
     // ---- the state: decayed, plus y^T (z times its decay), z's product in three bf16 parts
+    bf16x8 zr[2][NCT];
     {
       const float full = sLam[len];
+      bf16x8 yt[NDT];
+      float wz[2][8];
+      auto columns = [&](int ks) {
+        const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
+#pragma unroll
+        for (int dt = 0; dt < NDT; ++dt) {
+          const int yc = 16 * dt + 4 * (l16 & 3);
+          yt[dt] = join(tr_read(sY + at_lds<DX>(jr, yc)), tr_read(sY + at_lds<DX>(jr + 16, yc)));
+        }
+      };
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
+        lds_f32x4(sW + 32 * ks + 4 * g4, wz[ks]);
+        lds_f32x4(sW + 32 * ks + 16 + 4 * g4, wz[ks] + 4);
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+          const int zc = w * ZW + 16 * ct + 4 * (l16 & 3);
+          zr[ks][ct] = join(tr_read(sZ + at_lds<NZ>(jr, zc)), tr_read(sZ + at_lds<NZ>(jr + 16, zc)));
+        }
+      }
+      columns(0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
@@ -368,86 +510,76 @@ __global__ void __launch_bounds__(LT, DG ? 1 : 2) la_sweep_kernel(const LaArgs a
             if constexpr (DG) Rs[dt][ct][r] = full * (Rs[dt][ct][r] + (float)len * S[dt][ct][r]);
             S[dt][ct][r] *= full;
           }
-    }
-    bf16x8 zr[2][NCT];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
-      bf16x8 zw[NCT][3], zn[DG ? NCT : 1][3];
+      for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 zw[NCT][3], zn[DG ? NCT : 1][3];
 #pragma unroll
-      for (int ct = 0; ct < NCT; ++ct) {
-        const uint16_t* q = sZ + jr * ZP + w * ZW + 16 * ct + 4 * (l16 & 3);
-        zr[ks][ct] = join(tr_read(q), tr_read(q + 16 * ZP));
+        for (int ct = 0; ct < NCT; ++ct) {
+          float f[8], fn[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = 32 * ks + 4 * g4 + (e & 3) + 16 * (e >> 2);
-          const int n = len - j - p.off;  // len - 1 - j + (1 - off)
-          const float f = (n >= 0 ? sLam[n] : 0.0f) * p.c3 * (float)zr[ks][ct][e];
-          auto cut3 = [&](float v, bf16x8* o) {
-            o[0][e] = (__bf16)v;
-            v -= (float)o[0][e];
-            o[1][e] = (__bf16)v;
-            o[2][e] = (__bf16)(v - (float)o[1][e]);
-          };
-          cut3(f, zw[ct]);
-          if constexpr (DG) cut3(f * (float)(n >= 0 ? n : 0), zn[ct]);
-        }
-      }
-#pragma unroll
-      for (int dt = 0; dt < NDT; ++dt) {
-        const uint16_t* q = sY + jr * XP + 16 * dt + 4 * (l16 & 3);
-        const bf16x8 yt = join(tr_read(q), tr_read(q + 16 * XP));
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-          for (int m = 0; m < 3; ++m) {
-            S[dt][ct] = mfma_bf16(yt, zw[ct][m], S[dt][ct]);
-            if constexpr (DG) Rs[dt][ct] = mfma_bf16(yt, zn[ct][m], Rs[dt][ct]);
-          }
-      }
-    }
-
-    // ---- the pairs' part of the outputs
-    if constexpr (OUT) {
-      __syncthreads();
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int ks = 0; ks <= it >> 1; ++ks) {
-#pragma unroll
-          for (int m = 0; m < NP; ++m) {
-            const bf16x8 pm = __builtin_bit_cast(bf16x8, sP[m][2 * it + ks][lane]);
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) O[it][ct] = mfma_bf16(zr[ks][ct], pm, O[it][ct]);
+          for (int e = 0; e < 8; ++e) {
+            f[e] = wz[ks][e] * (float)zr[ks][ct][e];
             if constexpr (DG) {
-              const bf16x8 nm = __builtin_bit_cast(bf16x8, sP[NP + m][2 * it + ks][lane]);
-#pragma unroll
-              for (int ct = 0; ct < NCT; ++ct) On[it][ct] = mfma_bf16(zr[ks][ct], nm, On[it][ct]);
+              const int n = len - 1 - (32 * ks + 4 * g4 + (e & 3) + 16 * (e >> 2));
+              fn[e] = f[e] * (float)(n >= 0 ? n : 0);
             }
           }
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            zw[ct][m] = cut8(f);
+            if constexpr (DG) zn[ct][m] = cut8(fn);
+          }
         }
-      float sum = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int dt = 0; dt < NDT; ++dt) {
+              S[dt][ct] = mfma_bf16(yt[dt], zw[ct][m], S[dt][ct]);
+              if constexpr (DG) Rs[dt][ct] = mfma_bf16(yt[dt], zn[ct][m], Rs[dt][ct]);
+            }
+        if (ks == 0) {
+          columns(1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    __syncthreads();  // pair weights are there, tiles are read
+
+    // ---- the pairs' part of the outputs; the next step's tiles
+    bf16x8 pf[OUT ? 6 : 1][2];
+    if constexpr (OUT) {
+#pragma unroll
+      for (int f = 0; f < 6; ++f)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) pf[f][m] = __builtin_bit_cast(bf16x8, sP[m][f < 2 ? 2 * f : f + 2][lane]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    stage();
+    if constexpr (OUT) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int it = 2 * ks; it < 4; ++it) {
+            const int f = it < 2 ? it : 2 * it + ks - 2;
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) O[it][ct] = mfma_bf16(zr[ks][ct], pf[f][m], O[it][ct]);
+          }
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         const int i = 16 * it + l16;
         if (i < len) {
-          const int64_t row = rev ? row0 - i : row0 + i;
 #pragma unroll
           for (int ct = 0; ct < NCT; ++ct) {
-            const int at = slice * NZ + w * ZW + 16 * ct + 4 * g4;
-            bf16x4 o;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = (__bf16)O[it][ct][r];
-            *reinterpret_cast<bf16x4*>(p.out + (row * a.H + h) * DZ + at) = o;
-            if constexpr (DG) {
-              const bf16x4 q = *reinterpret_cast<const bf16x4*>(p.w + row * p.ws + h * p.wh + at);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) sum += On[it][ct][r] * (float)q[r];
-            }
+            *reinterpret_cast<uint2*>(po + i * os + 16 * ct + 4 * g4) =
+                round4(O[it][ct][0], O[it][ct][1], O[it][ct][2], O[it][ct][3]);
           }
         }
       }
-      if constexpr (DG) dg += sum;
+      po += LC * (int64_t)os;
     }
 
     // ---- the state that leaves a stretch
@@ -456,23 +588,35 @@ __global__ void __launch_bounds__(LT, DG ? 1 : 2) la_sweep_kernel(const LaArgs a
       const int64_t at = OUT ? ((int64_t)now.n * a.H + h) * a.KV : segat;
       const int sr = OUT ? p.sr : DZ, sc = OUT ? p.sc : 1;
       float sum = 0.0f;
+      if (dst) {
 #pragma unroll
-      for (int dt = 0; dt < NDT; ++dt)
+        for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
+          for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int d = 16 * dt + 4 * g4 + r, cc = col + 16 * ct;
-            if (dst) dst[at + d * sr + cc * sc] = S[dt][ct][r];
-            if constexpr (DG) {
-              if (!OUT) p.seg[rat + segat + d * DZ + cc] = Rs[dt][ct][r];
-              if (OUT && now.ends && p.rend) sum += Rs[dt][ct][r] * p.rend[at + d * sr + cc * sc];
+            for (int r = 0; r < 4; ++r) {
+              const int d = 16 * dt + 4 * g4 + r, cc = col + 16 * ct;
+              dst[at + d * sr + cc * sc] = S[dt][ct][r];
+              if constexpr (DG && !OUT) dst[rat + at + d * sr + cc * sc] = Rs[dt][ct][r];
             }
-          }
+      }
+      if constexpr (DG && OUT)
+        if (now.ends && p.rend) {
+#pragma unroll
+          for (int dt = 0; dt < NDT; ++dt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                sum += Rs[dt][ct][r] * p.rend[at + (16 * dt + 4 * g4 + r) * sr + (col + 16 * ct) * sc];
+        }
       if constexpr (DG) dg += sum;
     }
     if (!more) break;
-    __syncthreads();
+    first = last;
+    if (last) now = c;
+    left = ahead;
+    __syncthreads();  // the next tiles are there, pair weights are read
   }
 
   if constexpr (DG && OUT) {
@@ -612,20 +756,25 @@ __global__ void __launch_bounds__(LT) la_step_kernel(const LaStep a) {
 // blocks' heads is a chain of steps; with few chains the blocks are cut into
 // segments, whose entering states cost another pass over y and z.
 struct LaPlan {
-  int zw, slices, spb;
+  int slices, spb;
   int64_t L, nseg;
 };
 LaPlan la_plan(int64_t blocks, int64_t block, int64_t H, int64_t DZ, int64_t passes) {
   LaPlan pl;
-  pl.zw = 16;
   pl.slices = (int)(DZ / 64);
   const int64_t chains = blocks * H * pl.slices * passes;
-  int64_t spb = 1;
-  if (chains < kLaEnough) {
-    spb = (kLaWant + chains - 1) / chains;
-    const int64_t most = (block + kLaMinSeg - 1) / kLaMinSeg;
-    spb = spb < most ? spb : most;
-    spb = spb < 1 ? 1 : spb;
+  // Steps that the busiest CU does one after another, three of the first pass
+  // taken for one of the second.
+  int64_t spb = 1, best = INT64_MAX;
+  for (int64_t n = 1; n <= 64 && (n == 1 || chains * n <= kLaMost); ++n) {
+    const int64_t len = (block + n * LC - 1) / (n * LC);
+    if (n > 1 && len < kLaMinSteps) break;
+    const int64_t second = (chains * n + kLaWant - 1) / kLaWant * len;
+    const int64_t first = n > 1 ? (chains * (n - 1) + kLaWant - 1) / kLaWant * len : 0;
+    if (3 * second + first + (n > 1 ? 24 : 0) < best) {
+      best = 3 * second + first + (n > 1 ? 24 : 0);
+      spb = n;
+    }
   }
   pl.L = ((block + spb - 1) / spb + LC - 1) / LC * LC;
   pl.L = pl.L < LC ? LC : pl.L;
@@ -635,14 +784,16 @@ LaPlan la_plan(int64_t blocks, int64_t block, int64_t H, int64_t DZ, int64_t pas
   return pl;
 }
 
-// Bytes of the states of a sweep's segments, at most.  Only sweeps of fewer
-// than kLaEnough chains are cut, into fewer than kLaWant + kLaEnough pieces in all.
-size_t la_states_bytes(int64_t H, int64_t K, int64_t V) {
-  return H < kLaEnough ? (size_t)((kLaWant + kLaEnough) * K * V) * sizeof(float) : 0;
+// Bytes of the states of a sweep's segments: at most kLaMost pieces in all,
+// and, a cut block having more than 6 steps and a segment more than 3, at most
+// T / 128 pieces a head.
+size_t la_states_bytes(int64_t T_total, int64_t H, int64_t K, int64_t V) {
+  const int64_t by_length = T_total / 128 * H;
+  return (size_t)((by_length < kLaMost ? by_length : kLaMost) * K * V) * sizeof(float);
 }
 // Bytes of the decay gradient's parts, for at most N blocks of the axis.
 size_t la_part_bytes(int64_t N, int64_t H) {
-  return align256((size_t)(N * H * 2 + kLaWant + kLaEnough) * sizeof(float));
+  return align256((size_t)(N * H * 2 + kLaMost) * sizeof(float));
 }
 
 kda_status_t la_check(const void* q, int64_t qs, int64_t qh, const void* k, int64_t ks, int64_t kh, const void* v,
@@ -651,8 +802,8 @@ kda_status_t la_check(const void* q, int64_t qs, int64_t qh, const void* k, int6
   if (B < 1 || T < 0 || H < 1 || K < 1 || V < 1 || N < 1) return KDA_ERR_INVALID;
   if (cu ? B != 1 : N != B) return KDA_ERR_INVALID;
   if ((K != 64 && K != 128) || (V != 64 && V != 128)) return KDA_ERR_UNSUPPORTED;
-  if (H > 1 << 20 || N > 1 << 30 || !fits(B, T, kMaxElements) || !fits(B * T, H * 128, kMaxElements) ||
-      !fits(N, H * 128 * 128, kMaxElements) || (cu && T >= (int64_t)1 << 31))
+  if (H > 1 << 16 || N > 1 << 30 || !fits(B, T, kMaxElements) || !fits(B * T, H * 128, kMaxElements) ||
+      !fits(N, H * 128 * 128, kMaxElements) || T >= (int64_t)1 << 31)
     return KDA_ERR_INVALID;
   if (!(scale - scale == 0.0f)) return KDA_ERR_INVALID;  // NaN or infinite
   if (!g || (B * T > 0 && (!q || !k || !v))) return KDA_ERR_INVALID;
@@ -661,19 +812,23 @@ kda_status_t la_check(const void* q, int64_t qs, int64_t qh, const void* k, int6
   return KDA_SUCCESS;
 }
 
-template <int DX, bool DG>
-kda_status_t la_run(LaArgs& a, const LaPlan& pl, bool empties, hipStream_t st) {
+template <int DX, int ZW, bool DG>
+kda_status_t la_launch(LaArgs& a, bool empties, hipStream_t st) {
   const int64_t groups = (a.items + 7) / 8 * 8 * a.slices * a.passes;
   const int64_t more = empties ? (a.ax.N < 1024 ? a.ax.N : 1024) : 0;
   if (groups + more > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   a.main = groups;
   if (a.spb > 1) {  // otherwise every segment starts at a sequence's start
-    kda_status_t s = launch(&la_sweep_kernel<DX, 16, false, DG>, groups, LT, st, "linear attention segments", a);
+    kda_status_t s = launch(&la_sweep_kernel<DX, ZW, false, DG>, groups, LT, st, "linear attention segments", a);
     if (s != KDA_SUCCESS) return s;
     s = launch(&la_join_kernel<DG>, (int64_t)a.passes * a.H * (a.KV / (LT * 4)), LT, st, "linear attention join", a);
     if (s != KDA_SUCCESS) return s;
   }
-  return launch(&la_sweep_kernel<DX, 16, true, DG>, groups + more, LT, st, "linear attention", a);
+  return launch(&la_sweep_kernel<DX, ZW, true, DG>, groups + more, LT, st, "linear attention", a);
+}
+template <int DX, bool DG>
+kda_status_t la_run(LaArgs& a, const LaPlan& pl, bool empties, hipStream_t st) {
+  return la_launch<DX, 16, DG>(a, empties, st);
 }
 template <bool DG>
 kda_status_t la_sweep(LaArgs& a, int64_t DX, const LaPlan& pl, bool empties, hipStream_t st) {
@@ -708,10 +863,10 @@ using namespace kda;
 extern "C" {
 
 size_t kda_la_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V) {
-  if (T_total < 0 || H < 1 || H > 1 << 20 || (K != 64 && K != 128) || (V != 64 && V != 128) ||
+  if (T_total < 0 || H < 1 || H > 1 << 16 || (K != 64 && K != 128) || (V != 64 && V != 128) ||
       !fits(T_total, H * 128, kMaxElements))
     return 0;
-  return 256 + la_states_bytes(H, K, V);
+  return 256 + la_states_bytes(T_total, H, K, V);
 }
 
 kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -747,7 +902,7 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
 
 size_t kda_la_bwd_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V, int64_t N) {
   if (!kda_la_workspace_size(T_total, H, K, V) || N < 1 || N > 1 << 30) return 0;
-  return 256 + 4 * la_states_bytes(H, K, V) + la_part_bytes(N, H);
+  return 256 + 4 * la_states_bytes(T_total, H, K, V) + la_part_bytes(N, H);
 }
 
 kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -772,7 +927,7 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
     return KDA_ERR_INVALID;
   if (!workspace || workspace_bytes < kda_la_bwd_workspace_size(B * T, H, K, V, N)) return KDA_ERR_WORKSPACE;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const size_t sb = la_states_bytes(H, K, V);
+  const size_t sb = la_states_bytes(B * T, H, K, V);
   char* ws = static_cast<char*>(workspace);
   const uint16_t *qp = static_cast<const uint16_t*>(q), *kp = static_cast<const uint16_t*>(k),
                  *vp = static_cast<const uint16_t*>(v), *dp = static_cast<const uint16_t*>(d_out);

@@ -630,7 +630,7 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
  *   final_state   fp32 [N, H, K, V] written, or NULL; not initial_state
  *   scale         finite
  *   flags         0 or KDA_FLAG_ZERO_REST
- * A NaN or infinity stays within its own sequence and head; it reaches tokens
+ * T is below 2^31, H at most 2^16.  A NaN or infinity stays within its own sequence and head; it reaches tokens
  * up to 63 before its own, too (a step's tokens are multiplied together).
  */
 size_t kda_la_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V);
