@@ -20,11 +20,11 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"),
 ]
 # Per-source flags.  The two recurrence kernels (forward inter-chunk, backward
-# state gradient) keep their MFMA accumulators in arch VGPRs, where the VALU
-# scales and converts them without accumulator-register moves; their operand
-# prefetch sets, which only feed MFMAs, then go to the accumulator registers.
-SOURCE_FLAGS = {"kda_inter.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# state gradient) and the token mixers keep their MFMA accumulators in arch VGPRs,
+# where the VALU scales and converts them without accumulator-register moves; their
+# operand prefetch sets, which only feed MFMAs, then go to the accumulator registers.
+SOURCE_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+                for name in ("kda_inter.hip", "kda_bwd.hip", "kda_la.hip", "kda_attn.hip")}
 
 
 def build(extra_flags=(), out=LIB, sources=None) -> str:

@@ -97,45 +97,51 @@ __device__ __forceinline__ Place tile_place(const Axis& ax, int64_t slot, int mu
   return Place{lo, slot - (span_start(ax, lo, R) * mul / TILE + lo)};
 }
 
+// Element (row, col) of a tile of W columns in LDS: the 16-byte pieces of a row
+// are permuted by the row, so that both 16 rows of one piece (row operands) and
+// 4 rows of four neighbouring ones (transposing reads) meet all 64 banks once.
+template <int W>
+__device__ __forceinline__ int at_tile(int row, int col) {
+  static_assert(W == 64 || W == 128, "pieces of 16 bytes");
+  const int f = W == 128 ? (row & 3) << 2 | (row >> 2 & 3) : (row >> 1 & 1) << 2 | (row >> 2 & 3);
+  return row * W + (((col >> 3) ^ f) << 3) + (col & 7);
+}
+
 // ROWS rows of D channels: NT threads ask for them in 16-byte pieces (zeros
-// from `len` on), and put them into LDS rows of PITCH elements.
+// from `len` on), and put them into a tile in LDS.
 template <int D, int ROWS, int NT>
 struct TileRegs {
-  static constexpr int U = ROWS * D / 8 / NT;
+  static constexpr int PR = NT / (D / 8), U = ROWS / PR;  // rows a load covers, loads
   uint4 r[U];
   __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int64_t row0, int64_t len) {
-    const uint16_t* p = base + row0 * stride;
+    const __amdgpu_buffer_rsrc_t d = buf(base + row0 * stride, 0x7fffffffu);
     const int left = (int)(len - row0 < ROWS ? len - row0 : ROWS);
+    const int rt = threadIdx.x / (D / 8), at = rt * (int)stride * 2 + (int)(threadIdx.x % (D / 8)) * 16;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int e = threadIdx.x + NT * u, row = e / (D / 8);
-      r[u] = row < left ? *reinterpret_cast<const uint4*>(p + row * (int)stride + e % (D / 8) * 8) : make_uint4(0, 0, 0, 0);
-    }
+    for (int u = 0; u < U; ++u)  // a row from len on: an offset behind the descriptor's end
+      r[u] = bload<uint4>(d, rt + PR * u < left ? at : (int)0x80000000, u * PR * (int)stride * 2);
   }
-  template <int PITCH>
   __device__ __forceinline__ void store(uint16_t* lds) const {
+    const int rt = threadIdx.x / (D / 8), c = threadIdx.x % (D / 8) * 8;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int e = threadIdx.x + NT * u;
-      *reinterpret_cast<uint4*>(lds + e / (D / 8) * PITCH + e % (D / 8) * 8) = r[u];
-    }
+    for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(lds + at_tile<D>(rt + PR * u, c)) = r[u];
   }
 };
 
 // 32 rows of a tile as the A operand, channels 16 kk .. + 15.
-template <int PITCH>
+template <int D>
 __device__ __forceinline__ bf16x8 rows_frag(const uint16_t* lds, int row0, int kk) {
   const int lane = threadIdx.x & 63;
-  return *reinterpret_cast<const bf16x8*>(lds + (row0 + (lane & 31)) * PITCH + 16 * kk + 8 * (lane >> 5));
+  return *reinterpret_cast<const bf16x8*>(lds + at_tile<D>(row0 + (lane & 31), 16 * kk + 8 * (lane >> 5)));
 }
 // 32 channels from ch0 as the rows of the A operand, against 16 rows of the
 // tile from row0 in the order of a 32x32 result's registers: a lane of half h
 // has rows 4 h .. + 3 and 8 + 4 h .. + 3.
-template <int PITCH>
+template <int D>
 __device__ __forceinline__ bf16x8 cols_frag(const uint16_t* lds, int row0, int ch0) {
   const int lane = threadIdx.x & 63, l16 = lane & 15;
-  const uint16_t* p = lds + (row0 + 4 * (lane >> 5) + (l16 >> 2)) * PITCH + ch0 + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
-  return join(tr_read(p), tr_read(p + 8 * PITCH));
+  const int row = row0 + 4 * (lane >> 5) + (l16 >> 2), col = ch0 + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
+  return join(tr_read(lds + at_tile<D>(row, col)), tr_read(lds + at_tile<D>(row + 8, col)));
 }
 // Registers 8 b .. 8 b + 7 of a 32x32 result, rounded, as the B operand against cols_frag's rows 16 b .. + 15.
 __device__ __forceinline__ bf16x8 result_frag(const f32x16& s, int b) {
@@ -168,9 +174,8 @@ __device__ __forceinline__ void clear_rows(uint16_t* out, const Axis& ax, int64_
 template <int D, int NW, int KT, bool SPLIT>
 __global__ void __launch_bounds__(64 * NW, 2) attn_fwd_kernel(const AttnArgs a) {
   constexpr int NT = 64 * NW, BM = 32 * NW, ND = D / 16, NC = D / 32, NJ = KT / 32;
-  constexpr int KP = D + 8, VP = D + 16;  // LDS pitches: rows 4 banks apart for row reads, 8 for transposing ones
   constexpr int NBUF = NW == 1 ? 1 : 2;
-  __shared__ __align__(16) uint16_t sK[NBUF][KT * KP], sV[NBUF][KT * VP];
+  __shared__ __align__(16) uint16_t sK[NBUF][KT * D], sV[NBUF][KT * D];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h2 = lane >> 5;
 
   if ((int64_t)blockIdx.x >= a.main) {
@@ -232,8 +237,8 @@ __global__ void __launch_bounds__(64 * NW, 2) attn_fwd_kernel(const AttnArgs a) 
   for (int64_t jt = j0; jt < j1; ++jt) {
     const int b = NBUF == 1 ? 0 : (int)(jt & 1);
     if (NBUF == 1) __syncthreads();
-    rk.template store<KP>(sK[b]);
-    rv.template store<VP>(sV[b]);
+    rk.store(sK[b]);
+    rv.store(sV[b]);
     __syncthreads();
     if (jt + 1 < j1) {
       rk.load(kb, a.ks, (jt + 1) * KT, sk.len);
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(64 * NW, 2) attn_fwd_kernel(const AttnArgs a) 
     for (int js = 0; js < NJ; ++js) {
       S[js] = zero16();
 #pragma unroll
-      for (int kk = 0; kk < ND; ++kk) S[js] = mfma32(rows_frag<KP>(sK[b], 32 * js, kk), qf[kk], S[js]);
+      for (int kk = 0; kk < ND; ++kk) S[js] = mfma32(rows_frag<D>(sK[b], 32 * js, kk), qf[kk], S[js]);
     }
     if (key0 + KT - 1 > wall) {  // some row does not see all of these keys
       const int64_t left = see - key0;
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(64 * NW, 2) attn_fwd_kernel(const AttnArgs a) 
       for (int b2 = 0; b2 < 2; ++b2) {
         const bf16x8 pf = result_frag(S[js], b2);
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct) O[ct] = mfma32(cols_frag<VP>(sV[b], 32 * js + 16 * b2, 32 * ct), pf, O[ct]);
+        for (int ct = 0; ct < NC; ++ct) O[ct] = mfma32(cols_frag<D>(sV[b], 32 * js + 16 * b2, 32 * ct), pf, O[ct]);
       }
   }
   sum += __shfl_xor(sum, 32);
@@ -371,10 +376,9 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const uint16_t* out, co
 }
 
 template <int D>
-__global__ void __launch_bounds__(256, 1) attn_dq_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(256, 2) attn_dq_kernel(const AttnArgs a) {
   constexpr int NT = 256, BM = 128, KT = 32, ND = D / 16, NC = D / 32;
-  constexpr int KP = D + 16, VP = D + 8;
-  __shared__ __align__(16) uint16_t sK[2][KT * KP], sV[2][KT * VP];
+  __shared__ __align__(16) uint16_t sK[2][KT * D], sV[2][KT * D];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h2 = lane >> 5;
   if ((int64_t)blockIdx.x >= a.main) {
     clear_rows(a.dq, a.aq, (int64_t)a.Hq * D, blockIdx.x - a.main, gridDim.x - a.main);
@@ -390,12 +394,11 @@ __global__ void __launch_bounds__(256, 1) attn_dq_kernel(const AttnArgs a) {
   const int64_t row = r0 + 32 * w + (lane & 31), rc = row < rows ? row : rows - 1;
   const int64_t tok = rc / a.G;
   const int g = (int)(rc - tok * a.G);
-  const int64_t see = tok + off;
   const int64_t rl = r0 + BM - 1 < rows ? r0 + BM - 1 : rows - 1;
   const int64_t end = rl / a.G + off + 1;
-  const int64_t j1 = end > 0 ? (end + KT - 1) / KT : 0;
-  const int64_t wf = r0 + 32 * w < rows ? r0 + 32 * w : rows - 1, wl = wf + 31 < rows ? wf + 31 : rows - 1;
-  const int64_t wend = wl / a.G + off, wall = wf / a.G + off;
+  const int j1 = end > 0 ? (int)((end + KT - 1) / KT) : 0;
+  const int64_t wf = r0 + 32 * w < rows ? r0 + 32 * w : rows - 1;
+  const int64_t wall = wf / a.G + off;  // every row of the wave sees the keys up to this one
   const int64_t head = (sq.at + tok) * a.Hq + (int64_t)hk * a.G + g;
 
   bf16x8 qf[ND], df[ND];
@@ -411,45 +414,48 @@ __global__ void __launch_bounds__(256, 1) attn_dq_kernel(const AttnArgs a) {
   const float l = a.lse[head];
   const float l2 = l == -__builtin_inff() ? 0.0f : l * LOG2E;  // a row that sees no key: all is masked
   const float dd = a.delta[head];
+  const int64_t see = tok + off;  // the last key that this lane's row sees
   f32x16 Q[NC];
 #pragma unroll
   for (int ct = 0; ct < NC; ++ct) Q[ct] = zero16();
   const uint16_t* kb = a.k + sk.at * a.ks + hk * a.kh;
   const uint16_t* vb = a.v + sk.at * a.vs + hk * a.vh;
   TileRegs<D, KT, NT> rk, rv;
-  if (j1 > 0) {
-    rk.load(kb, a.ks, 0, sk.len);
-    rv.load(vb, a.vs, 0, sk.len);
-  }
-  for (int64_t jt = 0; jt < j1; ++jt) {
-    const int b = (int)(jt & 1);
-    rk.template store<KP>(sK[b]);
-    rv.template store<VP>(sV[b]);
+  auto fetch = [&](int jt) {
+    rk.load(kb, a.ks, (int64_t)jt * KT, sk.len);
+    rv.load(vb, a.vs, (int64_t)jt * KT, sk.len);
+  };
+  auto stage = [&](int b) {
+    rk.store(sK[b]);
+    rv.store(sV[b]);
+  };
+  if (j1 > 0) fetch(0);
+  for (int jt = 0; jt < j1; ++jt) {
+    const int b = jt & 1;
+    stage(b);
     __syncthreads();
-    if (jt + 1 < j1) {
-      rk.load(kb, a.ks, (jt + 1) * KT, sk.len);
-      rv.load(vb, a.vs, (jt + 1) * KT, sk.len);
-    }
-    const int64_t key0 = jt * KT;
-    if (key0 > wend) continue;
+    fetch(jt + 1);  // nothing but zeros behind the last key
     f32x16 S = zero16(), P = zero16();
 #pragma unroll
     for (int kk = 0; kk < ND; ++kk) {
-      S = mfma32(rows_frag<KP>(sK[b], 0, kk), qf[kk], S);
-      P = mfma32(rows_frag<VP>(sV[b], 0, kk), df[kk], P);
+      S = mfma32(rows_frag<D>(sK[b], 0, kk), qf[kk], S);
+      P = mfma32(rows_frag<D>(sV[b], 0, kk), df[kk], P);
     }
-    const int64_t left = see - key0;
-    const int last = key0 + KT - 1 > wall ? (int)(left < KT ? left : KT) : KT;
+    const int64_t key0 = (int64_t)jt * KT;
+    if (key0 + KT - 1 > wall) {  // some row does not see all of these keys
+      const int64_t left = see - key0;
+      const int last = (int)(left < -1 ? -1 : left < KT ? left : KT);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float p = fexp2(S[e] * a.c - l2);
-      S[e] = 8 * (e >> 2) + 4 * h2 + (e & 3) > last ? 0.0f : p * (P[e] - dd);
+      for (int e = 0; e < 16; ++e)
+        if (8 * (e >> 2) + 4 * h2 + (e & 3) > last) S[e] = -__builtin_inff(), P[e] = 0.0f;
     }
 #pragma unroll
-    for (int b2 = 0; b2 < 2; ++b2) {
-      const bf16x8 sf = result_frag(S, b2);
+    for (int e = 0; e < 16; ++e) S[e] = fexp2(S[e] * a.c - l2) * (P[e] - dd);
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct) Q[ct] = mfma32(cols_frag<KP>(sK[b], 16 * b2, 32 * ct), sf, Q[ct]);
+    for (int s = 0; s < 2; ++s) {
+      const bf16x8 sf = result_frag(S, s);
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct) Q[ct] = mfma32(cols_frag<D>(sK[b], 16 * s, 32 * ct), sf, Q[ct]);
     }
   }
   if (row >= rows) return;
@@ -457,22 +463,25 @@ __global__ void __launch_bounds__(256, 1) attn_dq_kernel(const AttnArgs a) {
 #pragma unroll
   for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a.scale * Q[ct][4 * q + e];
-      store4(po + 32 * ct + 8 * q + 4 * h2, v);
-    }
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint2*>(po + 32 * ct + 8 * q + 4 * h2) = round4(
+          a.scale * Q[ct][4 * q], a.scale * Q[ct][4 * q + 1], a.scale * Q[ct][4 * q + 2], a.scale * Q[ct][4 * q + 3]);
 }
 
+// A tile of 128 keys, 32 a wave, and two streams of rows: waves 0..3 take the
+// even tiles of 32 rows, waves 4..7 the odd ones, each with its own sums of dk
+// and dv, which are added at the end.  The 128 registers of sums leave room for
+// two waves a SIMD, whose products and weights overlap, as long as k and v are
+// read from LDS as operands: held in registers (one wave a SIMD, a tile ahead)
+// the same work took 384 us in place of 264 (2 x 4097 tokens x 12 heads of 128: 780
+// TFLOP/s of the four products).
 template <int D>
-__global__ void __launch_bounds__(256, 1) attn_dkv_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(512, 2) attn_dkv_kernel(const AttnArgs a) {
   constexpr int NT = 256, BN = 128, RT = 32, ND = D / 16, NC = D / 32;
-  constexpr int QP = D + 16;
-  __shared__ __align__(16) uint16_t sQ[2][RT * QP], sD[2][RT * QP];
-  __shared__ __align__(16) float sL[2][RT], sE[2][RT];  // lse log2(e) and d of the rows
-  __shared__ int sT[2][RT];                             // the last key that each row sees, from this tile's first
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h2 = lane >> 5;
+  __shared__ __align__(16) uint16_t sKV[2][BN * D], sR[2][2][2][RT * D];  // k, v; q, do of a stream's two buffers
+  __shared__ __align__(16) float sL[2][2][RT], sE[2][2][RT];              // lse log2(e) and d of the rows
+  __shared__ __align__(16) int sT[2][2][RT];  // the last key that each row sees, from this tile's first
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6 & 3, h2 = lane >> 5, st = threadIdx.x >> 8, t = threadIdx.x & 255;
   if ((int64_t)blockIdx.x >= a.main) {
     clear_rows(a.dk, a.ak, (int64_t)a.Hk * D, blockIdx.x - a.main, gridDim.x - a.main);
     clear_rows(a.dv, a.ak, (int64_t)a.Hk * D, blockIdx.x - a.main, gridDim.x - a.main);
@@ -485,19 +494,14 @@ __global__ void __launch_bounds__(256, 1) attn_dkv_kernel(const AttnArgs a) {
   const int64_t key0 = at.tile * BN;
   if (key0 >= sk.len) return;
   const int64_t off = sk.len - sq.len, rows = sq.len * a.G;
-  const int64_t key = key0 + 32 * w + (lane & 31), kc = key < sk.len ? key : sk.len - 1;
   const int64_t t0 = key0 > off ? key0 - off : 0;  // first token that sees a key of the tile
   const int64_t i0 = t0 * a.G / RT, i1 = (rows + RT - 1) / RT;
-
-  bf16x8 kf[ND], vf[ND];
   {
-    const uint16_t* p = a.k + (sk.at + kc) * a.ks + hk * a.kh + 8 * h2;
-    const uint16_t* q = a.v + (sk.at + kc) * a.vs + hk * a.vh + 8 * h2;
-#pragma unroll
-    for (int kk = 0; kk < ND; ++kk) {
-      kf[kk] = *reinterpret_cast<const bf16x8*>(p + 16 * kk);
-      vf[kk] = *reinterpret_cast<const bf16x8*>(q + 16 * kk);
-    }
+    TileRegs<D, BN, 512> r;
+    r.load(a.k + sk.at * a.ks + hk * a.kh, a.ks, key0, sk.len);
+    r.store(sKV[0]);
+    r.load(a.v + sk.at * a.vs + hk * a.vh, a.vs, key0, sk.len);
+    r.store(sKV[1]);
   }
   f32x16 K[NC], V[NC];
 #pragma unroll
@@ -506,99 +510,145 @@ __global__ void __launch_bounds__(256, 1) attn_dkv_kernel(const AttnArgs a) {
     V[ct] = zero16();
   }
 
-  constexpr int U = RT * D / 8 / NT;
+  // The next tile's first row is head ng of token nt; a row of the tile is
+  // (ng + row) / G tokens further (by a multiplication: (G + 32) G < 2^32).
+  constexpr int PR = NT / (D / 8), U = RT / PR;
+  const uint32_t recip = a.G > 1 ? (uint32_t)((((uint64_t)1 << 32) + a.G - 1) / a.G) : 0;
+  const int stepT = 2 * RT / a.G, stepG = 2 * RT % a.G;
+  int64_t nrow = (i0 + st) * RT, nt = nrow / a.G;
+  int ng = (int)(nrow - nt * a.G);
   uint4 rq[U], rd[U];
-  float rl = 0.0f, re = 0.0f;
+  uint32_t rl = 0, re = 0;
   int rt = -1;
-  auto fetch = [&](int64_t it) {
+  const int mine = t / (D / 8), c16 = t % (D / 8) * 16;
+  auto fetch = [&]() {
+    const __amdgpu_buffer_rsrc_t dq = buf(a.q + (sq.at + nt) * a.qs + (int64_t)hk * a.G * a.qh, 0x7fffffffu);
+    const int64_t h0 = (sq.at + nt) * a.Hq + (int64_t)hk * a.G;
+    const __amdgpu_buffer_rsrc_t dd = buf(a.d_out + h0 * D, 0x7fffffffu);
+    const int left = (int)(rows - nrow < RT ? rows - nrow : RT);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int e = threadIdx.x + NT * u;
-      const int64_t r = it * RT + e / (D / 8);
-      const int c8 = e % (D / 8) * 8;
-      rq[u] = rd[u] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int64_t tok = r / a.G, h = (int64_t)hk * a.G + (r - tok * a.G);
-        rq[u] = *reinterpret_cast<const uint4*>(a.q + (sq.at + tok) * a.qs + h * a.qh + c8);
-        rd[u] = *reinterpret_cast<const uint4*>(a.d_out + ((sq.at + tok) * a.Hq + h) * D + c8);
-      }
+      const int r = mine + PR * u, n = ng + r;
+      const int tk = a.G > 1 ? (int)__umulhi((uint32_t)n, recip) : n, g = n - tk * a.G;
+      rq[u] = bload<uint4>(dq, r < left ? (tk * (int)a.qs + g * (int)a.qh) * 2 + c16 : (int)0x80000000, 0);
+      rd[u] = bload<uint4>(dd, r < left ? (tk * a.Hq + g) * D * 2 + c16 : (int)0x80000000, 0);
     }
-    if (threadIdx.x < RT) {
-      const int64_t r = it * RT + threadIdx.x;
-      rl = re = 0.0f;
-      rt = -1;
-      if (r < rows) {
-        const int64_t tok = r / a.G, h = (sq.at + tok) * a.Hq + (int64_t)hk * a.G + (r - tok * a.G);
-        const float l = a.lse[h];
-        rl = l == -__builtin_inff() ? 0.0f : l * LOG2E;
-        re = a.delta[h];
-        const int64_t last = tok + off - key0;
-        rt = (int)(last < BN ? last : BN);
-      }
+    if (t < RT) {
+      const int n = ng + t;
+      const int tk = a.G > 1 ? (int)__umulhi((uint32_t)n, recip) : n, g = n - tk * a.G;
+      const int o = t < left ? (tk * a.Hq + g) * 4 : (int)0x80000000;
+      rl = __builtin_amdgcn_raw_buffer_load_b32(buf(a.lse + h0, 0x7fffffffu), o, 0, 0);
+      re = __builtin_amdgcn_raw_buffer_load_b32(buf(a.delta + h0, 0x7fffffffu), o, 0, 0);
+      const int64_t last = nt + tk + off - key0;
+      rt = t < left ? (int)(last < -1 ? -1 : last < BN ? last : BN) : -1;
+    }
+    nrow += 2 * RT;
+    nt += stepT;
+    ng += stepG;
+    if (ng >= a.G) ng -= a.G, ++nt;
+  };
+  auto stage = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int to = at_tile<D>(mine + PR * u, c16 / 2);
+      *reinterpret_cast<uint4*>(sR[st][b][0] + to) = rq[u];
+      *reinterpret_cast<uint4*>(sR[st][b][1] + to) = rd[u];
+    }
+    if (t < RT) {
+      const float l = __uint_as_float(rl);
+      sL[st][b][t] = l == -__builtin_inff() ? 0.0f : l * LOG2E;  // a row that sees no key: all is masked
+      sE[st][b][t] = __uint_as_float(re);
+      sT[st][b][t] = rt;
     }
   };
-  if (i0 < i1) fetch(i0);
-  for (int64_t it = i0; it < i1; ++it) {
-    const int b = (int)((it - i0) & 1);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int e = threadIdx.x + NT * u, to = e / (D / 8) * QP + e % (D / 8) * 8;
-      *reinterpret_cast<uint4*>(sQ[b] + to) = rq[u];
-      *reinterpret_cast<uint4*>(sD[b] + to) = rd[u];
-    }
-    if (threadIdx.x < RT) {
-      sL[b][threadIdx.x] = rl;
-      sE[b][threadIdx.x] = re;
-      sT[b][threadIdx.x] = rt;
-    }
+  int64_t first = (i0 + st) * RT / a.G;  // the current tile's first token, and its first row's head
+  int fg = (int)((i0 + st) * RT - first * a.G);
+  if (i0 < i1) fetch();
+  for (int64_t it = i0; it < i1; it += 2) {  // the streams keep step: one may end with a tile behind the last row
+    const int b = (int)((it - i0) >> 1 & 1);
+    stage(b);
     __syncthreads();
-    if (it + 1 < i1) fetch(it + 1);
+    fetch();  // nothing but zeros behind the last row
+    const uint16_t *tq = sR[st][b][0], *td = sR[st][b][1];
     f32x16 S = zero16(), P = zero16();
 #pragma unroll
     for (int kk = 0; kk < ND; ++kk) {
-      S = mfma32(rows_frag<QP>(sQ[b], 0, kk), kf[kk], S);
-      P = mfma32(rows_frag<QP>(sD[b], 0, kk), vf[kk], P);
+      S = mfma32(rows_frag<D>(tq, 0, kk), rows_frag<D>(sKV[0], 32 * w, kk), S);
+      P = mfma32(rows_frag<D>(td, 0, kk), rows_frag<D>(sKV[1], 32 * w, kk), P);
     }
-    const int mine = 32 * w + (lane & 31);
+    // Rows that do not see all keys of the tile; those behind the last one need
+    // no mask, their q, do and d are zeros.
+    if (first + off - key0 < BN - 1) {
+      const int my = 32 * w + (lane & 31);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int4 t4 = *reinterpret_cast<const int4*>(&sT[st][b][8 * q + 4 * h2]);
+        const int tv[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (my > tv[e]) S[4 * q + e] = -__builtin_inff(), P[4 * q + e] = 0.0f;
+      }
+    }
+    first += stepT;
+    fg += stepG;
+    if (fg >= a.G) fg -= a.G, ++first;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float4 l4 = *reinterpret_cast<const float4*>(&sL[b][8 * q + 4 * h2]);
-      const float4 e4 = *reinterpret_cast<const float4*>(&sE[b][8 * q + 4 * h2]);
-      const int4 t4 = *reinterpret_cast<const int4*>(&sT[b][8 * q + 4 * h2]);
-      const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, ev[4] = {e4.x, e4.y, e4.z, e4.w};
-      const int tv[4] = {t4.x, t4.y, t4.z, t4.w};
+      float lv[4], ev[4];
+      lds_f32x4(&sL[st][b][8 * q + 4 * h2], lv);
+      lds_f32x4(&sE[st][b][8 * q + 4 * h2], ev);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool on = mine <= tv[e];
-        const float p = on ? fexp2(S[4 * q + e] * a.c - lv[e]) : 0.0f;
-        S[4 * q + e] = p;
-        P[4 * q + e] = on ? p * (P[4 * q + e] - ev[e]) : 0.0f;
+        S[4 * q + e] = fexp2(S[4 * q + e] * a.c - lv[e]);
+        P[4 * q + e] = S[4 * q + e] * (P[4 * q + e] - ev[e]);
       }
     }
 #pragma unroll
-    for (int b2 = 0; b2 < 2; ++b2) {
-      const bf16x8 pf = result_frag(S, b2), sf = result_frag(P, b2);
+    for (int s = 0; s < 2; ++s) {
+      const bf16x8 pf = result_frag(S, s), sf = result_frag(P, s);
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) {
-        V[ct] = mfma32(cols_frag<QP>(sD[b], 16 * b2, 32 * ct), pf, V[ct]);
-        K[ct] = mfma32(cols_frag<QP>(sQ[b], 16 * b2, 32 * ct), sf, K[ct]);
+        V[ct] = mfma32(cols_frag<D>(td, 16 * s, 32 * ct), pf, V[ct]);
+        K[ct] = mfma32(cols_frag<D>(tq, 16 * s, 32 * ct), sf, K[ct]);
       }
     }
   }
-  if (key >= sk.len) return;
+
+  // ---- the second stream's sums to the first, dv and then dk through the LDS of k and v
+  float4* box = reinterpret_cast<float4*>(&sKV[0][0]) + w * 64 * NC * 4 + lane;  // 16 NC floats a lane: BN D halves in all
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    f32x16* X = part == 0 ? V : K;
+    __syncthreads();
+    if (st == 1) {
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          box[(4 * ct + q) * 64] = make_float4(X[ct][4 * q], X[ct][4 * q + 1], X[ct][4 * q + 2], X[ct][4 * q + 3]);
+    }
+    __syncthreads();
+    if (st == 0) {
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 y = box[(4 * ct + q) * 64];
+          X[ct][4 * q] += y.x, X[ct][4 * q + 1] += y.y, X[ct][4 * q + 2] += y.z, X[ct][4 * q + 3] += y.w;
+        }
+    }
+  }
+  const int64_t key = key0 + 32 * w + (lane & 31);
+  if (st == 1 || key >= sk.len) return;
   const int64_t to = ((sk.at + key) * a.Hk + hk) * D;
 #pragma unroll
   for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float x[4], y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = a.scale * K[ct][4 * q + e];
-        y[e] = V[ct][4 * q + e];
-      }
-      store4(reinterpret_cast<__bf16*>(a.dk) + to + 32 * ct + 8 * q + 4 * h2, x);
-      store4(reinterpret_cast<__bf16*>(a.dv) + to + 32 * ct + 8 * q + 4 * h2, y);
+      const int o = 32 * ct + 8 * q + 4 * h2;
+      *reinterpret_cast<uint2*>(a.dk + to + o) = round4(a.scale * K[ct][4 * q], a.scale * K[ct][4 * q + 1],
+                                                        a.scale * K[ct][4 * q + 2], a.scale * K[ct][4 * q + 3]);
+      *reinterpret_cast<uint2*>(a.dv + to + o) = round4(V[ct][4 * q], V[ct][4 * q + 1], V[ct][4 * q + 2], V[ct][4 * q + 3]);
     }
 }
 
@@ -635,7 +685,7 @@ kda_status_t attn_check(AttnArgs& a, const void* q, int64_t qs, int64_t qh, cons
   if (cq ? B != 1 : N != B) return KDA_ERR_INVALID;
   if (D != 64 && D != 128) return KDA_ERR_UNSUPPORTED;
   if (flags & ~FLAG_ZERO_REST) return KDA_ERR_INVALID;
-  if (Hq > 1 << 16 || N > 1 << 30 || !fits(B, Tq, kMaxElements) || !fits(B, Tk, kMaxElements) ||
+  if (Hq > 1 << 15 || N > 1 << 30 || !fits(B, Tq, kMaxElements) || !fits(B, Tk, kMaxElements) ||
       !fits(B * Tq, Hq * D, kMaxElements) || !fits(B * Tk, Hk * D, kMaxElements) || Tq >= (int64_t)1 << 31 ||
       Tk >= (int64_t)1 << 31)
     return KDA_ERR_INVALID;
@@ -693,7 +743,7 @@ kda_status_t attn_run_bwd(AttnArgs& a, const void* out, const void* out_lo, cons
   a.slots = a.ak.total / 128 + a.ak.N;
   if (a.slots > (kMaxGrid - 64) / a.Hk) return KDA_ERR_INVALID;
   a.main = a.slots * a.Hk;
-  const kda_status_t s = launch(&attn_dkv_kernel<D>, a.main + clear, 256, st, "attention dk, dv", a);
+  const kda_status_t s = launch(&attn_dkv_kernel<D>, a.main + clear, 512, st, "attention dk, dv", a);
   if (s != KDA_SUCCESS) return s;
   a.slots = a.aq.total * a.G / 128 + a.aq.N;
   if (a.slots > (kMaxGrid - 64) / a.Hk) return KDA_ERR_INVALID;
@@ -709,7 +759,7 @@ using namespace kda;
 extern "C" {
 
 size_t kda_attn_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N) {
-  if (Tq_total < 0 || Tk_total < 0 || Hq < 1 || Hk < 1 || Hq > 1 << 16 || Hq % Hk != 0 || (D != 64 && D != 128) ||
+  if (Tq_total < 0 || Tk_total < 0 || Hq < 1 || Hk < 1 || Hq > 1 << 15 || Hq % Hk != 0 || (D != 64 && D != 128) ||
       N < 1 || N > 1 << 30 || !fits(Tq_total, Hq * D, kMaxElements) || !fits(Tk_total, Hk * D, kMaxElements))
     return 0;
   return 256 + attn_plan(Tq_total, Tk_total, Hq, Hk, D, N).bytes;
@@ -742,7 +792,7 @@ kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride
 }
 
 size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Hq) {
-  if (Tq_total < 0 || Hq < 1 || Hq > 1 << 16 || !fits(Tq_total, Hq * 128, kMaxElements)) return 0;
+  if (Tq_total < 0 || Hq < 1 || Hq > 1 << 15 || !fits(Tq_total, Hq * 128, kMaxElements)) return 0;
   return 256 + align256((size_t)(Tq_total * Hq) * sizeof(float));
 }
 

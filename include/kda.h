@@ -688,7 +688,7 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
  *   scale         finite and positive
  *   flags         0 or KDA_FLAG_ZERO_REST (rows behind the last sequence: lse
  *                 becomes minus infinity there)
- * Tq and Tk are below 2^31.  A NaN or infinity stays within its own sequence
+ * Tq and Tk are below 2^31, Hq is at most 2^15.  A NaN or infinity stays within its own sequence
  * and key head; in v it reaches queries up to 63 tokens before its own, too
  * (a tile's keys are multiplied together, with weight zero).
  */
