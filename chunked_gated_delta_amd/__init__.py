@@ -636,6 +636,8 @@ def _heads(c, t, name, shape):
     """Pointer, token stride and head stride of a bf16 token array [B, T, H, channels] whose tokens and
     heads lie evenly apart."""
     p = c.token(t, name, torch.bfloat16, shape, contiguous=False)
+    if t.is_contiguous():
+        return p, shape[2] * shape[3], shape[3]
     if t.stride(3) != 1 and t.shape[3] > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
     return p, _row_stride(t, name), t.stride(2) if t.shape[2] > 1 else t.shape[3]
@@ -652,7 +654,7 @@ def _la(q, k, v, log_decay):
 
 
 def kda_la_workspace_size(T: int, H: int, K: int, V: int) -> int:
-    """Workspace bytes of kda_la_fwd for T packed tokens and H heads of K and V channels."""
+    """Workspace bytes of kda_la_fwd for T packed tokens and H heads of K and V channels (0: none needed)."""
     return int(_lib.kda_la_workspace_size(T, H, K, V))
 
 
@@ -667,12 +669,12 @@ def kda_la_fwd(q, k, v, log_decay, scale, out, workspace, initial_state=None, fi
     out_t = scale S_t^T q_t, on ``stream`` (default: torch's current stream).
 
     q, k bf16 [B,T,H,K], v bf16 [B,T,H,V], tokens and heads evenly apart; K and V 64 or 128; log_decay
-    fp32 [H], at most 0; out bf16 [B,T,H,V]; workspace >= kda_la_workspace_size(B*T, H, K, V) bytes;
+    fp32 [H], at most 0; out bf16 [B,T,H,V]; workspace >= kda_la_workspace_size(B*T, H, K, V) bytes (None if that is 0);
     initial_state / final_state fp32 [N,H,K,V] or None; cu_seqlens int32 [N+1] or None; flags 0 or
     FLAG_ZERO_REST."""
     c, B, T, H, K, V, p = _la(q, k, v, log_decay)
     N, pcu = _sequences(cu_seqlens, c, B)
-    ws, size = _bytes(c, workspace)
+    ws, size = (None, 0) if workspace is None else _bytes(c, workspace)
     st = (N, H, K, V)
     c.run("kda_la_fwd", stream, *p, float(scale), c.token(out, "out", torch.bfloat16, v.shape), ws, size,
           c.option(initial_state, "initial_state", torch.float32, st),
@@ -723,7 +725,7 @@ def _attn(q, k, v, cu_seqlens_q, cu_seqlens_k):
 
 
 def kda_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, N: int) -> int:
-    """Workspace bytes of kda_attn_fwd for Tq packed queries and Tk packed keys of N sequences."""
+    """Workspace bytes of kda_attn_fwd for Tq packed queries and Tk packed keys of N sequences (0: none needed)."""
     return int(_lib.kda_attn_workspace_size(Tq, Tk, Hq, Hk, D, N))
 
 
@@ -740,10 +742,10 @@ def kda_attn_fwd(q, k, v, scale, out, lse, workspace, out_lo=None, cu_seqlens_q=
     q bf16 [B,Tq,Hq,D], k, v bf16 [B,Tk,Hk,D], tokens and heads evenly apart, D 64 or 128, Hq a multiple
     of Hk; out bf16 [B,Tq,Hq,D]; out_lo the same for kda_attn_bwd (what out's rounding took off), or
     None; lse fp32 [B,Tq,Hq]; workspace >= kda_attn_workspace_size(B*Tq, B*Tk, Hq,
-    Hk, D, N) bytes; cu_seqlens_q, cu_seqlens_k int32 [N+1] (the same one for prompts without a past)
+    Hk, D, N) bytes (None if that is 0); cu_seqlens_q, cu_seqlens_k int32 [N+1] (the same one for prompts without a past)
     or None; flags 0 or FLAG_ZERO_REST."""
     c, sizes, p, pq, pk = _attn(q, k, v, cu_seqlens_q, cu_seqlens_k)
-    ws, size = _bytes(c, workspace)
+    ws, size = (None, 0) if workspace is None else _bytes(c, workspace)
     c.run("kda_attn_fwd", stream, *p, float(scale), c.token(out, "out", torch.bfloat16, q.shape),
           c.option(out_lo, "out_lo", torch.bfloat16, q.shape), c.token(lse, "lse", torch.float32, q.shape[:3]), ws, size, pq, pk, *sizes, int(flags))
 

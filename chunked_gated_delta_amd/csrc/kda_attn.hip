@@ -762,7 +762,7 @@ size_t kda_attn_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, i
   if (Tq_total < 0 || Tk_total < 0 || Hq < 1 || Hk < 1 || Hq > 1 << 15 || Hq % Hk != 0 || (D != 64 && D != 128) ||
       N < 1 || N > 1 << 30 || !fits(Tq_total, Hq * D, kMaxElements) || !fits(Tk_total, Hk * D, kMaxElements))
     return 0;
-  return 256 + attn_plan(Tq_total, Tk_total, Hq, Hk, D, N).bytes;
+  return attn_plan(Tq_total, Tk_total, Hq, Hk, D, N).bytes;
 }
 
 kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -779,13 +779,13 @@ kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride
   for (const void* i : {q, k, v})
     if (same(out, i) || same(out_lo, i)) return KDA_ERR_INVALID;
   if (same(out, out_lo)) return KDA_ERR_INVALID;
-  if (!workspace || workspace_bytes < kda_attn_workspace_size(B * Tq, B * Tk, Hq, Hk, D, N)) return KDA_ERR_WORKSPACE;
+  const AttnPlan p = attn_plan(B * Tq, B * Tk, Hq, Hk, D, N);
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return KDA_ERR_WORKSPACE;
   if (B * Tq == 0) return KDA_SUCCESS;
   a.out = static_cast<uint16_t*>(out);
   a.out_lo = static_cast<uint16_t*>(out_lo);
   a.lse = lse;
   a.part = static_cast<float*>(workspace);
-  const AttnPlan p = attn_plan(B * Tq, B * Tk, Hq, Hk, D, N);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const int64_t clear = attn_clear(cu_seqlens_q, flags);
   return D == 128 ? attn_run_fwd<128>(a, p, clear, st) : attn_run_fwd<64>(a, p, clear, st);

@@ -44,6 +44,7 @@ constexpr int LT = 256;  // threads
 constexpr int64_t kLaWant = 512;   // workgroups at a time: two per CU
 constexpr int64_t kLaMost = 2048;  // workgroups that cutting leads to at most
 constexpr int64_t kLaMinSteps = 4; // steps of a segment at least
+constexpr int64_t kLaAround = 3, kLaLaunches = 8;
 
 // One sweep.  State element (d, c) of sequence n and head h is at
 // (n H + h) K V + d sr + c sc.
@@ -152,6 +153,14 @@ __device__ __forceinline__ bf16x8 cut8(float (&x)[8]) {  // the next bf16 part o
 }
 
 constexpr int kWaitLoads = 0x0f70;  // s_waitcnt vmcnt(0) alone
+
+// A value that is computed where it stands: without this, the addresses of what
+// is seldom done are formed once, before the loop, and hold its registers.
+template <typename X>
+__device__ __forceinline__ X here(X x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uniform(int64_t x) {
@@ -334,16 +343,16 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
       if (src) {
         const float* at = src + (now.starts ? ((int64_t)now.n * a.H + h) * a.KV : segat);
         const int sr = now.starts ? p.sr : DZ, sc = now.starts ? p.sc : 1;
+        const int o = here(4 * g4 * sr + col * sc);
 #pragma unroll
         for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
           for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int d = 16 * dt + 4 * g4 + r;
-              S[dt][ct][r] = at[d * sr + (col + 16 * ct) * sc];
+              S[dt][ct][r] = at[o + (16 * dt + r) * sr + 16 * ct * sc];
               if constexpr (DG && OUT)
-                if (!now.starts) Rs[dt][ct][r] = at[rat + d * DZ + col + 16 * ct];
+                if (!now.starts) Rs[dt][ct][r] = at[rat + o + (16 * dt + r) * sr + 16 * ct * sc];
             }
         // Waited for here: a wait behind the branch would be one for the loads
         // issued after it, on the usual path without these.
@@ -363,111 +372,150 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
     if constexpr (OUT) {
       f32x4 P[4];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        P[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int it = 0; it < 4; ++it) P[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+      auto clear = [&](auto& o) {
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          O[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if constexpr (DG) On[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int ct = 0; ct < NCT; ++ct) o[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+      };
+      // 16 rows from row0, channels 32 kb + 4 g4 and 16 behind them.  With two
+      // states there are registers for one place a lane, not for one a block.
+      const int at0 = at_lds<DX>(l16, 4 * g4);
+      auto frag = [&](const uint16_t* tile, int row0, int kb) {
+        const int o = DG ? here(at0) : at0;
+        return join(*reinterpret_cast<const uint2*>(tile + (o ^ 32 * kb) + row0 * DX),
+                    *reinterpret_cast<const uint2*>(tile + (o ^ (32 * kb + 16)) + row0 * DX));
+      };
+      auto rows = [&](int kb, bf16x8 (&x)[4]) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) x[it] = frag(sX, 16 * it, kb);
+      };
+      auto cut = [&](const f32x4& u, const f32x4& v, bf16x8 (&o)[NP]) {
+        float f[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int m = 0; m < NP; ++m) o[m] = cut8(f);
+      };
+      f32x4 A[DG ? 4 : 1];  // (z q^T)[j][i] over this slice's channels
+      if constexpr (DG) {
+        // Two states leave no registers for reading ahead, if two waves are to
+        // share a SIMD: the pairs first, the states' part after them.
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+          bf16x8 xf[4];
+          rows(kb, xf);
+          const bf16x8 yf = frag(sY, 16 * w, kb);
+#pragma unroll
+          for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf, xf[it], P[it]);
         }
-      }
-      auto frag = [&](const uint16_t* tile, int row, int kb) {
-        const int ch = 32 * kb + 4 * g4;
-        return join(*reinterpret_cast<const uint2*>(tile + at_lds<DX>(row, ch)),
-                    *reinterpret_cast<const uint2*>(tile + at_lds<DX>(row, ch + 16)));
-      };
-      // Rows and state parts are one block of channels ahead of the products, so
-      // that the parts are cut while products run.
-      constexpr int AHEAD = DG ? 0 : 1;  // two states leave no registers for it
-      bf16x8 xf[1 + AHEAD][4], yf[1 + AHEAD], sp[1 + AHEAD][NCT][NP], rp[1 + AHEAD][DG ? NCT : 1][NP];
-      auto ready = [&](int kb) {
-        const int b = kb & AHEAD;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) xf[b][it] = frag(sX, 16 * it + l16, kb);
-        yf[b] = frag(sY, 16 * w + l16, kb);
-      };
-      auto parts = [&](int kb) {
-        auto cut = [&](f32x4 u, f32x4 v, bf16x8 (&o)[NP]) {
-          float f[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+        for (int it = 0; it < 4; ++it) A[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int m = 0; m < NP; ++m) o[m] = cut8(f);
+        for (int kb = 0; kb < NZ / 32; ++kb) {
+          const int o = here(at_lds<NZ>(l16, 8 * g4)) ^ 32 * kb;
+          const bf16x8 zf = *reinterpret_cast<const bf16x8*>(sZ + o + 16 * w * NZ);
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            A[it] = mfma_bf16(zf, *reinterpret_cast<const bf16x8*>(sQ + o + 16 * it * NZ), A[it]);
+        }
+      } else {
+        // Rows and state parts are one block of channels ahead of the products, so
+        // that the parts are cut while products run.
+        bf16x8 xf[2][4], yf[2], sp[2][NCT][NP];
+        clear(O);
+        auto ready = [&](int kb) {
+          rows(kb, xf[kb & 1]);
+          yf[kb & 1] = frag(sY, 16 * w, kb);
         };
+        auto parts = [&](int kb) {
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp[kb & AHEAD][ct]);
-          if constexpr (DG) cut(Rs[2 * kb][ct], Rs[2 * kb + 1][ct], rp[kb & AHEAD][ct]);
-        }
-      };
-      ready(0);
-      __builtin_amdgcn_sched_barrier(0);
-      parts(0);
+          for (int ct = 0; ct < NCT; ++ct) cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp[kb & 1][ct]);
+        };
+        ready(0);
+        __builtin_amdgcn_sched_barrier(0);
+        parts(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int kb = 0; kb < NKB; ++kb) {
-        const int b = kb & AHEAD;
-        if (kb + AHEAD < NKB && kb + AHEAD > 0) {
-          ready(kb + AHEAD);
-          parts(kb + AHEAD);
-        }
+        for (int kb = 0; kb < NKB; ++kb) {
+          const int b = kb & 1;
+          if (kb + 1 < NKB) {
+            ready(kb + 1);
+            parts(kb + 1);
+          }
 #pragma unroll
-        for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf[b], xf[b][it], P[it]);
+          for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf[b], xf[b][it], P[it]);
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
+          for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-          for (int m = 0; m < NP; ++m)
+            for (int m = 0; m < NP; ++m)
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-              O[it][ct] = mfma_bf16(sp[b][ct][m], xf[b][it], O[it][ct]);
-              if constexpr (DG) On[it][ct] = mfma_bf16(rp[b][ct][m], xf[b][it], On[it][ct]);
-            }
-        if constexpr (!DG) {  // reads first, then products with the cutting between them
+              for (int it = 0; it < 4; ++it) O[it][ct] = mfma_bf16(sp[b][ct][m], xf[b][it], O[it][ct]);
+          // reads first, then products with the cutting between them
           if (kb + 1 < NKB) __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
 #pragma unroll
           for (int i = 0; i < 4 + 4 * NCT * NP; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      f32x4 A[DG ? 4 : 1];  // (z q^T)[j][i] over this slice's channels
-      if constexpr (DG) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it) A[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < NZ / 32; ++kb) {
-          const bf16x8 zf = *reinterpret_cast<const bf16x8*>(sZ + at_lds<NZ>(16 * w + l16, 32 * kb + 8 * g4));
-#pragma unroll
-          for (int it = 0; it < 4; ++it)
-            A[it] = mfma_bf16(zf, *reinterpret_cast<const bf16x8*>(sQ + at_lds<NZ>(16 * it + l16, 32 * kb + 8 * g4)), A[it]);
-        }
+        __builtin_amdgcn_s_setprio(0);
       }
       float pairs = 0.0f;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         if (it < (w & 2)) continue;  // nothing reads those
         float v[4];
+        const float n0 = here((float)(l16 - 4 * g4 - 16 * w));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int n = 16 * (it - w) + l16 - 4 * g4 - r;
-          v[r] = n >= 0 ? P[it][r] * (it == w ? dec0[r] : dec1[r] * far[it]) : 0.0f;
-          if constexpr (DG) pairs += n > 0 ? (float)n * v[r] * A[it][r] : 0.0f;
+          const float n = n0 + (float)(16 * it - r);  // i - j
+          v[r] = n >= 0.0f ? P[it][r] * (it == w ? dec0[r] : dec1[r] * far[it]) : 0.0f;
+          if constexpr (DG) pairs += n > 0.0f ? n * v[r] * A[it][r] : 0.0f;
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
           reinterpret_cast<uint2*>(&sP[m][2 * it + (w >> 1)][lane])[w & 1] = cut_part(v);
       }
-      if constexpr (DG) dg += pairs;
+      if constexpr (DG) {
+        dg += pairs;
+        __builtin_amdgcn_sched_barrier(0);
+        clear(O);
+        clear(On);
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+          bf16x8 xf[4];
+          rows(kb, xf);
+#pragma unroll
+          for (int ct = 0; ct < NCT; ++ct) {
+            bf16x8 sp[NP];
+            cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp);
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+              for (int it = 0; it < 4; ++it) O[it][ct] = mfma_bf16(sp[m], xf[it], O[it][ct]);
+            cut(Rs[2 * kb][ct], Rs[2 * kb + 1][ct], sp);
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+              for (int it = 0; it < 4; ++it) On[it][ct] = mfma_bf16(sp[m], xf[it], On[it][ct]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
       float sum = 0.0f;
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-          float q[4];
-          if constexpr (DG)
-            widen4(*reinterpret_cast<const uint2*>(sQ + at_lds<NZ>(16 * it + l16, w * ZW + 16 * ct + 4 * g4)), q);
+          float q[4], i1 = 0.0f;
+          if constexpr (DG) {
+            widen4(*reinterpret_cast<const uint2*>(sQ + here(at_lds<NZ>(l16, w * ZW + 4 * g4)) + 16 * it * NZ), q);
+            i1 = here((float)l16) + (float)(16 * it + 1);
+          }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if constexpr (DG) sum += (On[it][ct][r] + O[it][ct][r] * (float)(16 * it + l16 + 1)) * lamo[it] * q[r];
+            if constexpr (DG) sum += (On[it][ct][r] + O[it][ct][r] * i1) * lamo[it] * q[r];
             O[it][ct][r] *= lamo[it];
           }
         }
@@ -478,29 +526,29 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
     bf16x8 zr[2][NCT];
     {
       const float full = sLam[len];
-      bf16x8 yt[NDT];
-      float wz[2][8];
-      auto columns = [&](int ks) {
-        const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
-#pragma unroll
-        for (int dt = 0; dt < NDT; ++dt) {
-          const int yc = 16 * dt + 4 * (l16 & 3);
-          yt[dt] = join(tr_read(sY + at_lds<DX>(jr, yc)), tr_read(sY + at_lds<DX>(jr + 16, yc)));
-        }
+      auto column = [&](int ks, int dt) {  // channels 16 dt .. + 15 of y, 32 rows, as the A operand
+        const int at1 = at_lds<DX>(4 * g4 + (l16 >> 2), 4 * (l16 & 3)), o = (DG ? here(at1) : at1) ^ 16 * dt;
+        return join(tr_read(sY + o + 32 * ks * DX), tr_read(sY + o + (32 * ks + 16) * DX));
       };
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
+      auto values = [&](int ks, float (&wz)[8]) {  // z's rows, and their decays
         const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
-        lds_f32x4(sW + 32 * ks + 4 * g4, wz[ks]);
-        lds_f32x4(sW + 32 * ks + 16 + 4 * g4, wz[ks] + 4);
+        lds_f32x4(sW + 32 * ks + 4 * g4, wz);
+        lds_f32x4(sW + 32 * ks + 16 + 4 * g4, wz + 4);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
           const int zc = w * ZW + 16 * ct + 4 * (l16 & 3);
           zr[ks][ct] = join(tr_read(sZ + at_lds<NZ>(jr, zc)), tr_read(sZ + at_lds<NZ>(jr + 16, zc)));
         }
+      };
+      float wz[2][8];
+      bf16x8 yt[DG ? 1 : NDT];
+      if constexpr (!DG) {
+        values(0, wz[0]);
+        values(1, wz[1]);
+#pragma unroll
+        for (int dt = 0; dt < NDT; ++dt) yt[dt] = column(0, dt);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      columns(0);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
@@ -512,17 +560,17 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
           }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
+        if constexpr (DG) values(ks, wz[ks]);
         bf16x8 zw[NCT][3], zn[DG ? NCT : 1][3];
+        const float left1 = DG ? here((float)(len - 1 - 4 * g4)) : 0.0f;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
           float f[8], fn[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             f[e] = wz[ks][e] * (float)zr[ks][ct][e];
-            if constexpr (DG) {
-              const int n = len - 1 - (32 * ks + 4 * g4 + (e & 3) + 16 * (e >> 2));
-              fn[e] = f[e] * (float)(n >= 0 ? n : 0);
-            }
+            if constexpr (DG)  // behind the step's end f is zero
+              fn[e] = f[e] * (left1 - (float)(32 * ks + (e & 3) + 16 * (e >> 2)));
           }
 #pragma unroll
           for (int m = 0; m < 3; ++m) {
@@ -530,18 +578,33 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
             if constexpr (DG) zn[ct][m] = cut8(fn);
           }
         }
+        if constexpr (DG) {
 #pragma unroll
-        for (int m = 0; m < 3; ++m)
+          for (int dt = 0; dt < NDT; ++dt) {
+            const bf16x8 y = column(ks, dt);
 #pragma unroll
-          for (int ct = 0; ct < NCT; ++ct)
+            for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-            for (int dt = 0; dt < NDT; ++dt) {
-              S[dt][ct] = mfma_bf16(yt[dt], zw[ct][m], S[dt][ct]);
-              if constexpr (DG) Rs[dt][ct] = mfma_bf16(yt[dt], zn[ct][m], Rs[dt][ct]);
-            }
-        if (ks == 0) {
-          columns(1);
+              for (int m = 0; m < 3; ++m) {
+                S[dt][ct] = mfma_bf16(y, zw[ct][m], S[dt][ct]);
+                Rs[dt][ct] = mfma_bf16(y, zn[ct][m], Rs[dt][ct]);
+              }
+          }
           __builtin_amdgcn_sched_barrier(0);
+        } else {
+          __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+          for (int m = 0; m < 3; ++m)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+              for (int dt = 0; dt < NDT; ++dt) S[dt][ct] = mfma_bf16(yt[dt], zw[ct][m], S[dt][ct]);
+          __builtin_amdgcn_s_setprio(0);
+          if (ks == 0) {
+#pragma unroll
+            for (int dt = 0; dt < NDT; ++dt) yt[dt] = column(1, dt);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
       }
     }
@@ -587,7 +650,7 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
       float* dst = OUT ? (now.ends ? p.sout : nullptr) : p.seg;
       const int64_t at = OUT ? ((int64_t)now.n * a.H + h) * a.KV : segat;
       const int sr = OUT ? p.sr : DZ, sc = OUT ? p.sc : 1;
-      float sum = 0.0f;
+      const int o = here(4 * g4 * sr + col * sc);
       if (dst) {
 #pragma unroll
         for (int dt = 0; dt < NDT; ++dt)
@@ -595,22 +658,22 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
           for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int d = 16 * dt + 4 * g4 + r, cc = col + 16 * ct;
-              dst[at + d * sr + cc * sc] = S[dt][ct][r];
-              if constexpr (DG && !OUT) dst[rat + at + d * sr + cc * sc] = Rs[dt][ct][r];
+              const int e = o + (16 * dt + r) * sr + 16 * ct * sc;
+              dst[at + e] = S[dt][ct][r];
+              if constexpr (DG && !OUT) dst[rat + at + e] = Rs[dt][ct][r];
             }
       }
       if constexpr (DG && OUT)
         if (now.ends && p.rend) {
+          float sum = 0.0f;
 #pragma unroll
           for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                sum += Rs[dt][ct][r] * p.rend[at + (16 * dt + 4 * g4 + r) * sr + (col + 16 * ct) * sc];
+              for (int r = 0; r < 4; ++r) sum += Rs[dt][ct][r] * p.rend[at + o + (16 * dt + r) * sr + 16 * ct * sc];
+          dg += sum;
         }
-      if constexpr (DG) dg += sum;
     }
     if (!more) break;
     first = last;
@@ -629,49 +692,63 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
   }
 }
 
-// The states that enter the segments, from those that each of them leaves by
-// itself: the stretch that goes on beyond segment s starts inside it, or
-// entered it and crosses it whole.
+// The states that enter the segments of a block, from those that each of them
+// leaves by itself: the stretch that goes on beyond segment s starts inside it,
+// or entered it and crosses it whole.  What happens at each segment is found by
+// a lane of its own; the states of four segments are asked for at a time.
 template <bool DG>
 __global__ void __launch_bounds__(LT) la_join_kernel(const LaArgs a) {
-  const int per = a.KV / (LT * 4);  // workgroups per head
-  const int h = blockIdx.x / per % a.H;
-  const LaPass& p = a.p[blockIdx.x / per / a.H];
-  const int64_t e = (int64_t)h * a.KV + ((int64_t)(blockIdx.x % per) * LT + threadIdx.x) * 4;
-  const int64_t step = (int64_t)a.H * a.KV;
+  const int per = a.KV / (LT * 4), blocks = a.nseg / a.spb;  // workgroups per head
+  int id = blockIdx.x;
+  const int piece = id % per, h = (id /= per) % a.H, b = (id /= a.H) % blocks;
+  const LaPass& p = a.p[id / blocks];
+  const int64_t e = (int64_t)h * a.KV + ((int64_t)piece * LT + threadIdx.x) * 4, step = (int64_t)a.H * a.KV;
   const int64_t R = axis_rows(a.ax);
-  const float gh = a.g[h];
-  float4 E = make_float4(0.f, 0.f, 0.f, 0.f), Q = E;
-  for (int k = 0; k < a.nseg; ++k) {
-    const int s = p.rev ? a.nseg - 1 - k : k;
-    float4* at = reinterpret_cast<float4*>(p.seg + s * step + e);
-    float4* rat = reinterpret_cast<float4*>(p.seg + (a.nseg + s) * step + e);
-    const LaSeg sg = la_seg(a, s, R);
-    bool on = false, whole = false;
+  const int lane = threadIdx.x & 63;  // at most 64 segments a block
+  bool on = false;                    // a stretch goes on beyond the segment
+  float f = 0.0f, m = 0.0f;           // its decay across the segment, if it entered it, and tokens
+  if (lane < a.spb) {
+    const LaSeg sg = la_seg(a, b * a.spb + lane, R);
     if (sg.p0 < sg.p1) {
       const int64_t n = axis_owner(a.ax, p.rev ? sg.p0 : sg.p1 - 1);
       const int64_t bos = axis_start(a.ax, n), eos = la_end(a.ax, n, R);
       on = p.rev ? bos < sg.p0 : eos > sg.p1;
-      whole = p.rev ? eos > sg.p1 : bos < sg.p0;
+      m = (float)(sg.p1 - sg.p0);
+      if (on && (p.rev ? eos > sg.p1 : bos < sg.p0)) f = la_pow(a.g[h], (double)(sg.p1 - sg.p0));
     }
-    float4 own = make_float4(0.f, 0.f, 0.f, 0.f), rown = own;
-    if (on) {
-      own = *at;
-      if (DG) rown = *rat;
+  }
+  constexpr int AT = 4;
+  float4 E = make_float4(0.f, 0.f, 0.f, 0.f), Q = E;
+  for (int k0 = 0; k0 < a.spb; k0 += AT) {
+    float4 own[AT], rown[AT];
+#pragma unroll
+    for (int u = 0; u < AT; ++u) {
+      const int k = k0 + u < a.spb ? k0 + u : a.spb - 1, s = b * a.spb + (p.rev ? a.spb - 1 - k : k);
+      own[u] = *reinterpret_cast<const float4*>(p.seg + s * step + e);
+      if (DG) rown[u] = *reinterpret_cast<const float4*>(p.seg + (a.nseg + s) * step + e);
     }
-    *at = E;
-    if (DG) *rat = Q;
-    const float f = whole && on ? la_pow(gh, (double)(sg.p1 - sg.p0)) : 0.0f, m = (float)(sg.p1 - sg.p0);
-    if (DG) {
-      Q.x = f != 0.0f ? f * (Q.x + m * E.x) + rown.x : rown.x;
-      Q.y = f != 0.0f ? f * (Q.y + m * E.y) + rown.y : rown.y;
-      Q.z = f != 0.0f ? f * (Q.z + m * E.z) + rown.z : rown.z;
-      Q.w = f != 0.0f ? f * (Q.w + m * E.w) + rown.w : rown.w;
+#pragma unroll
+    for (int u = 0; u < AT; ++u) {
+      const int k = k0 + u;
+      if (k >= a.spb) break;
+      const int l = p.rev ? a.spb - 1 - k : k, s = b * a.spb + l;
+      *reinterpret_cast<float4*>(p.seg + s * step + e) = E;
+      if (DG) *reinterpret_cast<float4*>(p.seg + (a.nseg + s) * step + e) = Q;
+      const bool go = __shfl((int)on, l) != 0;
+      const float fk = __shfl(f, l), mk = __shfl(m, l);
+      // Where nothing goes on, what the segment's place holds is not a state.
+      auto next = [&](float x, float y) { return !go ? 0.0f : fk != 0.0f ? fk * x + y : y; };
+      if (DG) {
+        Q.x = next(Q.x + mk * E.x, rown[u].x);
+        Q.y = next(Q.y + mk * E.y, rown[u].y);
+        Q.z = next(Q.z + mk * E.z, rown[u].z);
+        Q.w = next(Q.w + mk * E.w, rown[u].w);
+      }
+      E.x = next(E.x, own[u].x);
+      E.y = next(E.y, own[u].y);
+      E.z = next(E.z, own[u].z);
+      E.w = next(E.w, own[u].w);
     }
-    E.x = whole && on ? f * E.x + own.x : own.x;
-    E.y = whole && on ? f * E.y + own.y : own.y;
-    E.z = whole && on ? f * E.z + own.z : own.z;
-    E.w = whole && on ? f * E.w + own.w : own.w;
   }
 }
 
@@ -759,20 +836,23 @@ struct LaPlan {
   int slices, spb;
   int64_t L, nseg;
 };
-LaPlan la_plan(int64_t blocks, int64_t block, int64_t H, int64_t DZ, int64_t passes) {
+LaPlan la_plan(int64_t blocks, int64_t block, int64_t H, int64_t DZ, int64_t passes, bool dg) {
   LaPlan pl;
   pl.slices = (int)(DZ / 64);
   const int64_t chains = blocks * H * pl.slices * passes;
   // Steps that the busiest CU does one after another, three of the first pass
-  // taken for one of the second.
+  // taken for one of the second; what a workgroup does before and after its steps
+  // is counted as kLaAround of them, the two launches more as kLaLaunches.  With the
+  // decay's gradient the second pass has one workgroup per CU, not two.
+  const int64_t want = dg ? kLaWant / 2 : kLaWant;
   int64_t spb = 1, best = INT64_MAX;
   for (int64_t n = 1; n <= 64 && (n == 1 || chains * n <= kLaMost); ++n) {
     const int64_t len = (block + n * LC - 1) / (n * LC);
     if (n > 1 && len < kLaMinSteps) break;
-    const int64_t second = (chains * n + kLaWant - 1) / kLaWant * len;
-    const int64_t first = n > 1 ? (chains * (n - 1) + kLaWant - 1) / kLaWant * len : 0;
-    if (3 * second + first + (n > 1 ? 24 : 0) < best) {
-      best = 3 * second + first + (n > 1 ? 24 : 0);
+    int64_t cost = 3 * ((chains * n + want - 1) / want * (len + kLaAround));
+    if (n > 1) cost += (chains * (n - 1) + kLaWant - 1) / kLaWant * (len + kLaAround) + 3 * kLaLaunches;
+    if (cost < best) {
+      best = cost;
       spb = n;
     }
   }
@@ -788,12 +868,17 @@ LaPlan la_plan(int64_t blocks, int64_t block, int64_t H, int64_t DZ, int64_t pas
 // and, a cut block having more than 6 steps and a segment more than 3, at most
 // T / 128 pieces a head.
 size_t la_states_bytes(int64_t T_total, int64_t H, int64_t K, int64_t V) {
-  const int64_t by_length = T_total / 128 * H;
+  const int64_t by_length = T_total > 6 * LC ? T_total / 128 * H : 0;
   return (size_t)((by_length < kLaMost ? by_length : kLaMost) * K * V) * sizeof(float);
 }
 // Bytes of the decay gradient's parts, for at most N blocks of the axis.
 size_t la_part_bytes(int64_t N, int64_t H) {
   return align256((size_t)(N * H * 2 + kLaMost) * sizeof(float));
+}
+
+bool la_sizes_ok(int64_t T_total, int64_t H, int64_t K, int64_t V) {
+  return T_total >= 0 && H >= 1 && H <= 1 << 16 && (K == 64 || K == 128) && (V == 64 || V == 128) &&
+         fits(T_total, H * 128, kMaxElements);
 }
 
 kda_status_t la_check(const void* q, int64_t qs, int64_t qh, const void* k, int64_t ks, int64_t kh, const void* v,
@@ -821,7 +906,8 @@ kda_status_t la_launch(LaArgs& a, bool empties, hipStream_t st) {
   if (a.spb > 1) {  // otherwise every segment starts at a sequence's start
     kda_status_t s = launch(&la_sweep_kernel<DX, ZW, false, DG>, groups, LT, st, "linear attention segments", a);
     if (s != KDA_SUCCESS) return s;
-    s = launch(&la_join_kernel<DG>, (int64_t)a.passes * a.H * (a.KV / (LT * 4)), LT, st, "linear attention join", a);
+    s = launch(&la_join_kernel<DG>, (int64_t)a.passes * (a.nseg / a.spb) * a.H * (a.KV / (LT * 4)), LT, st,
+               "linear attention join", a);
     if (s != KDA_SUCCESS) return s;
   }
   return launch(&la_sweep_kernel<DX, ZW, true, DG>, groups + more, LT, st, "linear attention", a);
@@ -837,8 +923,8 @@ kda_status_t la_sweep(LaArgs& a, int64_t DX, const LaPlan& pl, bool empties, hip
 
 // The arguments of a sweep of `passes` passes with DZ channels of z.
 LaPlan la_common(LaArgs& a, const float* g, const int32_t* cu, int64_t B, int64_t T, int64_t H, int64_t K, int64_t V,
-                 int64_t N, int64_t DZ, int passes, unsigned flags) {
-  const LaPlan pl = la_plan(B, T, H, DZ, passes);
+                 int64_t N, int64_t DZ, int passes, bool dg, unsigned flags) {
+  const LaPlan pl = la_plan(B, T, H, DZ, passes, dg);
   a = LaArgs{};
   a.ax = make_axis(cu, T, B * T, N);
   a.g = g;
@@ -863,10 +949,7 @@ using namespace kda;
 extern "C" {
 
 size_t kda_la_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V) {
-  if (T_total < 0 || H < 1 || H > 1 << 16 || (K != 64 && K != 128) || (V != 64 && V != 128) ||
-      !fits(T_total, H * 128, kMaxElements))
-    return 0;
-  return 256 + la_states_bytes(T_total, H, K, V);
+  return !la_sizes_ok(T_total, H, K, V) ? 0 : la_states_bytes(T_total, H, K, V);
 }
 
 kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -881,9 +964,10 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   if (B * T > 0 && !out) return KDA_ERR_INVALID;
   if (!aligned_all(16, {out, workspace, initial_state, final_state})) return KDA_ERR_INVALID;
   if (same(q, out) || same(k, out) || same(v, out) || same(initial_state, final_state)) return KDA_ERR_INVALID;
-  if (!workspace || workspace_bytes < kda_la_workspace_size(B * T, H, K, V)) return KDA_ERR_WORKSPACE;
+  const size_t need = kda_la_workspace_size(B * T, H, K, V);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   LaArgs a;
-  const LaPlan pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, flags);
+  const LaPlan pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
   LaPass& p = a.p[0];
   p.x = static_cast<const uint16_t*>(q);
   p.y = static_cast<const uint16_t*>(k);
@@ -901,8 +985,8 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
 }
 
 size_t kda_la_bwd_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V, int64_t N) {
-  if (!kda_la_workspace_size(T_total, H, K, V) || N < 1 || N > 1 << 30) return 0;
-  return 256 + 4 * la_states_bytes(T_total, H, K, V) + la_part_bytes(N, H);
+  if (!la_sizes_ok(T_total, H, K, V) || N < 1 || N > 1 << 30) return 0;
+  return 4 * la_states_bytes(T_total, H, K, V) + la_part_bytes(N, H);
 }
 
 kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -935,7 +1019,7 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
 
   // dq: of do, v, k; the state is S^T
   LaArgs a;
-  LaPlan pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, flags);
+  LaPlan pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, d_log_decay != nullptr, flags);
   LaPass& p = a.p[0];
   p.x = dp, p.xs = H * V, p.xh = V;
   p.y = vp, p.ys = v_stride, p.yh = v_head_stride;
@@ -983,16 +1067,16 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   pv.seg = reinterpret_cast<float*>(ws + 2 * sb);
   pk.seg = reinterpret_cast<float*>(ws + 3 * sb);
   if (K == V) {  // one launch: both read q and do
-    pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 2, flags);
+    pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 2, false, flags);
     a.p[0] = pv;
     a.p[1] = pk;
     return la_sweep<false>(a, K, pl, d_initial_state && none, st);
   }
-  pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, flags);
+  pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
   a.p[0] = pv;
   s = la_sweep<false>(a, K, pl, d_initial_state && none, st);
   if (s != KDA_SUCCESS) return s;
-  pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, flags);
+  pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, false, flags);
   a.p[0] = pk;
   return la_sweep<false>(a, V, pl, false, st);
 }

@@ -298,12 +298,17 @@ def kda_qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_we
     return _QkNormRope.apply(*args) if _wants_derivative(q, k, q_weight, k_weight, inv_freq) else _qk_forward(*args)
 
 
+def _maybe_scratch(size, like):
+    return _scratch(size, like) if size else None
+
+
 def _la_forward(q, k, v, log_decay, initial_state, scale, cu_seqlens):
     B, T, H, K = q.shape
     V = v.shape[3]
     out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     final = torch.empty(_count(q, cu_seqlens), H, K, V, dtype=torch.float32, device=q.device)
-    kda_la_fwd(q, k, v, log_decay, scale, out, _scratch(kda_la_workspace_size(B * T, H, K, V), q), initial_state, final,
+    kda_la_fwd(q, k, v, log_decay, scale, out, _maybe_scratch(kda_la_workspace_size(B * T, H, K, V), q), initial_state,
+               final,
                cu_seqlens, FLAG_ZERO_REST)
     return out, final
 
@@ -352,7 +357,7 @@ def _attn_forward(q, k, v, scale, cu_q, cu_k, out_lo=None):
     Tk, Hk = k.shape[1:3]
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    ws = _scratch(kda_attn_workspace_size(B * Tq, B * Tk, Hq, Hk, D, _count(q, cu_q)), q)
+    ws = _maybe_scratch(kda_attn_workspace_size(B * Tq, B * Tk, Hq, Hk, D, _count(q, cu_q)), q)
     kda_attn_fwd(q, k, v, scale, out, lse, ws, out_lo, cu_q, cu_k, FLAG_ZERO_REST)
     return out, lse
 

@@ -625,7 +625,8 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
  *                 infinity: nothing is kept).  Values above 0 are not refused;
  *                 the states then grow, and overflow where the formula does.
  *   out           [B, T, H, V] written, contiguous
- *   workspace     scratch of >= kda_la_workspace_size(B * T, H, K, V) bytes
+ *   workspace     scratch of >= kda_la_workspace_size(B * T, H, K, V) bytes;
+ *                 NULL will do where that is 0 (short calls)
  *   initial_state fp32 [N, H, K, V] or NULL for zeros
  *   final_state   fp32 [N, H, K, V] written, or NULL; not initial_state
  *   scale         finite
@@ -681,7 +682,7 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
  *                 which kda_attn_bwd needs
  *   lse           fp32 [B, Tq, Hq] written (natural logarithm)
  *   workspace     scratch of >= kda_attn_workspace_size(B * Tq, B * Tk, Hq,
- *                 Hk, D, N) bytes
+ *                 Hk, D, N) bytes; NULL will do where that is 0 (whole prompts)
  *   cu_seqlens_q, cu_seqlens_k  int32 [N + 1] offsets of the queries and the
  *                 keys with B == 1 (the same array for prompts without a
  *                 past), or both NULL for N == B

@@ -73,7 +73,9 @@ REFUSED = [
        dict(Tk=1 << 31), dict(Hq=1 << 17), dict(B=1 << 40, N=1 << 40), dict(N=1 << 31, cq=P[18], ck=P[18]), dict(scale=0.0),
        dict(scale=-1.0), dict(scale=NAN), dict(scale=INF))],
     *[(f, o, UNSUPPORTED) for f in AT for o in (dict(D=32), dict(D=96), dict(D=256))],
-    *[(f, o, WORKSPACE) for f in (*LA, *AT) for o in (dict(ws=None), dict(size=255))],
+    *[(f, o, WORKSPACE) for f in (la_bwd, at_bwd) for o in (dict(ws=None), dict(size=63))],
+    *[(la_fwd, dict(T=4096) | o, WORKSPACE) for o in (dict(ws=None), dict(size=1 << 16))],
+    (at_fwd, dict(ws=None, Tq=1, Tk=4096, B=64, N=64), WORKSPACE),
     (at_fwd, dict(size=1 << 16, Tq=1, Tk=4096, B=64, N=64), WORKSPACE),  # parts of the keys need room
     (la_bwd, dict(size=1 << 20, T=4096, dg=P[12]), WORKSPACE),
     # an output that is an input, or another output
@@ -113,11 +115,11 @@ def test_workspaces_are_bounded():
     """States of at most 2048 pieces of a call, and none of a short one; parts of split keys only for few rows."""
     for T in (1, 4096, 1 << 24):
         for H in (1, 7, 96, 200):
-            assert 0 < kda.kda_la_workspace_size(T, H, 128, 128) <= 256 + min(2048, T // 128 * H) * 65536
-            assert kda.kda_la_bwd_workspace_size(T, H, 128, 128, 4) <= 512 + 4 * min(2048, T // 128 * H) * 65536 + \
+            assert kda.kda_la_workspace_size(T, H, 128, 128) <= min(2048, T // 128 * H) * 65536
+            assert kda.kda_la_bwd_workspace_size(T, H, 128, 128, 4) <= 256 + 4 * min(2048, T // 128 * H) * 65536 + \
                 4 * (4 * H * 2 + 2048) + 256
-    assert kda.kda_attn_workspace_size(16384, 16384, 32, 8, 128, 1) == 256
-    assert kda.kda_attn_workspace_size(64, 64 * 8192, 32, 8, 128, 64) <= 256 + 64 * 64 * 32 * 129 * 4 + 256
+    assert kda.kda_la_workspace_size(384, 1, 128, 128) == 0 == kda.kda_attn_workspace_size(16384, 16384, 32, 8, 128, 1)
+    assert 0 < kda.kda_attn_workspace_size(64, 64 * 8192, 32, 8, 128, 64) <= 64 * 64 * 32 * 129 * 4 + 256
     assert kda.kda_attn_bwd_workspace_size(100, 3) >= 1200
 
 
