@@ -139,7 +139,7 @@ for _name, _args in {
 for _name, _n in {"kda_glr_workspace_size": 3, "kda_glr_states_size": 3, "kda_glr_bwd_workspace_size": 3,
                   "kda_conv_bwd_workspace_size": 3, "kda_qk_rope_bwd_workspace_size": 4,
                   "kda_la_workspace_size": 4, "kda_la_bwd_workspace_size": 5,
-                  "kda_attn_workspace_size": 6, "kda_attn_bwd_workspace_size": 2}.items():
+                  "kda_attn_workspace_size": 6, "kda_attn_bwd_workspace_size": 6}.items():
     getattr(_lib, _name).argtypes = [_I64] * _n
     getattr(_lib, _name).restype = _SZ
 
@@ -729,9 +729,9 @@ def kda_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, N: int) 
     return int(_lib.kda_attn_workspace_size(Tq, Tk, Hq, Hk, D, N))
 
 
-def kda_attn_bwd_workspace_size(Tq: int, Hq: int) -> int:
-    """Workspace bytes of kda_attn_bwd for Tq packed queries of Hq heads."""
-    return int(_lib.kda_attn_bwd_workspace_size(Tq, Hq))
+def kda_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, N: int) -> int:
+    """Workspace bytes of kda_attn_bwd for Tq packed queries and Tk packed keys of N sequences."""
+    return int(_lib.kda_attn_bwd_workspace_size(Tq, Tk, Hq, Hk, D, N))
 
 
 def kda_attn_fwd(q, k, v, scale, out, lse, workspace, out_lo=None, cu_seqlens_q=None, cu_seqlens_k=None, flags=0,
@@ -754,7 +754,7 @@ def kda_attn_bwd(q, k, v, scale, out, out_lo, lse, d_out, dq, dk, dv, workspace,
                  cu_seqlens_k=None, flags=0, stream=None):
     """Enqueue the gradients of a kda_attn_fwd call with the same inputs, which wrote out, out_lo and lse,
     for d_out bf16 [B,Tq,Hq,D] and d_lse (fp32 [B,Tq,Hq], None for zero).  Writes dq, dk and dv (bf16,
-    contiguous); workspace >= kda_attn_bwd_workspace_size(B*Tq, Hq) bytes."""
+    contiguous); workspace >= kda_attn_bwd_workspace_size(B*Tq, B*Tk, Hq, Hk, D, N) bytes."""
     c, sizes, p, pq, pk = _attn(q, k, v, cu_seqlens_q, cu_seqlens_k)
     ws, size = _bytes(c, workspace)
     bf, ls = torch.bfloat16, q.shape[:3]

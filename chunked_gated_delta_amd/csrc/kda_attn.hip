@@ -41,6 +41,7 @@ namespace kda {
 namespace {
 
 constexpr float LN2 = 0.6931471805599453f;
+constexpr int64_t kAttnRound = 256;  // CUs
 constexpr int64_t kAttnWant = 1024;  // workgroups that a call with few rows is split into
 
 struct AttnArgs {
@@ -48,7 +49,7 @@ struct AttnArgs {
   uint16_t* out;
   uint16_t* out_lo;  // out's rounding errors, or nullptr
   float* lse;
-  float* part;  // [splits][rows of q][Hq][D] partial outputs, then their lse
+  float* part;  // forward: [splits][rows of q][Hq][D] outputs, then their lse; backward: [splits] dk, dv sums in fp32
   const uint16_t* d_out;  // [tokens][Hq][D]
   const float* delta;     // [tokens][Hq]
   uint16_t *dq, *dk, *dv;
@@ -475,7 +476,10 @@ __global__ void __launch_bounds__(256, 2) attn_dq_kernel(const AttnArgs a) {
 // read from LDS as operands: held in registers (one wave a SIMD, a tile ahead)
 // the same work took 384 us in place of 264 (2 x 4097 tokens x 12 heads of 128: 780
 // TFLOP/s of the four products).
-template <int D>
+//
+// With few tiles (few key heads, whose groups make each tile's rows many) the rows
+// of a tile are split over workgroups, which leave fp32 sums to be added.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(512, 2) attn_dkv_kernel(const AttnArgs a) {
   constexpr int NT = 256, BN = 128, RT = 32, ND = D / 16, NC = D / 32;
   __shared__ __align__(16) uint16_t sKV[2][BN * D], sR[2][2][2][RT * D];  // k, v; q, do of a stream's two buffers
@@ -489,13 +493,20 @@ __global__ void __launch_bounds__(512, 2) attn_dkv_kernel(const AttnArgs a) {
   }
   const int64_t id = blockIdx.x;
   const int hk = (int)(id % a.Hk);
-  const Place at = tile_place<BN>(a.ak, id / a.Hk, 1);  // the first keys are seen by the most rows
+  const int split = SPLIT ? (int)(id / a.Hk % a.splits) : 0;
+  // the first keys are seen by the most rows
+  const Place at = tile_place<BN>(a.ak, id / a.Hk / (SPLIT ? a.splits : 1), 1);
   const Span sq = span(a.aq, at.n), sk = span(a.ak, at.n);
   const int64_t key0 = at.tile * BN;
   if (key0 >= sk.len) return;
   const int64_t off = sk.len - sq.len, rows = sq.len * a.G;
   const int64_t t0 = key0 > off ? key0 - off : 0;  // first token that sees a key of the tile
-  const int64_t i0 = t0 * a.G / RT, i1 = (rows + RT - 1) / RT;
+  int64_t i0 = t0 * a.G / RT, i1 = (rows + RT - 1) / RT;
+  if (SPLIT) {  // pairs of tiles, one for each stream
+    const int64_t pairs = i1 > i0 ? (i1 - i0 + 1) / 2 : 0, per = (pairs + a.splits - 1) / a.splits * 2;
+    i0 += per * split;
+    i1 = i0 + per < i1 ? i0 + per : i1;
+  }
   {
     TileRegs<D, BN, 512> r;
     r.load(a.k + sk.at * a.ks + hk * a.kh, a.ks, key0, sk.len);
@@ -641,6 +652,19 @@ __global__ void __launch_bounds__(512, 2) attn_dkv_kernel(const AttnArgs a) {
   const int64_t key = key0 + 32 * w + (lane & 31);
   if (st == 1 || key >= sk.len) return;
   const int64_t to = ((sk.at + key) * a.Hk + hk) * D;
+  if (SPLIT) {
+    const int64_t size = a.ak.total * a.Hk * D;
+    float* pk = a.part + 2 * split * size + to;
+#pragma unroll
+    for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int o = 32 * ct + 8 * q + 4 * h2;
+        *reinterpret_cast<float4*>(pk + o) = make_float4(K[ct][4 * q], K[ct][4 * q + 1], K[ct][4 * q + 2], K[ct][4 * q + 3]);
+        *reinterpret_cast<float4*>(pk + size + o) = make_float4(V[ct][4 * q], V[ct][4 * q + 1], V[ct][4 * q + 2], V[ct][4 * q + 3]);
+      }
+    return;
+  }
 #pragma unroll
   for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
@@ -650,6 +674,25 @@ __global__ void __launch_bounds__(512, 2) attn_dkv_kernel(const AttnArgs a) {
                                                         a.scale * K[ct][4 * q + 2], a.scale * K[ct][4 * q + 3]);
       *reinterpret_cast<uint2*>(a.dv + to + o) = round4(V[ct][4 * q], V[ct][4 * q + 1], V[ct][4 * q + 2], V[ct][4 * q + 3]);
     }
+}
+
+// The sums of split rows, added in order: four values of dk and dv a thread.
+__global__ void __launch_bounds__(256) attn_sum_kernel(const AttnArgs a, int64_t row) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = a.ak.total * row;
+  if (at >= axis_rows(a.ak) * row) return;
+  float k[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) {
+    float x[4], y[4];
+    load_f4(a.part + 2 * s * size + at, x);
+    load_f4(a.part + (2 * s + 1) * size + at, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      k[e] += x[e];
+      v[e] += y[e];
+    }
+  }
+  *reinterpret_cast<uint2*>(a.dk + at) = round4(a.scale * k[0], a.scale * k[1], a.scale * k[2], a.scale * k[3]);
+  *reinterpret_cast<uint2*>(a.dv + at) = round4(v[0], v[1], v[2], v[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -677,6 +720,20 @@ AttnPlan attn_plan(int64_t tq, int64_t tk, int64_t Hq, int64_t Hk, int64_t D, in
   return p;
 }
 
+// Workgroups that the rows of a backward's tile of keys are split over: two
+// rounds of the card's CUs in all (a workgroup's LDS fills one), each with 8
+// pairs of row tiles at least.  A whole backward, us, unsplit and split: 1 x 1500
+// tokens of 16 heads on 2 key heads of 128, 434 and 98; 1 x 2000, 32 on 8, 337
+// and 189 (four rounds 217); 1 x 4096, 32 on 8, 765 and 570 (610); 2 x 1024, 8 on
+// 8, 79 and 73 (with 4 pairs at least 82).
+int attn_bwd_splits(int64_t tq, int64_t tk, int64_t Hq, int64_t Hk, int64_t N) {
+  const int64_t tiles = (tk + 127) / 128 * Hk, most = tq / N * (Hq / Hk) / 512;
+  int64_t s = tiles > 0 ? (kAttnRound * 2 + tiles / 2) / tiles : 1;
+  s = s < most ? s : most;
+  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+size_t attn_delta_bytes(int64_t tq, int64_t Hq) { return align256((size_t)(tq * Hq) * sizeof(float)); }
+
 kda_status_t attn_check(AttnArgs& a, const void* q, int64_t qs, int64_t qh, const void* k, int64_t ks, int64_t kh,
                         const void* v, int64_t vs, int64_t vh, float scale, const int32_t* cq, const int32_t* ck,
                         int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t N, unsigned flags) {
@@ -692,6 +749,8 @@ kda_status_t attn_check(AttnArgs& a, const void* q, int64_t qs, int64_t qh, cons
   if (!(scale > 0.0f) || !(scale - scale == 0.0f)) return KDA_ERR_INVALID;
   if ((B * Tq > 0 && !q) || (B * Tk > 0 && (!k || !v))) return KDA_ERR_INVALID;
   if (!mix_strides_ok(qs, qh) || !mix_strides_ok(ks, kh) || !mix_strides_ok(vs, vh)) return KDA_ERR_INVALID;
+  // 32-bit byte offsets within 32 rows of q
+  if (Hq / Hk * qh + 33 * qs >= (int64_t)1 << 30) return KDA_ERR_INVALID;
   if (!aligned_all(16, {q, k, v})) return KDA_ERR_INVALID;
   a = AttnArgs{};
   a.q = static_cast<const uint16_t*>(q);
@@ -707,6 +766,11 @@ kda_status_t attn_check(AttnArgs& a, const void* q, int64_t qs, int64_t qh, cons
   a.c = scale * LOG2E;
   a.splits = 1;
   return KDA_SUCCESS;
+}
+
+bool attn_sizes_ok(int64_t tq, int64_t tk, int64_t Hq, int64_t Hk, int64_t D, int64_t N) {
+  return tq >= 0 && tk >= 0 && Hq >= 1 && Hk >= 1 && Hq <= 1 << 15 && Hq % Hk == 0 && (D == 64 || D == 128) && N >= 1 &&
+         N <= 1 << 30 && fits(tq, Hq * D, kMaxElements) && fits(tk, Hk * D, kMaxElements);
 }
 
 // Workgroups that clear the rows of no sequence.
@@ -741,10 +805,17 @@ kda_status_t attn_run_bwd(AttnArgs& a, const void* out, const void* out_lo, cons
     if (s != KDA_SUCCESS) return s;
   }
   a.slots = a.ak.total / 128 + a.ak.N;
-  if (a.slots > (kMaxGrid - 64) / a.Hk) return KDA_ERR_INVALID;
-  a.main = a.slots * a.Hk;
-  const kda_status_t s = launch(&attn_dkv_kernel<D>, a.main + clear, 512, st, "attention dk, dv", a);
+  a.splits = attn_bwd_splits(a.aq.total, a.ak.total, a.Hq, a.Hk, a.ak.N);
+  if (a.slots > (kMaxGrid - 64) / a.Hk / a.splits) return KDA_ERR_INVALID;
+  a.main = a.slots * a.Hk * a.splits;
+  kda_status_t s = a.splits == 1 ? launch(&attn_dkv_kernel<D, false>, a.main + clear, 512, st, "attention dk, dv", a)
+                                 : launch(&attn_dkv_kernel<D, true>, a.main + clear, 512, st, "attention dk, dv parts", a);
   if (s != KDA_SUCCESS) return s;
+  if (a.splits > 1) {
+    const int64_t row = (int64_t)a.Hk * D;
+    s = launch(&attn_sum_kernel, (a.ak.total * row / 4 + 255) / 256, 256, st, "attention dk, dv sums", a, row);
+    if (s != KDA_SUCCESS) return s;
+  }
   a.slots = a.aq.total * a.G / 128 + a.aq.N;
   if (a.slots > (kMaxGrid - 64) / a.Hk) return KDA_ERR_INVALID;
   a.main = a.slots * a.Hk;
@@ -759,9 +830,7 @@ using namespace kda;
 extern "C" {
 
 size_t kda_attn_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N) {
-  if (Tq_total < 0 || Tk_total < 0 || Hq < 1 || Hk < 1 || Hq > 1 << 15 || Hq % Hk != 0 || (D != 64 && D != 128) ||
-      N < 1 || N > 1 << 30 || !fits(Tq_total, Hq * D, kMaxElements) || !fits(Tk_total, Hk * D, kMaxElements))
-    return 0;
+  if (!attn_sizes_ok(Tq_total, Tk_total, Hq, Hk, D, N)) return 0;
   return attn_plan(Tq_total, Tk_total, Hq, Hk, D, N).bytes;
 }
 
@@ -791,9 +860,11 @@ kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride
   return D == 128 ? attn_run_fwd<128>(a, p, clear, st) : attn_run_fwd<64>(a, p, clear, st);
 }
 
-size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Hq) {
-  if (Tq_total < 0 || Hq < 1 || Hq > 1 << 15 || !fits(Tq_total, Hq * 128, kMaxElements)) return 0;
-  return 256 + align256((size_t)(Tq_total * Hq) * sizeof(float));
+size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N) {
+  if (!attn_sizes_ok(Tq_total, Tk_total, Hq, Hk, D, N)) return 0;
+  const int splits = attn_bwd_splits(Tq_total, Tk_total, Hq, Hk, N);
+  return 256 + attn_delta_bytes(Tq_total, Hq) +
+         (splits > 1 ? align256((size_t)splits * 2 * (size_t)(Tk_total * Hk * D) * sizeof(float)) : 0);
 }
 
 kda_status_t kda_attn_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -812,7 +883,7 @@ kda_status_t kda_attn_bwd(const void* q, int64_t q_stride, int64_t q_head_stride
     for (const void* i : {q, k, v, out, out_lo, d_out})
       if (same(o, i)) return KDA_ERR_INVALID;
   if (same(dq, dk) || same(dq, dv) || same(dk, dv)) return KDA_ERR_INVALID;
-  if (!workspace || workspace_bytes < kda_attn_bwd_workspace_size(B * Tq, Hq)) return KDA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < kda_attn_bwd_workspace_size(B * Tq, B * Tk, Hq, Hk, D, N)) return KDA_ERR_WORKSPACE;
   a.lse = const_cast<float*>(lse);
   a.d_out = static_cast<const uint16_t*>(d_out);
   a.dq = static_cast<uint16_t*>(dq);
@@ -821,6 +892,7 @@ kda_status_t kda_attn_bwd(const void* q, int64_t q_stride, int64_t q_head_stride
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const int64_t clear = attn_clear(cu_seqlens_q, flags);
   float* delta = static_cast<float*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn_delta_bytes(B * Tq, Hq));
   return D == 128 ? attn_run_bwd<128>(a, out, out_lo, d_lse, delta, clear, st)
                   : attn_run_bwd<64>(a, out, out_lo, d_lse, delta, clear, st);
 }

@@ -378,7 +378,9 @@ class _Attn(torch.autograd.Function):
         q, k, v, out, out_lo, lse, cu_q, cu_k = ctx.saved_tensors
         d_lse = None if d_lse is None else _as_taken(d_lse, torch.float32)
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        ws = _scratch(kda_attn_bwd_workspace_size(q.shape[0] * q.shape[1], q.shape[2]), q)
+        B, Tq, Hq, D = q.shape
+        Tk, Hk = k.shape[1:3]
+        ws = _scratch(kda_attn_bwd_workspace_size(B * Tq, B * Tk, Hq, Hk, D, _count(q, cu_q)), q)
         kda_attn_bwd(q, k, v, ctx.scale, out, out_lo, lse, _grad(d_out, q), dq, dk, dv, ws, d_lse, cu_q, cu_k,
                      FLAG_ZERO_REST)
         return dq, dk, dv, None, None, None

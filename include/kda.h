@@ -689,9 +689,12 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
  *   scale         finite and positive
  *   flags         0 or KDA_FLAG_ZERO_REST (rows behind the last sequence: lse
  *                 becomes minus infinity there)
- * Tq and Tk are below 2^31, Hq is at most 2^15.  A NaN or infinity stays within its own sequence
- * and key head; in v it reaches queries up to 63 tokens before its own, too
- * (a tile's keys are multiplied together, with weight zero).
+ * Tq and Tk are below 2^31, Hq is at most 2^15, and the heads of a group lie
+ * within 2^30 elements: Hq / Hk q_head_stride + 33 q_stride is less.
+ * A NaN or infinity stays within its own sequence and key head; in v it reaches
+ * queries up to 63 tokens before its own, too (a tile's keys are multiplied
+ * together, with weight zero).  Keys whose scores are all minus infinity weigh
+ * nothing, as if there were none.
  */
 size_t kda_attn_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N);
 kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -706,9 +709,11 @@ kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride
  *   d_out         [B, Tq, Hq, D], contiguous;  d_lse fp32 [B, Tq, Hq] or NULL for zero
  *   dq, dk, dv    [B, Tq, Hq, D], [B, Tk, Hk, D] twice, written, contiguous;
  *                 dk and dv are sums over the query heads of a key head
- *   workspace     >= kda_attn_bwd_workspace_size(B * Tq, Hq) bytes
+ * A NaN or infinity stays within its sequence and key head; it reaches tokens of
+ * its tiles that the mask keeps from it (up to 127 before or behind), too.
+ *   workspace     >= kda_attn_bwd_workspace_size(B * Tq, B * Tk, Hq, Hk, D, N) bytes
  */
-size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Hq);
+size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N);
 kda_status_t kda_attn_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
                           int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride, float scale,
                           const void* out, const void* out_lo, const float* lse, const void* d_out, const float* d_lse, void* dq, void* dk,

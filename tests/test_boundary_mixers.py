@@ -72,6 +72,8 @@ REFUSED = [
        dict(cq=P[18]), dict(ck=P[18]), dict(B=2, N=2, cq=P[18], ck=P[18]), dict(flags=1), dict(flags=4096), dict(Tq=1 << 31),
        dict(Tk=1 << 31), dict(Hq=1 << 17), dict(B=1 << 40, N=1 << 40), dict(N=1 << 31, cq=P[18], ck=P[18]), dict(scale=0.0),
        dict(scale=-1.0), dict(scale=NAN), dict(scale=INF))],
+    # a group's heads too far apart for 32-bit offsets
+    *[(f, o, INVALID) for f in AT for o in (dict(Hq=256, qh=1 << 23), dict(Hq=254, qh=1 << 23, qs=1 << 18))],
     *[(f, o, UNSUPPORTED) for f in AT for o in (dict(D=32), dict(D=96), dict(D=256))],
     *[(f, o, WORKSPACE) for f in (la_bwd, at_bwd) for o in (dict(ws=None), dict(size=63))],
     *[(la_fwd, dict(T=4096) | o, WORKSPACE) for o in (dict(ws=None), dict(size=1 << 16))],
@@ -97,7 +99,7 @@ def test_refused(call, change, status):
 
 def test_calls_without_queries_do_nothing():
     """No query: nothing to write, so that arrays without storage will do."""
-    assert at_fwd(Tq=0, q=None, out=None, lse=None) == OK
+    assert at_fwd(Tq=0, q=None, out=None, lse=None) == OK == at_fwd(Tq=0, q=None, out=None, lse=None, Hq=254, qh=1 << 23)
 
 
 @pytest.mark.parametrize("args", [(-1, 2, 64, 64), (8, 0, 64, 64), (8, 2, 32, 64), (8, 2, 64, 65), (1 << 45, 2, 64, 64), (8, 1 << 21, 64, 64)])
@@ -108,7 +110,7 @@ def test_sizes_that_no_call_takes_need_no_workspace(args):
 @pytest.mark.parametrize("args", [(-1, 8, 2, 2, 64, 1), (8, -1, 2, 2, 64, 1), (8, 8, 0, 2, 64, 1), (8, 8, 3, 2, 64, 1), (8, 8, 2, 2, 96, 1),
                                   (8, 8, 2, 2, 64, 0), (1 << 45, 8, 2, 2, 64, 1)])
 def test_attention_sizes_that_no_call_takes(args):
-    assert kda.kda_attn_workspace_size(*args) == 0
+    assert kda.kda_attn_workspace_size(*args) == 0 == kda.kda_attn_bwd_workspace_size(*args)
 
 
 def test_workspaces_are_bounded():
@@ -120,7 +122,8 @@ def test_workspaces_are_bounded():
                 4 * (4 * H * 2 + 2048) + 256
     assert kda.kda_la_workspace_size(384, 1, 128, 128) == 0 == kda.kda_attn_workspace_size(16384, 16384, 32, 8, 128, 1)
     assert 0 < kda.kda_attn_workspace_size(64, 64 * 8192, 32, 8, 128, 64) <= 64 * 64 * 32 * 129 * 4 + 256
-    assert kda.kda_attn_bwd_workspace_size(100, 3) >= 1200
+    assert kda.kda_attn_bwd_workspace_size(100, 100, 3, 3, 64, 1) >= 1200
+    assert kda.kda_attn_bwd_workspace_size(8194, 8194, 12, 12, 128, 2) <= 512 + 4 * 8194 * 12
 
 
 def test_the_binding_refuses_tensors_that_are_not_on_the_gpu():

@@ -115,8 +115,8 @@ def bwd(c, d_lse=True, flags=0):
     q, k, v = dev(c["q"]), dev(c["k"]), dev(c["v"])
     out, lse, lo = fwd(c, keep=True)
     dq, dk, dv = (torch.full(t.shape, 7.0, dtype=BF, device=DEV) for t in (q, k, v))
-    ws = torch.full((kda.kda_attn_bwd_workspace_size(q.shape[0] * q.shape[1], q.shape[2]),), 255, dtype=torch.uint8,
-                    device=DEV)
+    ws = torch.full((kda.kda_attn_bwd_workspace_size(q.shape[0] * q.shape[1], k.shape[0] * k.shape[1], q.shape[2], k.shape[2],
+                                                    q.shape[3], c["N"]),), 255, dtype=torch.uint8, device=DEV)
     kda.kda_attn_bwd(q, k, v, c["scale"], out, lo, lse, dev(c["d_out"]), dq, dk, dv, ws, dev(c["d_lse"]) if d_lse else None,
                      dev(c["cq"]), dev(c["ck"]), flags)
     return dq, dk, dv
@@ -144,7 +144,7 @@ WHOLE = {
     "prompt": (1, 200, 2, 2), "odd_group": (2, 133, 10, 2, 64), "one_key_head": (1, 150, 7, 1), "many_tiles": (1, 700, 4, 2),
     "past": (1, 100, 4, 2, 128, 333), "past_odd": (2, 77, 6, 3, 64, 61), "token": (3, 1, 8, 2, 128, 1000),
     "token_far": (1, 1, 4, 1, 64, 5000), "tokens": (2, 5, 12, 4, 128, 1500), "big_group": (1, 3, 40, 1, 64, 700),
-    "fewer_keys": (1, 90, 2, 1, 64, -30), "fewer_keys_tiles": (2, 300, 4, 2, 128, -70), "no_keys": (1, 20, 2, 1, 64, -20),
+    "split_rows": (1, 700, 8, 1), "split_rows_two": (2, 1100, 6, 2, 64), "fewer_keys": (1, 90, 2, 1, 64, -30), "fewer_keys_tiles": (2, 300, 4, 2, 128, -70), "no_keys": (1, 20, 2, 1, 64, -20),
 }
 PACKED = {
     "ones": ([1, 1, 1], None, 0), "empties": ([0, 5, 0, 0, 64, 0], None, 3), "edges": ([63, 64, 65, 128, 1, 127, 129], None, 0),
