@@ -19,7 +19,7 @@
 // is taken (sum t (q_t.dq_t - k_t.dk_t) would be one).
 //
 // A workgroup of four waves takes one head, one slice of z's channels and a
-// segment of the packed token axis, 64 tokens a step.  Each wave owns 16 or 32
+// segment of the packed token axis, 64 tokens a step.  Each wave owns 16
 // channels c of z and keeps S[d][c] in accumulators.  That layout is the A
 // operand of out^T = S^T x^T and the result layout of S += y^T z, so the state
 // meets no LDS; y^T and z^T come from transposing LDS reads of the row-major
@@ -41,10 +41,12 @@ namespace {
 
 constexpr int LC = 64;  // tokens of a step
 constexpr int LT = 256;  // threads
-constexpr int64_t kLaWant = 512;   // workgroups at a time: two per CU
-constexpr int64_t kLaMost = 2048;  // workgroups that cutting leads to at most
-constexpr int64_t kLaMinSteps = 4; // steps of a segment at least
-constexpr int64_t kLaAround = 3, kLaLaunches = 8;
+// How sweeps are cut.  Measured, us: a prompt of 1 x 65539 tokens of 32 heads of
+// 128 (forward), and training of 2 x 4097 of 12 (all gradients).
+constexpr int64_t kLaWant = 512;    // workgroups at a time, two per CU: 1291, 304 (256: 1521, 311; 1024: 1270, 342)
+constexpr int64_t kLaMost = 1024;   // workgroups that cutting leads to at most: 1267, 303 (2048: 1291, 304)
+constexpr int64_t kLaMinSteps = 4;  // steps of a segment at least: 2 and 8 took the same time; it bounds the workspace
+constexpr int64_t kLaAround = 3;    // steps that a workgroup's beginning and end cost: 1291, 304 (0: 1297, 358)
 
 // One sweep.  State element (d, c) of sequence n and head h is at
 // (n H + h) K V + d sr + c sc.
@@ -167,9 +169,9 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
 }
 
-template <int DX, int ZW, bool OUT, bool DG>
+template <int DX, bool OUT, bool DG>
 __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const LaArgs a) {
-  constexpr int NZ = 4 * ZW, NCT = ZW / 16, NDT = DX / 16, NKB = DX / 32;
+  constexpr int NZ = 64, NDT = DX / 16, NKB = DX / 32;  // channels of a slice of z; tiles, blocks of the state's rows
   constexpr int NP = DG ? 3 : 2;  // bf16 parts of entering states
   __shared__ __align__(16) uint16_t sX[OUT ? LC * DX : 8], sY[LC * DX], sZ[LC * NZ];
   __shared__ uint4 sP[OUT ? 2 : 1][OUT ? 8 : 1][64];  // pair weights as B operands, two parts
@@ -280,9 +282,9 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
   if (t <= LC) sLam[t] = la_pow(gh, t);
   __syncthreads();
 
-  f32x4 S[NDT][NCT], Rs[DG ? NDT : 1][DG ? NCT : 1];
+  f32x4 S[NDT], Rs[DG ? NDT : 1];
   double dg = 0.0;
-  const int col = slice * NZ + w * ZW + l16;  // the lane's channel of z (+ 16 ct)
+  const int col = slice * NZ + 16 * w + l16;  // the lane's channel of z
   const int64_t segat = ((int64_t)s * a.H + h) * a.KV;
   const int64_t rat = (int64_t)a.nseg * a.H * a.KV;  // R's segments lie behind S's
   // a^{i-j} of the wave's 16 rows j: against the columns of its own tile, of the
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
   while (true) {
     const int len = left < LC ? left : LC;
     const bool last = left <= LC;
-    if (OUT && first) po = p.out + ((rev ? now.b - 1 : now.a) * a.H + h) * DZ + slice * NZ + w * ZW;
+    if (OUT && first) po = p.out + ((rev ? now.b - 1 : now.a) * a.H + h) * DZ + slice * NZ + 16 * w;
 
     // ---- the next step
     bool more = true;
@@ -334,12 +336,10 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
     if (first) {
       const float* src = now.starts ? p.sin : OUT ? p.seg : nullptr;
 #pragma unroll
-      for (int dt = 0; dt < NDT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          S[dt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if constexpr (DG) Rs[dt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+      for (int dt = 0; dt < NDT; ++dt) {
+        S[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (DG) Rs[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
       if (src) {
         const float* at = src + (now.starts ? ((int64_t)now.n * a.H + h) * a.KV : segat);
         const int sr = now.starts ? p.sr : DZ, sc = now.starts ? p.sc : 1;
@@ -347,13 +347,11 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
         for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-          for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              S[dt][ct][r] = at[o + (16 * dt + r) * sr + 16 * ct * sc];
-              if constexpr (DG && OUT)
-                if (!now.starts) Rs[dt][ct][r] = at[rat + o + (16 * dt + r) * sr + 16 * ct * sc];
-            }
+          for (int r = 0; r < 4; ++r) {
+            S[dt][r] = at[o + (16 * dt + r) * sr];
+            if constexpr (DG && OUT)
+              if (!now.starts) Rs[dt][r] = at[rat + o + (16 * dt + r) * sr];
+          }
         // Waited for here: a wait behind the branch would be one for the loads
         // issued after it, on the usual path without these.
         __builtin_amdgcn_s_waitcnt(kWaitLoads);
@@ -368,16 +366,14 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
     // ---- the entering state's part of the outputs, out^T[c][i] = S^T x^T, and
     // the pairs, rows j of this wave: (y x^T)[j][i].  Both take x's rows in the
     // channel order of the state's registers.
-    f32x4 O[OUT ? 4 : 1][NCT], On[DG && OUT ? 4 : 1][DG && OUT ? NCT : 1];
+    f32x4 O[OUT ? 4 : 1], On[DG && OUT ? 4 : 1];
     if constexpr (OUT) {
       f32x4 P[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) P[it] = f32x4{0.f, 0.f, 0.f, 0.f};
       auto clear = [&](auto& o) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int ct = 0; ct < NCT; ++ct) o[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int it = 0; it < 4; ++it) o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
       };
       // 16 rows from row0, channels 32 kb + 4 g4 and 16 behind them.  With two
       // states there are registers for one place a lane, not for one a block.
@@ -421,15 +417,14 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
       } else {
         // Rows and state parts are one block of channels ahead of the products, so
         // that the parts are cut while products run.
-        bf16x8 xf[2][4], yf[2], sp[2][NCT][NP];
+        bf16x8 xf[2][4], yf[2], sp[2][NP];
         clear(O);
         auto ready = [&](int kb) {
           rows(kb, xf[kb & 1]);
           yf[kb & 1] = frag(sY, 16 * w, kb);
         };
         auto parts = [&](int kb) {
-#pragma unroll
-          for (int ct = 0; ct < NCT; ++ct) cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp[kb & 1][ct]);
+          cut(S[2 * kb], S[2 * kb + 1], sp[kb & 1]);
         };
         ready(0);
         __builtin_amdgcn_sched_barrier(0);
@@ -445,15 +440,13 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
           for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf[b], xf[b][it], P[it]);
 #pragma unroll
-          for (int ct = 0; ct < NCT; ++ct)
+          for (int m = 0; m < NP; ++m)
 #pragma unroll
-            for (int m = 0; m < NP; ++m)
-#pragma unroll
-              for (int it = 0; it < 4; ++it) O[it][ct] = mfma_bf16(sp[b][ct][m], xf[b][it], O[it][ct]);
+            for (int it = 0; it < 4; ++it) O[it] = mfma_bf16(sp[b][m], xf[b][it], O[it]);
           // reads first, then products with the cutting between them
           if (kb + 1 < NKB) __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
 #pragma unroll
-          for (int i = 0; i < 4 + 4 * NCT * NP; ++i) {
+          for (int i = 0; i < 4 + 4 * NP; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
           }
@@ -486,44 +479,39 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
         for (int kb = 0; kb < NKB; ++kb) {
           bf16x8 xf[4];
           rows(kb, xf);
+          bf16x8 sp[NP];
+          cut(S[2 * kb], S[2 * kb + 1], sp);
 #pragma unroll
-          for (int ct = 0; ct < NCT; ++ct) {
-            bf16x8 sp[NP];
-            cut(S[2 * kb][ct], S[2 * kb + 1][ct], sp);
+          for (int m = 0; m < NP; ++m)
 #pragma unroll
-            for (int m = 0; m < NP; ++m)
+            for (int it = 0; it < 4; ++it) O[it] = mfma_bf16(sp[m], xf[it], O[it]);
+          cut(Rs[2 * kb], Rs[2 * kb + 1], sp);
 #pragma unroll
-              for (int it = 0; it < 4; ++it) O[it][ct] = mfma_bf16(sp[m], xf[it], O[it][ct]);
-            cut(Rs[2 * kb][ct], Rs[2 * kb + 1][ct], sp);
+          for (int m = 0; m < NP; ++m)
 #pragma unroll
-            for (int m = 0; m < NP; ++m)
-#pragma unroll
-              for (int it = 0; it < 4; ++it) On[it][ct] = mfma_bf16(sp[m], xf[it], On[it][ct]);
-          }
+            for (int it = 0; it < 4; ++it) On[it] = mfma_bf16(sp[m], xf[it], On[it]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       float sum = 0.0f;
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          float q[4], i1 = 0.0f;
-          if constexpr (DG) {
-            widen4(*reinterpret_cast<const uint2*>(sQ + here(at_lds<NZ>(l16, w * ZW + 4 * g4)) + 16 * it * NZ), q);
-            i1 = here((float)l16) + (float)(16 * it + 1);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (DG) sum += (On[it][ct][r] + O[it][ct][r] * i1) * lamo[it] * q[r];
-            O[it][ct][r] *= lamo[it];
-          }
+      for (int it = 0; it < 4; ++it) {
+        float q[4], i1 = 0.0f;
+        if constexpr (DG) {
+          widen4(*reinterpret_cast<const uint2*>(sQ + here(at_lds<NZ>(l16, 16 * w + 4 * g4)) + 16 * it * NZ), q);
+          i1 = here((float)l16) + (float)(16 * it + 1);
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (DG) sum += (On[it][r] + O[it][r] * i1) * lamo[it] * q[r];
+          O[it][r] *= lamo[it];
+        }
+      }
       if constexpr (DG) dg += sum;
     }
 
     // ---- the state: decayed, plus y^T (z times its decay), z's product in three bf16 parts
-    bf16x8 zr[2][NCT];
+    bf16x8 zr[2];
     {
       const float full = sLam[len];
       auto column = [&](int ks, int dt) {  // channels 16 dt .. + 15 of y, 32 rows, as the A operand
@@ -534,11 +522,8 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
         const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
         lds_f32x4(sW + 32 * ks + 4 * g4, wz);
         lds_f32x4(sW + 32 * ks + 16 + 4 * g4, wz + 4);
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          const int zc = w * ZW + 16 * ct + 4 * (l16 & 3);
-          zr[ks][ct] = join(tr_read(sZ + at_lds<NZ>(jr, zc)), tr_read(sZ + at_lds<NZ>(jr + 16, zc)));
-        }
+        const int zc = 16 * w + 4 * (l16 & 3);
+        zr[ks] = join(tr_read(sZ + at_lds<NZ>(jr, zc)), tr_read(sZ + at_lds<NZ>(jr + 16, zc)));
       };
       float wz[2][8];
       bf16x8 yt[DG ? 1 : NDT];
@@ -552,43 +537,36 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
       for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (DG) Rs[dt][ct][r] = full * (Rs[dt][ct][r] + (float)len * S[dt][ct][r]);
-            S[dt][ct][r] *= full;
-          }
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (DG) Rs[dt][r] = full * (Rs[dt][r] + (float)len * S[dt][r]);
+          S[dt][r] *= full;
+        }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if constexpr (DG) values(ks, wz[ks]);
-        bf16x8 zw[NCT][3], zn[DG ? NCT : 1][3];
+        bf16x8 zw[3], zn[3];
         const float left1 = DG ? here((float)(len - 1 - 4 * g4)) : 0.0f;
+        float f[8], fn[8];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          float f[8], fn[8];
+        for (int e = 0; e < 8; ++e) {
+          f[e] = wz[ks][e] * (float)zr[ks][e];
+          if constexpr (DG)  // behind the step's end f is zero
+            fn[e] = f[e] * (left1 - (float)(32 * ks + (e & 3) + 16 * (e >> 2)));
+        }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            f[e] = wz[ks][e] * (float)zr[ks][ct][e];
-            if constexpr (DG)  // behind the step's end f is zero
-              fn[e] = f[e] * (left1 - (float)(32 * ks + (e & 3) + 16 * (e >> 2)));
-          }
-#pragma unroll
-          for (int m = 0; m < 3; ++m) {
-            zw[ct][m] = cut8(f);
-            if constexpr (DG) zn[ct][m] = cut8(fn);
-          }
+        for (int m = 0; m < 3; ++m) {
+          zw[m] = cut8(f);
+          if constexpr (DG) zn[m] = cut8(fn);
         }
         if constexpr (DG) {
 #pragma unroll
           for (int dt = 0; dt < NDT; ++dt) {
             const bf16x8 y = column(ks, dt);
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-              for (int m = 0; m < 3; ++m) {
-                S[dt][ct] = mfma_bf16(y, zw[ct][m], S[dt][ct]);
-                Rs[dt][ct] = mfma_bf16(y, zn[ct][m], Rs[dt][ct]);
-              }
+            for (int m = 0; m < 3; ++m) {
+              S[dt] = mfma_bf16(y, zw[m], S[dt]);
+              Rs[dt] = mfma_bf16(y, zn[m], Rs[dt]);
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
         } else {
@@ -596,9 +574,7 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
           for (int m = 0; m < 3; ++m)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-              for (int dt = 0; dt < NDT; ++dt) S[dt][ct] = mfma_bf16(yt[dt], zw[ct][m], S[dt][ct]);
+            for (int dt = 0; dt < NDT; ++dt) S[dt] = mfma_bf16(yt[dt], zw[m], S[dt]);
           __builtin_amdgcn_s_setprio(0);
           if (ks == 0) {
 #pragma unroll
@@ -628,19 +604,13 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
           for (int it = 2 * ks; it < 4; ++it) {
             const int f = it < 2 ? it : 2 * it + ks - 2;
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) O[it][ct] = mfma_bf16(zr[ks][ct], pf[f][m], O[it][ct]);
+            O[it] = mfma_bf16(zr[ks], pf[f][m], O[it]);
           }
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         const int i = 16 * it + l16;
-        if (i < len) {
-#pragma unroll
-          for (int ct = 0; ct < NCT; ++ct) {
-            *reinterpret_cast<uint2*>(po + i * os + 16 * ct + 4 * g4) =
-                round4(O[it][ct][0], O[it][ct][1], O[it][ct][2], O[it][ct][3]);
-          }
-        }
+        if (i < len)
+          *reinterpret_cast<uint2*>(po + i * os + 4 * g4) = round4(O[it][0], O[it][1], O[it][2], O[it][3]);
       }
       po += LC * (int64_t)os;
     }
@@ -655,13 +625,11 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
         for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-          for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int e = o + (16 * dt + r) * sr + 16 * ct * sc;
-              dst[at + e] = S[dt][ct][r];
-              if constexpr (DG && !OUT) dst[rat + at + e] = Rs[dt][ct][r];
-            }
+          for (int r = 0; r < 4; ++r) {
+            const int e = o + (16 * dt + r) * sr;
+            dst[at + e] = S[dt][r];
+            if constexpr (DG && !OUT) dst[rat + at + e] = Rs[dt][r];
+          }
       }
       if constexpr (DG && OUT)
         if (now.ends && p.rend) {
@@ -669,9 +637,7 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
           for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) sum += Rs[dt][ct][r] * p.rend[at + o + (16 * dt + r) * sr + 16 * ct * sc];
+            for (int r = 0; r < 4; ++r) sum += Rs[dt][r] * p.rend[at + o + (16 * dt + r) * sr];
           dg += sum;
         }
     }
@@ -841,16 +807,15 @@ LaPlan la_plan(int64_t blocks, int64_t block, int64_t H, int64_t DZ, int64_t pas
   pl.slices = (int)(DZ / 64);
   const int64_t chains = blocks * H * pl.slices * passes;
   // Steps that the busiest CU does one after another, three of the first pass
-  // taken for one of the second; what a workgroup does before and after its steps
-  // is counted as kLaAround of them, the two launches more as kLaLaunches.  With the
-  // decay's gradient the second pass has one workgroup per CU, not two.
+  // taken for one of the second.  With the decay's gradient the second pass has
+  // one workgroup per CU, not two.
   const int64_t want = dg ? kLaWant / 2 : kLaWant;
   int64_t spb = 1, best = INT64_MAX;
   for (int64_t n = 1; n <= 64 && (n == 1 || chains * n <= kLaMost); ++n) {
     const int64_t len = (block + n * LC - 1) / (n * LC);
     if (n > 1 && len < kLaMinSteps) break;
     int64_t cost = 3 * ((chains * n + want - 1) / want * (len + kLaAround));
-    if (n > 1) cost += (chains * (n - 1) + kLaWant - 1) / kLaWant * (len + kLaAround) + 3 * kLaLaunches;
+    if (n > 1) cost += (chains * (n - 1) + kLaWant - 1) / kLaWant * (len + kLaAround);
     if (cost < best) {
       best = cost;
       spb = n;
@@ -897,33 +862,29 @@ kda_status_t la_check(const void* q, int64_t qs, int64_t qh, const void* k, int6
   return KDA_SUCCESS;
 }
 
-template <int DX, int ZW, bool DG>
+template <int DX, bool DG>
 kda_status_t la_launch(LaArgs& a, bool empties, hipStream_t st) {
   const int64_t groups = (a.items + 7) / 8 * 8 * a.slices * a.passes;
   const int64_t more = empties ? (a.ax.N < 1024 ? a.ax.N : 1024) : 0;
   if (groups + more > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
   a.main = groups;
   if (a.spb > 1) {  // otherwise every segment starts at a sequence's start
-    kda_status_t s = launch(&la_sweep_kernel<DX, ZW, false, DG>, groups, LT, st, "linear attention segments", a);
+    kda_status_t s = launch(&la_sweep_kernel<DX, false, DG>, groups, LT, st, "linear attention segments", a);
     if (s != KDA_SUCCESS) return s;
     s = launch(&la_join_kernel<DG>, (int64_t)a.passes * (a.nseg / a.spb) * a.H * (a.KV / (LT * 4)), LT, st,
                "linear attention join", a);
     if (s != KDA_SUCCESS) return s;
   }
-  return launch(&la_sweep_kernel<DX, ZW, true, DG>, groups + more, LT, st, "linear attention", a);
-}
-template <int DX, bool DG>
-kda_status_t la_run(LaArgs& a, const LaPlan& pl, bool empties, hipStream_t st) {
-  return la_launch<DX, 16, DG>(a, empties, st);
+  return launch(&la_sweep_kernel<DX, true, DG>, groups + more, LT, st, "linear attention", a);
 }
 template <bool DG>
-kda_status_t la_sweep(LaArgs& a, int64_t DX, const LaPlan& pl, bool empties, hipStream_t st) {
-  return DX == 128 ? la_run<128, DG>(a, pl, empties, st) : la_run<64, DG>(a, pl, empties, st);
+kda_status_t la_sweep(LaArgs& a, int64_t DX, bool empties, hipStream_t st) {
+  return DX == 128 ? la_launch<128, DG>(a, empties, st) : la_launch<64, DG>(a, empties, st);
 }
 
 // The arguments of a sweep of `passes` passes with DZ channels of z.
-LaPlan la_common(LaArgs& a, const float* g, const int32_t* cu, int64_t B, int64_t T, int64_t H, int64_t K, int64_t V,
-                 int64_t N, int64_t DZ, int passes, bool dg, unsigned flags) {
+void la_common(LaArgs& a, const float* g, const int32_t* cu, int64_t B, int64_t T, int64_t H, int64_t K, int64_t V,
+               int64_t N, int64_t DZ, int passes, bool dg, unsigned flags) {
   const LaPlan pl = la_plan(B, T, H, DZ, passes, dg);
   a = LaArgs{};
   a.ax = make_axis(cu, T, B * T, N);
@@ -938,7 +899,6 @@ LaPlan la_common(LaArgs& a, const float* g, const int32_t* cu, int64_t B, int64_
   a.passes = passes;
   a.items = pl.nseg * H;
   a.zero_rest = flags & FLAG_ZERO_REST ? 1 : 0;
-  return pl;
 }
 
 }  // namespace
@@ -967,7 +927,7 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   const size_t need = kda_la_workspace_size(B * T, H, K, V);
   if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   LaArgs a;
-  const LaPlan pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
+  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
   LaPass& p = a.p[0];
   p.x = static_cast<const uint16_t*>(q);
   p.y = static_cast<const uint16_t*>(k);
@@ -981,7 +941,7 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   p.off = 1;
   p.c1 = p.c2 = scale;
   p.c3 = 1.0f;
-  return la_sweep<false>(a, K, pl, final_state && (cu_seqlens || T == 0), reinterpret_cast<hipStream_t>(stream));
+  return la_sweep<false>(a, K, final_state && (cu_seqlens || T == 0), reinterpret_cast<hipStream_t>(stream));
 }
 
 size_t kda_la_bwd_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V, int64_t N) {
@@ -1019,7 +979,7 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
 
   // dq: of do, v, k; the state is S^T
   LaArgs a;
-  LaPlan pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, d_log_decay != nullptr, flags);
+  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, d_log_decay != nullptr, flags);
   LaPass& p = a.p[0];
   p.x = dp, p.xs = H * V, p.xh = V;
   p.y = vp, p.ys = v_stride, p.yh = v_head_stride;
@@ -1035,12 +995,12 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
     p.w = qp, p.ws = q_stride, p.wh = q_head_stride;
     p.rend = d_final;
     p.part = reinterpret_cast<float*>(ws + 4 * sb);
-    s = la_sweep<true>(a, V, pl, false, st);
+    s = la_sweep<true>(a, V, false, st);
     if (s != KDA_SUCCESS) return s;
     s = launch(&la_reduce_kernel, H, 64, st, "linear attention decay", (const float*)p.part, d_log_decay,
                (int)(a.nseg * a.slices));
   } else {
-    s = la_sweep<false>(a, V, pl, false, st);
+    s = la_sweep<false>(a, V, false, st);
   }
   if (s != KDA_SUCCESS) return s;
 
@@ -1067,18 +1027,18 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   pv.seg = reinterpret_cast<float*>(ws + 2 * sb);
   pk.seg = reinterpret_cast<float*>(ws + 3 * sb);
   if (K == V) {  // one launch: both read q and do
-    pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 2, false, flags);
+    la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 2, false, flags);
     a.p[0] = pv;
     a.p[1] = pk;
-    return la_sweep<false>(a, K, pl, d_initial_state && none, st);
+    return la_sweep<false>(a, K, d_initial_state && none, st);
   }
-  pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
+  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
   a.p[0] = pv;
-  s = la_sweep<false>(a, K, pl, d_initial_state && none, st);
+  s = la_sweep<false>(a, K, d_initial_state && none, st);
   if (s != KDA_SUCCESS) return s;
-  pl = la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, false, flags);
+  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, false, flags);
   a.p[0] = pk;
-  return la_sweep<false>(a, V, pl, false, st);
+  return la_sweep<false>(a, V, false, st);
 }
 
 kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,

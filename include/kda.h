@@ -622,8 +622,9 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
  *
  *   q, k          [B, T, H, K];  v [B, T, H, V];  K, V each 64 or 128
  *   log_decay     fp32 [H], natural logarithm per token, at most 0 (minus
- *                 infinity: nothing is kept).  Values above 0 are not refused;
- *                 the states then grow, and overflow where the formula does.
+ *                 infinity: nothing is kept).  Values above 0 are not refused:
+ *                 the states then grow.  Above 1.3 the factors of a step of 64
+ *                 tokens overflow, and gradients may be NaN.
  *   out           [B, T, H, V] written, contiguous
  *   workspace     scratch of >= kda_la_workspace_size(B * T, H, K, V) bytes;
  *                 NULL will do where that is 0 (short calls)
@@ -631,8 +632,10 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
  *   final_state   fp32 [N, H, K, V] written, or NULL; not initial_state
  *   scale         finite
  *   flags         0 or KDA_FLAG_ZERO_REST
- * T is below 2^31, H at most 2^16.  A NaN or infinity stays within its own sequence and head; it reaches tokens
- * up to 63 before its own, too (a step's tokens are multiplied together).
+ * T is below 2^31, H at most 2^16.  A NaN or infinity stays within its own
+ * sequence and head; beside the tokens that the formula takes it to it reaches
+ * the 63 around its own (a step's tokens are multiplied together), in the
+ * gradients too.
  */
 size_t kda_la_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V);
 kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -645,7 +648,7 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
  * Gradients of kda_la_fwd for loss = <d_out, out> + <d_final, final_state>.
  *   d_out         [B, T, H, V], contiguous;  d_final fp32 [N, H, K, V] or NULL for zero
  *   dq, dk, dv    [B, T, H, K], [B, T, H, K], [B, T, H, V] written, contiguous
- *   d_log_decay   fp32 [H] written, or NULL (which saves about a sixth of the time)
+ *   d_log_decay   fp32 [H] written, or NULL (which saves about 30 % of the time)
  *   d_initial_state fp32 [N, H, K, V] written, or NULL
  *   workspace     >= kda_la_bwd_workspace_size(B * T, H, K, V, N) bytes
  */
