@@ -143,9 +143,10 @@ struct LaRows {
     p += (rev ? -LC : LC) * (int64_t)(ts >> 1);
   }
   __device__ __forceinline__ void store(uint16_t* lds) const {
-    const int rt = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+    static_assert(PR % 16 == 0, "rows whose pieces are permuted alike");
+    uint16_t* to = lds + at_lds<W>(threadIdx.x / (W / 8), threadIdx.x % (W / 8) * 8);
 #pragma unroll
-    for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(lds + at_lds<W>(rt + PR * u, c)) = r[u];
+    for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(to + u * PR * W) = r[u];
   }
 };
 
@@ -247,7 +248,8 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
   rz.start((int)p.zs, rev);
   if constexpr (OUT && DG) rq.start((int)p.ws, rev);
   uint16_t* po = nullptr;  // the step's first token in the output
-  const int os = (rev ? -a.H : a.H) * DZ;
+  const int os = a.H * DZ;  // elements a token
+  const int o0 = (rev ? LC - 1 - l16 : l16) * os * 2 + 8 * g4, o1 = (rev ? -16 : 16) * os * 2;  // bytes: this lane, 16 tokens
   auto seek = [&]() {
     const int64_t row0 = rev ? c.b - 1 : c.a;
     if constexpr (OUT) rx.seek(p.x + h * p.xh, row0, rev);
@@ -375,13 +377,11 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
         for (int it = 0; it < 4; ++it) o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
       };
-      // 16 rows from row0, channels 32 kb + 4 g4 and 16 behind them.  With two
-      // states there are registers for one place a lane, not for one a block.
+      // 16 rows from row0, channels 32 kb + 4 g4 and 16 behind them
       const int at0 = at_lds<DX>(l16, 4 * g4);
       auto frag = [&](const uint16_t* tile, int row0, int kb) {
-        const int o = DG ? here(at0) : at0;
-        return join(*reinterpret_cast<const uint2*>(tile + (o ^ 32 * kb) + row0 * DX),
-                    *reinterpret_cast<const uint2*>(tile + (o ^ (32 * kb + 16)) + row0 * DX));
+        return join(*reinterpret_cast<const uint2*>(tile + (at0 ^ 32 * kb) + row0 * DX),
+                    *reinterpret_cast<const uint2*>(tile + (at0 ^ (32 * kb + 16)) + row0 * DX));
       };
       auto rows = [&](int kb, bf16x8 (&x)[4]) {
 #pragma unroll
@@ -392,74 +392,68 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
         for (int m = 0; m < NP; ++m) o[m] = cut8(f);
       };
+      // Rows and state parts are one block of channels ahead of the products, so
+      // that the parts are cut while products run.
+      bf16x8 xf[2][4], yf[2], sp[2][NP], rp[DG ? 2 : 1][NP];
+      clear(O);
+      if constexpr (DG) clear(On);
+      auto ready = [&](int kb) {
+        rows(kb, xf[kb & 1]);
+        yf[kb & 1] = frag(sY, 16 * w, kb);
+      };
+      auto parts = [&](int kb) {
+        cut(S[2 * kb], S[2 * kb + 1], sp[kb & 1]);
+        if constexpr (DG) cut(Rs[2 * kb], Rs[2 * kb + 1], rp[kb & 1]);
+      };
+      ready(0);
+      __builtin_amdgcn_sched_barrier(0);
+      parts(0);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int kb = 0; kb < NKB; ++kb) {
+        const int b = kb & 1;
+        if (kb + 1 < NKB) {
+          ready(kb + 1);
+          parts(kb + 1);
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf[b], xf[b][it], P[it]);
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            O[it] = mfma_bf16(sp[b][m], xf[b][it], O[it]);
+            if constexpr (DG) On[it] = mfma_bf16(rp[b][m], xf[b][it], On[it]);
+          }
+        // reads first, then products with the cutting between them
+        if (kb + 1 < NKB) __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
+#pragma unroll
+        for (int i = 0; i < 4 + (DG ? 8 : 4) * NP; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
       f32x4 A[DG ? 4 : 1];  // (z q^T)[j][i] over this slice's channels
       if constexpr (DG) {
-        // Two states leave no registers for reading ahead, if two waves are to
-        // share a SIMD: the pairs first, the states' part after them.
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-          bf16x8 xf[4];
-          rows(kb, xf);
-          const bf16x8 yf = frag(sY, 16 * w, kb);
-#pragma unroll
-          for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf, xf[it], P[it]);
-        }
 #pragma unroll
         for (int it = 0; it < 4; ++it) A[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < NZ / 32; ++kb) {
-          const int o = here(at_lds<NZ>(l16, 8 * g4)) ^ 32 * kb;
+          const int o = at_lds<NZ>(l16, 8 * g4) ^ 32 * kb;
           const bf16x8 zf = *reinterpret_cast<const bf16x8*>(sZ + o + 16 * w * NZ);
 #pragma unroll
           for (int it = 0; it < 4; ++it)
             A[it] = mfma_bf16(zf, *reinterpret_cast<const bf16x8*>(sQ + o + 16 * it * NZ), A[it]);
         }
-      } else {
-        // Rows and state parts are one block of channels ahead of the products, so
-        // that the parts are cut while products run.
-        bf16x8 xf[2][4], yf[2], sp[2][NP];
-        clear(O);
-        auto ready = [&](int kb) {
-          rows(kb, xf[kb & 1]);
-          yf[kb & 1] = frag(sY, 16 * w, kb);
-        };
-        auto parts = [&](int kb) {
-          cut(S[2 * kb], S[2 * kb + 1], sp[kb & 1]);
-        };
-        ready(0);
-        __builtin_amdgcn_sched_barrier(0);
-        parts(0);
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-          const int b = kb & 1;
-          if (kb + 1 < NKB) {
-            ready(kb + 1);
-            parts(kb + 1);
-          }
-#pragma unroll
-          for (int it = 0; it < 4; ++it) P[it] = mfma_bf16(yf[b], xf[b][it], P[it]);
-#pragma unroll
-          for (int m = 0; m < NP; ++m)
-#pragma unroll
-            for (int it = 0; it < 4; ++it) O[it] = mfma_bf16(sp[b][m], xf[b][it], O[it]);
-          // reads first, then products with the cutting between them
-          if (kb + 1 < NKB) __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
-#pragma unroll
-          for (int i = 0; i < 4 + 4 * NP; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_s_setprio(0);
       }
       float pairs = 0.0f;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         if (it < (w & 2)) continue;  // nothing reads those
         float v[4];
-        const float n0 = here((float)(l16 - 4 * g4 - 16 * w));
+        const float n0 = (float)(l16 - 4 * g4 - 16 * w);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float n = n0 + (float)(16 * it - r);  // i - j
@@ -470,36 +464,14 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
         for (int m = 0; m < 2; ++m)
           reinterpret_cast<uint2*>(&sP[m][2 * it + (w >> 1)][lane])[w & 1] = cut_part(v);
       }
-      if constexpr (DG) {
-        dg += pairs;
-        __builtin_amdgcn_sched_barrier(0);
-        clear(O);
-        clear(On);
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-          bf16x8 xf[4];
-          rows(kb, xf);
-          bf16x8 sp[NP];
-          cut(S[2 * kb], S[2 * kb + 1], sp);
-#pragma unroll
-          for (int m = 0; m < NP; ++m)
-#pragma unroll
-            for (int it = 0; it < 4; ++it) O[it] = mfma_bf16(sp[m], xf[it], O[it]);
-          cut(Rs[2 * kb], Rs[2 * kb + 1], sp);
-#pragma unroll
-          for (int m = 0; m < NP; ++m)
-#pragma unroll
-            for (int it = 0; it < 4; ++it) On[it] = mfma_bf16(sp[m], xf[it], On[it]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+      if constexpr (DG) dg += pairs;
       float sum = 0.0f;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         float q[4], i1 = 0.0f;
         if constexpr (DG) {
-          widen4(*reinterpret_cast<const uint2*>(sQ + here(at_lds<NZ>(l16, 16 * w + 4 * g4)) + 16 * it * NZ), q);
-          i1 = here((float)l16) + (float)(16 * it + 1);
+          widen4(*reinterpret_cast<const uint2*>(sQ + at_lds<NZ>(l16, 16 * w + 4 * g4) + 16 * it * NZ), q);
+          i1 = (float)l16 + (float)(16 * it + 1);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -515,25 +487,22 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
     {
       const float full = sLam[len];
       auto column = [&](int ks, int dt) {  // channels 16 dt .. + 15 of y, 32 rows, as the A operand
-        const int at1 = at_lds<DX>(4 * g4 + (l16 >> 2), 4 * (l16 & 3)), o = (DG ? here(at1) : at1) ^ 16 * dt;
-        return join(tr_read(sY + o + 32 * ks * DX), tr_read(sY + o + (32 * ks + 16) * DX));
+        const int at1 = at_lds<DX>(4 * g4 + (l16 >> 2), 4 * (l16 & 3)) ^ 16 * dt;
+        return join(tr_read(sY + at1 + 32 * ks * DX), tr_read(sY + at1 + (32 * ks + 16) * DX));
       };
       auto values = [&](int ks, float (&wz)[8]) {  // z's rows, and their decays
-        const int jr = 32 * ks + 4 * g4 + (l16 >> 2);
         lds_f32x4(sW + 32 * ks + 4 * g4, wz);
         lds_f32x4(sW + 32 * ks + 16 + 4 * g4, wz + 4);
-        const int zc = 16 * w + 4 * (l16 & 3);
-        zr[ks] = join(tr_read(sZ + at_lds<NZ>(jr, zc)), tr_read(sZ + at_lds<NZ>(jr + 16, zc)));
+        const uint16_t* at1 = sZ + at_lds<NZ>(4 * g4 + (l16 >> 2), 16 * w + 4 * (l16 & 3)) + 32 * ks * NZ;
+        zr[ks] = join(tr_read(at1), tr_read(at1 + 16 * NZ));
       };
       float wz[2][8];
-      bf16x8 yt[DG ? 1 : NDT];
-      if constexpr (!DG) {
-        values(0, wz[0]);
-        values(1, wz[1]);
+      bf16x8 yt[NDT];
+      values(0, wz[0]);
+      values(1, wz[1]);
 #pragma unroll
-        for (int dt = 0; dt < NDT; ++dt) yt[dt] = column(0, dt);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      for (int dt = 0; dt < NDT; ++dt) yt[dt] = column(0, dt);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
@@ -543,9 +512,8 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
         }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        if constexpr (DG) values(ks, wz[ks]);
         bf16x8 zw[3], zn[3];
-        const float left1 = DG ? here((float)(len - 1 - 4 * g4)) : 0.0f;
+        const float left1 = DG ? (float)(len - 1 - 4 * g4) : 0.0f;
         float f[8], fn[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -558,29 +526,19 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
           zw[m] = cut8(f);
           if constexpr (DG) zn[m] = cut8(fn);
         }
-        if constexpr (DG) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
 #pragma unroll
           for (int dt = 0; dt < NDT; ++dt) {
-            const bf16x8 y = column(ks, dt);
-#pragma unroll
-            for (int m = 0; m < 3; ++m) {
-              S[dt] = mfma_bf16(y, zw[m], S[dt]);
-              Rs[dt] = mfma_bf16(y, zn[m], Rs[dt]);
-            }
+            S[dt] = mfma_bf16(yt[dt], zw[m], S[dt]);
+            if constexpr (DG) Rs[dt] = mfma_bf16(yt[dt], zn[m], Rs[dt]);
           }
+        __builtin_amdgcn_s_setprio(0);
+        if (ks == 0) {
+#pragma unroll
+          for (int dt = 0; dt < NDT; ++dt) yt[dt] = column(1, dt);
           __builtin_amdgcn_sched_barrier(0);
-        } else {
-          __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-          for (int m = 0; m < 3; ++m)
-#pragma unroll
-            for (int dt = 0; dt < NDT; ++dt) S[dt] = mfma_bf16(yt[dt], zw[m], S[dt]);
-          __builtin_amdgcn_s_setprio(0);
-          if (ks == 0) {
-#pragma unroll
-            for (int dt = 0; dt < NDT; ++dt) yt[dt] = column(1, dt);
-            __builtin_amdgcn_sched_barrier(0);
-          }
         }
       }
     }
@@ -606,13 +564,15 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
             const int f = it < 2 ? it : 2 * it + ks - 2;
             O[it] = mfma_bf16(zr[ks], pf[f][m], O[it]);
           }
+      const __amdgpu_buffer_rsrc_t d = buf(po - (rev ? (LC - 1) * (int64_t)os : 0), 0x7fffffffu);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const int i = 16 * it + l16;
-        if (i < len)
-          *reinterpret_cast<uint2*>(po + i * os + 4 * g4) = round4(O[it][0], O[it][1], O[it][2], O[it][3]);
+        const uint2 o = round4(O[it][0], O[it][1], O[it][2], O[it][3]);
+        // behind the step's end: an offset behind the descriptor's
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), d, 16 * it + l16 < len ? o0 + it * o1 : (int)0x80000000,
+                                              0, 0);
       }
-      po += LC * (int64_t)os;
+      po += (rev ? -LC : LC) * (int64_t)os;
     }
 
     // ---- the state that leaves a stretch
