@@ -42,7 +42,6 @@ namespace {
 
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int64_t kAttnRound = 256;  // CUs
-constexpr int64_t kAttnWant = 1024;  // workgroups that a call with few rows is split into
 
 struct AttnArgs {
   const uint16_t *q, *k, *v;
@@ -324,28 +323,58 @@ __global__ void __launch_bounds__(64 * NW, 2) attn_fwd_kernel(const AttnArgs a) 
   if (h2 == 0) a.lse[head] = lse;
 }
 
-// The parts of split keys, joined: one row and head a D / 4 lanes.
-template <int D>
+// The parts of split keys, joined: a row and head has D / 4 lanes for each of GRP
+// groups of splits, four of which are asked for at a time: one after another, 64
+// parts took 0.6 us each.  What a group has seen is again sums and a maximum, so
+// groups are joined as splits are.
+template <int D, int GRP>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
-  constexpr int LR = D / 4;
+  constexpr int LR = D / 4, ROWS = 256 / (LR * GRP), U = 4;
+  __shared__ float sO[GRP > 1 ? 256 : 1][4], sM[GRP > 1 ? 256 : 1], sS[GRP > 1 ? 256 : 1];
   const int64_t total = a.aq.total * a.Hq, live = axis_rows(a.aq) * a.Hq;
-  const int64_t head = (int64_t)blockIdx.x * (256 / LR) + threadIdx.x / LR;
-  if (head >= live) return;
-  const int c4 = threadIdx.x % LR * 4;
-  const float* lp = a.part + a.splits * total * D + head;
-  float m = -__builtin_inff();
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, lp[s * total]);
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float l = lp[s * total];
-    if (l == -__builtin_inff()) continue;
-    const float f = fexp2((l - m) * LOG2E);
-    float v[4];
-    load_f4(a.part + (s * total + head) * D + c4, v);
-    sum += f;
+  const int lane = threadIdx.x % LR, grp = threadIdx.x / LR % GRP, c4 = lane * 4;
+  const int64_t head = (int64_t)blockIdx.x * ROWS + threadIdx.x / (LR * GRP), hc = head < live ? head : live - 1;
+  if (live == 0) return;
+  const float *po = a.part + hc * D + c4, *pl = a.part + a.splits * total * D + hc;
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.0f, m = -__builtin_inff();
+  // takes in sums w, v of weights exp(lse - l)
+  auto take = [&](float l, float w, const float (&v)[4]) {
+    const float mn = fmaxf(m, l), ms = mn == -__builtin_inff() ? 0.0f : mn;  // no key yet: all weights are 0
+    const float f = fexp2((m - ms) * LOG2E), g = fexp2((l - ms) * LOG2E);
+    m = mn;
+    sum = f * sum + g * w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += f * v[e];
+    for (int e = 0; e < 4; ++e) o[e] = f * o[e] + g * v[e];
+  };
+  for (int s0 = grp; s0 < a.splits; s0 += GRP * U) {
+    float l[U], v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t s = s0 + u * GRP < a.splits ? s0 + u * GRP : s0;
+      load_f4(po + s * total * D, v[u]);
+      l[u] = pl[s * total];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s0 + u * GRP < a.splits) take(l[u], 1.0f, v[u]);
   }
+  if constexpr (GRP > 1) {
+    const int at = threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sO[at][e] = o[e];
+    sM[at] = m;
+    sS[at] = sum;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int i = 1; i < GRP; ++i) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = sO[at + i * LR][e];
+      take(sM[at + i * LR], sS[at + i * LR], v);
+    }
+  }
+  if (head >= live) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] *= inv;
@@ -698,7 +727,20 @@ __global__ void __launch_bounds__(256) attn_sum_kernel(const AttnArgs a, int64_t
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-// How a forward is cut: rows of a tile (32 or 128), parts of the keys.
+// How a forward is cut: rows of a tile (32, a wave, or 128, four waves), and parts
+// of the keys.  Measured, us, on 8 key heads of 128 with 4 query heads each, both
+// sides of each rule:
+// - Rows of a tile.  One wave where it has all rows of a sequence, or where keys
+//   are few: 64 sequences of 24 tokens by themselves, 12.6 (128 rows: 16.4).  More
+//   rows on long keys share what they read: 16 sequences, 14 tokens behind 4096,
+//   55 (32 rows: 87).
+// - Parts.  One round of 128-row workgroups, two on a CU (16 sequences, 18 tokens
+//   behind 4096: 59, two rounds 75), or of single waves, eight on a CU (64 tokens
+//   behind 8191 each: 370, half of that 412), as long as the parts' own traffic is a
+//   sixteenth of the keys' or most CUs would be idle without (16 sequences, 8 tokens
+//   behind 4096: 57, without this limit 73).  At most 64 (1 token behind 65535: 45,
+//   with 256 parts 53), of 128 or 256 keys at least (1 token of 8 heads on one key
+//   head behind 8191: 12.7, with 256 16.3; 24 tokens behind 8000: 20.2, with 128 22.4).
 struct AttnPlan {
   int bm;
   int64_t slots;
@@ -708,13 +750,19 @@ struct AttnPlan {
 AttnPlan attn_plan(int64_t tq, int64_t tk, int64_t Hq, int64_t Hk, int64_t D, int64_t N) {
   AttnPlan p;
   const int64_t rows = tq * (Hq / Hk);
-  p.bm = rows <= 64 * N ? 32 : 128;
+  const int64_t keys = tk / N;
+  p.bm = rows <= 32 * N || (rows <= 128 * N && keys <= 256) ? 32 : 128;
   p.slots = rows / p.bm + N;
-  // tiles that hold rows, as far as the host knows, and keys of a sequence
+  // tiles that hold rows, as far as the host knows
   const int64_t tiles = ((rows + p.bm - 1) / p.bm > N ? (rows + p.bm - 1) / p.bm : (rows < N ? rows : N)) * Hk;
-  const int64_t most = (tk / N + 255) / 256;
-  int64_t s = tiles > 0 ? kAttnWant / tiles : 1;
-  s = s < most ? s : most;
+  int64_t s = 1;
+  if (tiles > 0) {
+    s = p.bm == 128 ? 2 * kAttnRound / tiles : 8 * kAttnRound / tiles;
+    const int64_t least = p.bm == 128 ? 256 : 128, most = (keys + least - 1) / least;
+    const int64_t few = kAttnRound / tiles, light = keys * N / (32 * rows);
+    if (p.bm == 32 && s > few && s > light) s = few > light ? few : light;
+    s = s < most ? s : most;
+  }
   p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   p.bytes = p.splits > 1 ? align256((size_t)p.splits * (size_t)(tq * Hq) * (size_t)(D + 1) * sizeof(float)) : 0;
   return p;
@@ -790,8 +838,9 @@ kda_status_t attn_run_fwd(AttnArgs& a, const AttnPlan& p, int64_t clear, hipStre
   const kda_status_t s = p.bm == 32 ? launch(&attn_fwd_kernel<D, 1, 32, true>, a.main + clear, 64, st, "attention parts", a)
                                     : launch(&attn_fwd_kernel<D, 4, 64, true>, a.main + clear, 256, st, "attention parts", a);
   if (s != KDA_SUCCESS) return s;
-  const int64_t per = 256 / (D / 4);
-  return launch(&attn_join_kernel<D>, (a.aq.total * a.Hq + per - 1) / per, 256, st, "attention join", a);
+  const int64_t heads = a.aq.total * a.Hq, per = 256 / (D / 4);
+  return p.splits <= 8 ? launch(&attn_join_kernel<D, 1>, (heads + per - 1) / per, 256, st, "attention join", a)
+                       : launch(&attn_join_kernel<D, 8>, (heads + per / 8 - 1) / (per / 8), 256, st, "attention join", a);
 }
 
 template <int D>
