@@ -8,7 +8,9 @@ kernels behind the C ABI of include/kda.h.  The names mirror that header:
 ``kda_workspace_faults`` (with the ``FAULT_*`` bits), ``kda_fwd_noalloc`` and the operators around
 the core: the gated linear recurrence (``kda_glr_fwd``, ``kda_glr_bwd``, ``kda_glr_step``), the short
 causal convolution (``kda_conv_fwd``, ``kda_conv_bwd``, ``kda_conv_step``) and the norm and rotation
-of queries and keys (``kda_qk_rope_fwd``, ``kda_qk_rope_bwd``).  PyTorch provides
+of queries and keys (``kda_qk_rope_fwd``, ``kda_qk_rope_bwd``), and the token mixers beside the
+core: linear attention with a decay for each head (``kda_la_fwd``, ``kda_la_bwd``, ``kda_la_step``) and
+causal softmax attention (``kda_attn_fwd``, ``kda_attn_bwd``).  PyTorch provides
 device memory and the current stream; there is no CPU or PyTorch fallback, and
 importing this module fails if the library has not been built.
 """

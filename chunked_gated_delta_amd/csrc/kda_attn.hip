@@ -180,6 +180,15 @@ __device__ __forceinline__ void clear_rows(uint16_t* out, const Axis& ax, int64_
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+// Tiles of 128 rows, 64 keys and two buffers (64 KB of LDS for D = 128, two
+// workgroups on a CU), or of one wave's 32 rows and 32 keys in one buffer, eight
+// on a CU.  A prompt of 16384 tokens, 32 heads on 8 of 128: 2194 us, 1000 TFLOP/s,
+// where a library product of 16384^3 reaches 1395.  The matrix cores are
+// busy 51 % of the cycles, the exponentials and sums take about as many issue slots
+// as they do, and LDS reads (32 KB a wave and tile) as much time; the clock falls
+// as they overlap better (11 % fewer cycles by reading ahead saved 4.5 % of the
+// time).  Three waves a SIMD where D = 64 has registers for them (168): 89 us in
+// place of 95 on packed prompts of 100 to 4000 tokens.
 template <int D, int NW, int KT, bool SPLIT>
 __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : 2) attn_fwd_kernel(const AttnArgs a) {
   constexpr int NT = 64 * NW, BM = 32 * NW, ND = D / 16, NC = D / 32, NJ = KT / 32;
@@ -425,7 +434,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// d = do.o - dl for every row and head.
+// d = do.o - dl for every row and head: three arrays read once (30 us for 8219 tokens
+// of 32 heads of 128, 6.7 TB/s).
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const uint16_t* out, const uint16_t* out_lo,
                                                          const uint16_t* d_out, const float* d_lse, float* delta,
@@ -445,6 +455,11 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const uint16_t* out, co
   if (threadIdx.x % LR == 0) delta[head] = s - (d_lse ? d_lse[head] : 0.0f);
 }
 
+// dq: a tile of 128 rows, 32 a wave, which walks the keys 32 at a time.  q and do
+// stay in registers as operands, P and dS never leave them.  166 us for 2 x 4097
+// tokens of 12 heads of 128 (three products: 930 TFLOP/s; matrix cores busy 53 % of
+// the cycles).  With one wave a SIMD and a tile ahead it took 235 us, and reading
+// operands ahead as the forward does made no difference.
 template <int D>
 __global__ void __launch_bounds__(256, 2) attn_dq_kernel(const AttnArgs a) {
   constexpr int NT = 256, BM = 128, KT = 32, ND = D / 16, NC = D / 32;

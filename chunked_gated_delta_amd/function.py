@@ -2,7 +2,9 @@
 
 ``kda_chunk`` is the chunked forward; ``kda_glr`` the gated linear recurrence,
 ``kda_short_conv`` the short causal convolution and ``kda_qk_norm_rope`` the
-norm and rotation of queries and keys.  Each allocates its outputs and
+norm and rotation of queries and keys; ``kda_linear_attn`` is linear attention
+with a decay for each head and ``kda_attn`` causal softmax attention, the mixers
+that stand beside it in a stack.  Each allocates its outputs and
 workspaces with PyTorch and calls the library's entry points for both
 directions; without a gradient to compute they are the inference calls too.
 
