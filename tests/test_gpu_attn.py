@@ -150,6 +150,7 @@ PACKED = {
     "ones": ([1, 1, 1], None, 0), "empties": ([0, 5, 0, 0, 64, 0], None, 3), "edges": ([63, 64, 65, 128, 1, 127, 129], None, 0),
     "all_empty": ([0, 0], None, 5), "pasts": ([3, 0, 40, 70, 1], [100, 7, 0, 33, 1], 40), "no_past_keys": ([30, 20], [-30, 4], 2),
     "fewer": ([130, 20, 9], [-70, -1, 2], 0), "long_among": ([1, 600, 2], [900, 0, 0], 9), "tokens": ([1] * 9, [1000, 0, 3, 700, 64, 63, 1, 2, 900], 0),
+    "sixty_four": ([37 * i % 190 for i in range(64)], None, 7), "sixty_five": ([53 * i % 170 for i in range(65)], None, 0),
 }
 
 
