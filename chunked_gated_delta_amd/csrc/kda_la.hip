@@ -175,6 +175,7 @@ __device__ __forceinline__ X here(X x) {
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float uniform(float x) { return __int_as_float(uniform(__float_as_int(x))); }
 __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
 }
@@ -304,16 +305,18 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
   const int col = slice * NZ + 16 * w + l16;  // the lane's channel of z
   const int64_t segat = ((int64_t)s * a.H + h) * a.KV;
   const int64_t rat = (int64_t)a.nseg * a.H * a.KV;  // R's segments lie behind S's
-  // a^{i-j} of the wave's 16 rows j: against the columns of its own tile, of the
-  // next one, and what is more for a tile further away; a^{i + off}
-  float dec0[4], dec1[4], far[4], lamo[4];
+  // a^{i-j} of the wave's 16 rows j: against the columns of its own tile (zero for
+  // i < j), of the next one, and what is more for a tile further away (own: whether
+  // it is its own); a^{i + off}
+  float dec0[4], dec1[4], own[4], far[4], lamo[4];
   if constexpr (OUT) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int n = l16 - 4 * g4 - r;
-      dec0[r] = sLam[n >= 0 ? n : 0] * p.c1;
+      dec0[r] = n >= 0 ? sLam[n] * p.c1 : 0.0f;
       dec1[r] = sLam[16 + n] * p.c1;
-      far[r] = sLam[r - w > 1 ? 16 * (r - w - 1) : 0];
+      own[r] = r == w ? 1.0f : 0.0f;
+      far[r] = r > w ? uniform(sLam[16 * (r - w - 1)]) : 0.0f;
       lamo[r] = sLam[16 * r + l16 + p.off] * p.c2;
     }
   }
@@ -472,8 +475,8 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float n = n0 + (float)(16 * it - r);  // i - j
-          v[r] = n >= 0.0f ? P[it][r] * (it == w ? dec0[r] : dec1[r] * far[it]) : 0.0f;
-          if constexpr (DG) pairs += n > 0.0f ? n * v[r] * A[it][r] : 0.0f;
+          v[r] = P[it][r] * __builtin_fmaf(dec0[r], own[it], dec1[r] * far[it]);
+          if constexpr (DG) pairs += n * v[r] * A[it][r];
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
