@@ -37,8 +37,9 @@
 // What bounds it.  The chain of steps: 2 x 4096 tokens are 64 steps one after
 // another whatever the card's width, and a step of two waves a SIMD (242 registers,
 // 58 KB of LDS) has two barriers.  A prompt of 32768 tokens of 96 heads of 128 takes
-// 0.95 ms in the second pass (3.2 GB: 3.4 TB/s; matrix cores busy 36 % of the
-// cycles, an eighth of them lost to LDS banks), 0.28 ms in the pass before it
+// 0.92 ms in the second pass (3.2 GB: 3.5 TB/s; matrix cores busy 36 % of the
+// cycles, with five other vector instructions for each of theirs, and an eighth of
+// the cycles lost to LDS banks), 0.28 ms in the pass before it
 // that makes the segments' states, 0.01 ms in their join.  What cutting costs
 // is that pass: unsplit there were 192 workgroups for 512 places.
 
@@ -180,12 +181,11 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
 }
 
-// With the decay's gradient the second state leaves one wave a SIMD (390 registers):
-// 1.61 ms over 69141 packed tokens of 32 heads where the plain sweep takes 0.64.
+// With the decay's gradient the second state leaves one wave a SIMD (370 registers):
+// 1.51 ms over 69141 packed tokens of 32 heads where the plain sweep takes 0.60.
 // Instead of it, the states that enter all steps can be left in memory for the dk
 // sweep, which then sums a^C <S_in, dS_out>; with two waves a SIMD, the 2.2 GB
-// written and read made both sweeps slower than the second state does (1.30 and
-// 1.26 ms).
+// written and read made it 1.30 ms, and the dk sweep 1.26 in place of 0.67.
 template <int DX, bool OUT, bool DG>
 __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const LaArgs a) {
   constexpr int NZ = 64, NDT = DX / 16, NKB = DX / 32;  // channels of a slice of z; tiles, blocks of the state's rows
