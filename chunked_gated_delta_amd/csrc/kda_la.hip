@@ -51,8 +51,8 @@ namespace {
 
 constexpr int LC = 64;  // tokens of a step
 constexpr int LT = 256;  // threads
-// How sweeps are cut.  Measured, us: a prompt of 1 x 65539 tokens of 32 heads of
-// 128 (forward), and training of 2 x 4097 of 12 (all gradients).
+// How sweeps are cut.  Measured, us: a prompt of 32768 tokens of 96 heads of 128
+// (forward), and training on 2 x 4096 of 12 (all gradients).
 constexpr int64_t kLaWant = 512;    // workgroups at a time, two per CU: 1291, 304 (256: 1521, 311; 1024: 1270, 342)
 constexpr int64_t kLaMost = 1024;   // workgroups that cutting leads to at most: 1267, 303 (2048: 1291, 304)
 constexpr int64_t kLaMinSteps = 4;  // steps of a segment at least: 2 and 8 took the same time; it bounds the workspace
