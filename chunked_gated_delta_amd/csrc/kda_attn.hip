@@ -926,13 +926,18 @@ bool attn_sizes_ok(int64_t tq, int64_t tk, int64_t Hq, int64_t Hk, int64_t D, in
 // Workgroups that clear the rows of no sequence.
 int64_t attn_clear(const int32_t* cu, unsigned flags) { return cu && (flags & FLAG_ZERO_REST) ? 64 : 0; }
 
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+// Whether tiles times heads times splits workgroups of `threads`, and those that
+// clear, are a grid.
+bool attn_fits(int64_t tiles, int64_t heads, int64_t splits, int64_t clear, int threads) {
+  return tiles <= (most_groups(threads) - clear) / heads / splits;
+}
 
 template <int D>
 kda_status_t attn_run_fwd(AttnArgs& a, const AttnPlan& p, int64_t clear, hipStream_t st) {
   a.slots = p.slots;
   a.splits = p.splits;
-  if (p.slots > kMaxGrid / a.Hk / p.splits - 64) return KDA_ERR_INVALID;
+  // (keys are split for few rows only: the join's grid is small)
+  if (!attn_fits(p.slots, a.Hk, p.splits, clear, p.bm == 32 ? 64 : 256)) return KDA_ERR_INVALID;
   a.main = p.slots * a.Hk * p.splits;
   if (p.splits == 1)
     return p.bm == 32 ? launch(&attn_fwd_kernel<D, 1, 32, false>, a.main + clear, 64, st, "attention", a)
@@ -949,15 +954,20 @@ template <int D>
 kda_status_t attn_run_bwd(AttnArgs& a, const void* out, const void* out_lo, const float* d_lse, float* delta, int64_t clear, hipStream_t st) {
   const int64_t heads = a.aq.total * a.Hq, per = 256 / (D / 8);
   a.delta = delta;
+  a.slots = a.ak.total / 128 + a.ak.N;
+  a.splits = attn_bwd_splits(a.aq.total, a.ak.total, a.Hq, a.Hk, a.ak.N);
+  const int64_t rows = a.aq.total * a.G / 128 + a.aq.N;  // tiles of rows
+  // Nothing is enqueued unless all of it can be (rows are split for few tiles of keys
+  // only: the sums' grid is small).
+  if ((heads + per - 1) / per > most_groups(256) || !attn_fits(a.slots, a.Hk, a.splits, clear, 512) ||
+      !attn_fits(rows, a.Hk, 1, clear, 256))
+    return KDA_ERR_INVALID;
   if (heads > 0) {
     const kda_status_t s = launch(&attn_delta_kernel<D>, (heads + per - 1) / per, 256, st, "attention delta",
                                   static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(out_lo), a.d_out, d_lse,
                                   delta, heads);
     if (s != KDA_SUCCESS) return s;
   }
-  a.slots = a.ak.total / 128 + a.ak.N;
-  a.splits = attn_bwd_splits(a.aq.total, a.ak.total, a.Hq, a.Hk, a.ak.N);
-  if (a.slots > (kMaxGrid - 64) / a.Hk / a.splits) return KDA_ERR_INVALID;
   a.main = a.slots * a.Hk * a.splits;
   kda_status_t s = a.splits == 1 ? launch(&attn_dkv_kernel<D, false>, a.main + clear, 512, st, "attention dk, dv", a)
                                  : launch(&attn_dkv_kernel<D, true>, a.main + clear, 512, st, "attention dk, dv parts", a);
@@ -967,8 +977,7 @@ kda_status_t attn_run_bwd(AttnArgs& a, const void* out, const void* out_lo, cons
     s = launch(&attn_sum_kernel, (a.ak.total * row / 4 + 255) / 256, 256, st, "attention dk, dv sums", a, row);
     if (s != KDA_SUCCESS) return s;
   }
-  a.slots = a.aq.total * a.G / 128 + a.aq.N;
-  if (a.slots > (kMaxGrid - 64) / a.Hk) return KDA_ERR_INVALID;
+  a.slots = rows;
   a.main = a.slots * a.Hk;
   return launch(&attn_dq_kernel<D>, a.main + clear, 256, st, "attention dq", a);
 }

@@ -842,11 +842,16 @@ kda_status_t la_check(const void* q, int64_t qs, int64_t qh, const void* k, int6
   return KDA_SUCCESS;
 }
 
+// Workgroups of a sweep's passes, and those for sequences without tokens.
+int64_t la_groups(const LaArgs& a) { return (a.items + 7) / 8 * 8 * a.slices * a.passes; }
+int64_t la_more(const LaArgs& a, bool empties) { return !empties ? 0 : a.ax.N < 1024 ? a.ax.N : 1024; }
+// Whether every launch of a sweep has a grid (a join has workgroups only where the
+// axis is cut, and few heads then).
+bool la_fits(const LaArgs& a, bool empties) { return la_groups(a) + la_more(a, empties) <= most_groups(LT); }
+
 template <int DX, bool DG>
 kda_status_t la_launch(LaArgs& a, bool empties, hipStream_t st) {
-  const int64_t groups = (a.items + 7) / 8 * 8 * a.slices * a.passes;
-  const int64_t more = empties ? (a.ax.N < 1024 ? a.ax.N : 1024) : 0;
-  if (groups + more > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
+  const int64_t groups = la_groups(a), more = la_more(a, empties);
   a.main = groups;
   if (a.spb > 1) {  // otherwise every segment starts at a sequence's start
     kda_status_t s = launch(&la_sweep_kernel<DX, false, DG>, groups, LT, st, "linear attention segments", a);
@@ -921,7 +926,8 @@ kda_status_t kda_la_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   p.off = 1;
   p.c1 = p.c2 = scale;
   p.c3 = 1.0f;
-  return la_sweep<false>(a, K, final_state && (cu_seqlens || T == 0), reinterpret_cast<hipStream_t>(stream));
+  const bool empties = final_state && (cu_seqlens || T == 0);
+  return la_fits(a, empties) ? la_sweep<false>(a, K, empties, reinterpret_cast<hipStream_t>(stream)) : KDA_ERR_INVALID;
 }
 
 size_t kda_la_bwd_workspace_size(int64_t T_total, int64_t H, int64_t K, int64_t V, int64_t N) {
@@ -958,9 +964,9 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   const bool none = cu_seqlens || T == 0;  // there may be sequences without tokens
 
   // dq: of do, v, k; the state is S^T
-  LaArgs a;
-  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, d_log_decay != nullptr, flags);
-  LaPass& p = a.p[0];
+  LaArgs aq, av, ak;
+  la_common(aq, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, d_log_decay != nullptr, flags);
+  LaPass& p = aq.p[0];
   p.x = dp, p.xs = H * V, p.xh = V;
   p.y = vp, p.ys = v_stride, p.yh = v_head_stride;
   p.z = kp, p.zs = k_stride, p.zh = k_head_stride;
@@ -975,14 +981,7 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
     p.w = qp, p.ws = q_stride, p.wh = q_head_stride;
     p.rend = d_final;
     p.part = reinterpret_cast<float*>(ws + 4 * sb);
-    s = la_sweep<true>(a, V, false, st);
-    if (s != KDA_SUCCESS) return s;
-    s = launch(&la_reduce_kernel, H, 64, st, "linear attention decay", (const float*)p.part, d_log_decay,
-               (int)(a.nseg * a.slices));
-  } else {
-    s = la_sweep<false>(a, V, false, st);
   }
-  if (s != KDA_SUCCESS) return s;
 
   // dv: of k, q, do backwards in time, the state is dS; dk: of v, do, q, the state is dS^T
   LaPass pv{}, pk{};
@@ -1006,19 +1005,21 @@ kda_status_t kda_la_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, 
   }
   pv.seg = reinterpret_cast<float*>(ws + 2 * sb);
   pk.seg = reinterpret_cast<float*>(ws + 3 * sb);
-  if (K == V) {  // one launch: both read q and do
-    la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 2, false, flags);
-    a.p[0] = pv;
-    a.p[1] = pk;
-    return la_sweep<false>(a, K, d_initial_state && none, st);
-  }
-  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, V, 1, false, flags);
-  a.p[0] = pv;
-  s = la_sweep<false>(a, K, d_initial_state && none, st);
-  if (s != KDA_SUCCESS) return s;
-  la_common(a, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, false, flags);
-  a.p[0] = pk;
-  return la_sweep<false>(a, V, false, st);
+  const bool both = K == V;  // one launch: both read q and do
+  la_common(av, log_decay, cu_seqlens, B, T, H, K, V, N, V, both ? 2 : 1, false, flags);
+  la_common(ak, log_decay, cu_seqlens, B, T, H, K, V, N, K, 1, false, flags);
+  av.p[0] = pv;
+  av.p[1] = ak.p[0] = pk;
+
+  // nothing is enqueued unless all of it can be
+  const bool empties = d_initial_state && none;
+  if (!la_fits(aq, false) || !la_fits(av, empties) || !la_fits(ak, false)) return KDA_ERR_INVALID;
+  s = d_log_decay ? la_sweep<true>(aq, V, false, st) : la_sweep<false>(aq, V, false, st);
+  if (s == KDA_SUCCESS && d_log_decay)
+    s = launch(&la_reduce_kernel, H, 64, st, "linear attention decay", (const float*)aq.p[0].part, d_log_decay,
+               (int)(aq.nseg * aq.slices));
+  if (s == KDA_SUCCESS) s = la_sweep<false>(av, K, empties, st);
+  return s != KDA_SUCCESS || both ? s : la_sweep<false>(ak, V, false, st);
 }
 
 kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,
@@ -1031,7 +1032,7 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
   if (B * T > 0 && !out) return KDA_ERR_INVALID;
   if (!aligned_all(16, {out, initial_state, final_state})) return KDA_ERR_INVALID;
   if (same(q, out) || same(k, out) || same(v, out)) return KDA_ERR_INVALID;
-  if (T > 1 << 20 || B * H > ((int64_t)1 << 31) - 1) return KDA_ERR_INVALID;
+  if (T > 1 << 20 || !fits(B, H, most_groups(LT))) return KDA_ERR_INVALID;
   LaStep a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
            static_cast<uint16_t*>(out), log_decay, initial_state, final_state, q_stride, q_head_stride, k_stride,
            k_head_stride, v_stride, v_head_stride, scale, (int)T, (int)H};

@@ -200,15 +200,14 @@ inline size_t dtype_bytes(int dtype) { return dtype == 0 ? 2 : dtype == 1 ? 4 : 
 
 constexpr int64_t kMaxElements = (int64_t)1 << 46;  // of one token array; byte offsets stay in int64
 
-inline int64_t grid_of(int64_t items) {
-  const int64_t most = (int64_t)1 << 30;  // kernels that stride over their items
-  return items < 1 ? 1 : items < most ? items : most;
-}
+// Workgroups that a launch can have: HIP takes fewer than 2^32 threads in a dimension of the grid.
+inline int64_t most_groups(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
 
 kda_status_t launch_status(hipError_t err, const char* what);
 
 template <typename... P>
 inline kda_status_t launch(void (*fn)(P...), int64_t grid, int threads, hipStream_t st, const char* what, P... p) {
+  if (grid > most_groups(threads)) return KDA_ERR_INVALID;  // an entry point of several launches checks all of them first
   void* args[] = {(void*)&p...};
   return launch_status(
       hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)grid), dim3(threads), args, 0, st), what);
