@@ -698,8 +698,9 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
  * Tq and Tk are below 2^31, Hq is at most 2^15, and the heads of a group lie
  * within 2^30 elements: Hq / Hk q_head_stride + 33 q_stride is less.
  * A NaN or infinity stays within its own sequence and key head; in v it reaches
- * queries up to 63 tokens before its own, too (a tile's keys are multiplied
- * together, with weight zero).  Keys whose scores are all minus infinity weigh
+ * queries up to 94 tokens before the first that sees it, too (up to 63 where
+ * nq == nk): a tile's keys are multiplied together, with weight zero, by a tile's
+ * rows.  In k it reaches the queries that see it.  Keys whose scores are all minus infinity weigh
  * nothing, as if there were none.
  */
 size_t kda_attn_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N);
@@ -716,7 +717,9 @@ kda_status_t kda_attn_fwd(const void* q, int64_t q_stride, int64_t q_head_stride
  *   dq, dk, dv    [B, Tq, Hq, D], [B, Tk, Hk, D] twice, written, contiguous;
  *                 dk and dv are sums over the query heads of a key head
  * A NaN or infinity stays within its sequence and key head; it reaches tokens of
- * its tiles that the mask keeps from it (up to 127 before or behind), too.
+ * its tiles that the mask keeps from it, too: in k (dq) queries up to 158 before
+ * the first that sees it, in q and d_out (dk, dv) keys up to 158 behind the last
+ * one seen (127 both where nq == nk), in v what the forward says.
  *   workspace     >= kda_attn_bwd_workspace_size(B * Tq, B * Tk, Hq, Hk, D, N) bytes
  */
 size_t kda_attn_bwd_workspace_size(int64_t Tq_total, int64_t Tk_total, int64_t Hq, int64_t Hk, int64_t D, int64_t N);
