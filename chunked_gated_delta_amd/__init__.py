@@ -741,8 +741,8 @@ def kda_attn_fwd(q, k, v, scale, out, lse, workspace, out_lo=None, cu_seqlens_q=
     """Enqueue causal softmax attention on ``stream`` (default: torch's current stream): query i of a
     sequence of nq queries and nk keys sees the keys j <= i + nk - nq.
 
-    q bf16 [B,Tq,Hq,D], k, v bf16 [B,Tk,Hk,D], tokens and heads evenly apart, D 64 or 128, Hq a multiple
-    of Hk; out bf16 [B,Tq,Hq,D]; out_lo the same for kda_attn_bwd (what out's rounding took off), or
+    q bf16 [B,Tq,Hq,D], k, v bf16 [B,Tk,Hk,D], tokens and heads evenly apart (the first Tk rows of a longer
+    cache only with B = 1), D 64 or 128, Hq a multiple of Hk; out bf16 [B,Tq,Hq,D]; out_lo the same for kda_attn_bwd (what out's rounding took off), or
     None; lse fp32 [B,Tq,Hq]; workspace >= kda_attn_workspace_size(B*Tq, B*Tk, Hq,
     Hk, D, N) bytes (None if that is 0); cu_seqlens_q, cu_seqlens_k int32 [N+1] (the same one for prompts without a past)
     or None; flags 0 or FLAG_ZERO_REST."""

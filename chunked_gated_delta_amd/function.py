@@ -396,7 +396,9 @@ def kda_attn(q, k, v, *, scale=None, cu_seqlens=None, cu_seqlens_k=None):
     head h Hk / Hq), tokens and heads evenly apart (slices of one projection's output will do); ``scale``
     defaults to D^-1/2.  The queries are the last ones of their sequence: query i of nq sees the keys
     j <= i + nk - nq, so that Tk > Tq is a prompt or token behind a past.  cu_seqlens int32 [N+1] (with
-    B = 1) are the offsets of packed queries, and of the keys too unless cu_seqlens_k gives theirs.  A
+    B = 1) are the offsets of packed queries, and of the keys too unless cu_seqlens_k gives theirs.  The
+    keys of all sequences lie one after another: ``cache[:, :n]`` of a wider cache is taken with B = 1 and
+    refused with B > 1 (ValueError), where it has to be made contiguous first.  A
     query without keys, and rows behind the last sequence, come back as zeros with lse minus infinity.
     Gradients flow from both results.  All tensors on one GPU, unchanged until the backward, and on a
     boundary of 16 bytes, rows and heads too (KdaError otherwise).

@@ -611,6 +611,9 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
  *                 those of the one before) and between heads: multiples of 8
  *                 from 0 to 2^23, so that slices of one projection's output or
  *                 one head's rows for all heads will do.
+ *                 There is no stride between sequences: what is left free
+ *                 behind a sequence's tokens in a wider array (a cache that is
+ *                 not full) can only stand behind the last one's.
  *   alignment     16 bytes for token arrays, states and workspaces
  * A workspace belongs to one call at a time: calls (and graphs) that may
  * overlap need their own.
@@ -680,7 +683,10 @@ kda_status_t kda_la_step(const void* q, int64_t q_stride, int64_t q_head_stride,
  * s_ij = scale q_i.k_j over those,
  *     lse_i = log sum_j exp(s_ij),   out_i = sum_j exp(s_ij - lse_i) v_j.
  * A query that sees no key (nq > nk) gives zeros and lse = minus infinity, and
- * no gradient.  Decoding is the call with one query a sequence.
+ * no gradient.  Decoding is the call with one query a sequence: behind a cache of
+ * one sequence, or of several whose keys are packed one sequence after another.
+ * A cache [B, Tmax, Hk, D] of B > 1 sequences with fewer than Tmax keys each has
+ * to be copied into that form.
  *
  *   q, out        [B, Tq, Hq, D];  k, v [B, Tk, Hk, D];  D 64 or 128
  *   Hq            a multiple of Hk: query head h uses key head h Hk / Hq

@@ -2,8 +2,10 @@
 device work, so its pointers are never dereferenced)."""
 
 import pytest
+import torch
 
-from test_boundary_mixers import INVALID, P, at_bwd, at_fwd, la_bwd, la_fwd, la_step
+import chunked_gated_delta_amd as kda
+from test_boundary_mixers import INVALID, P, Meta, at_bwd, at_fwd, la_bwd, la_fwd, la_step
 
 M = 1 << 20
 
@@ -26,3 +28,19 @@ M = 1 << 20
 def test_more_threads_than_a_launch_has_are_refused(call, sizes):
     """Before the first of a call's launches: gradients are written by all of them or by none."""
     assert call(**sizes) == INVALID
+
+
+def test_the_first_keys_of_a_longer_cache(monkeypatch):
+    """Of one sequence they are taken as they lie; of several there is no stride between sequences, and they
+    are refused rather than read from the wrong rows."""
+    monkeypatch.setattr(kda, "_Call", Meta)
+    bf = torch.bfloat16
+    q, cache = torch.zeros(3, 1, 4, 64, dtype=bf), torch.zeros(3, 10, 2, 64, dtype=bf)
+    for k, v in ((cache[:, :7], cache[:, :7].contiguous()), (cache[:, :7].contiguous(), cache[:, :7])):
+        with pytest.raises(ValueError, match="evenly"):
+            kda._attn(q, k, v, None, None)
+    for k in (cache, cache[:, :7].contiguous(), cache[:, 9:], cache.transpose(1, 2).contiguous().transpose(1, 2)[:1, :7]):
+        _, sizes, p, _, _ = kda._attn(q[:len(k)], k, k, None, None)
+        at = {(b, t, h): k[b, t, h].data_ptr() for b in range(len(k)) for t in range(k.shape[1]) for h in range(2)}
+        assert all(p[3] + 2 * ((b * k.shape[1] + t) * p[4] + h * p[5]) == x for (b, t, h), x in at.items())
+        assert sizes == (len(k), 1, k.shape[1], 4, 2, 64, len(k))
