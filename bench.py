@@ -55,8 +55,8 @@ STATE_BYTES = 128 * 128 * 4
 _CSRC = os.path.join(ROOT, "chunked_gated_delta_amd", "csrc")
 _FWD_SRCS = ("kda_common.h", "kda_host.h", "kda_intra.hip", "kda_inter.hip", "kda_chain.h", "kda_chain.hip",
              "kda_api.hip")
-# the sources whose kernels each mode's counters measure (the build script too:
-# compile flags shape the kernels)
+# the sources whose kernels each mode's counters measure (their compile flags, which
+# shape the kernels, count too: kernel_source_hash)
 KERNEL_SRCS = {
     "fwd": _FWD_SRCS,
     "single": _FWD_SRCS,
@@ -79,11 +79,14 @@ WORKLOADS = {
 
 
 def kernel_source_hash(mode="fwd") -> str:
+    from chunked_gated_delta_amd import build
+
     h = hashlib.sha256()
-    for path in [os.path.join(_CSRC, f) for f in KERNEL_SRCS[mode]] + [
-            os.path.join(ROOT, "chunked_gated_delta_amd", "build.py")]:
-        with open(path, "rb") as f:
+    for name in KERNEL_SRCS[mode]:
+        with open(os.path.join(_CSRC, name), "rb") as f:
             h.update(f.read())
+        flags = [x for x in (*build.FLAGS, *build.SOURCE_FLAGS.get(name, ())) if not os.path.isabs(x)]
+        h.update("\0".join(flags).encode())
     return h.hexdigest()
 
 
