@@ -234,8 +234,9 @@ __device__ __forceinline__ void clear_rows(uint16_t* out, const Axis& ax, int64_
 // busy 51 % of the cycles, the exponentials and sums take about as many issue slots
 // as they do, and LDS reads (32 KB a wave and tile) as much time; the clock falls
 // as they overlap better (11 % fewer cycles by reading ahead saved 4.5 % of the
-// time).  Three waves a SIMD where D = 64 has registers for them (168): 89 us in
-// place of 95 on 16 ragged prompts in 16411 tokens, 12 heads.
+// time).  Three waves a SIMD where D = 64 has registers for them (168, all but one
+// value that goes to memory): 89 us in place of 95 on 16 ragged prompts in 16411
+// tokens, 12 heads.
 template <int D, int NW, int KT, bool SPLIT>
 __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : 2) attn_fwd_kernel(const AttnArgs a) {
   constexpr int NT = 64 * NW, BM = 32 * NW, ND = D / 16, NC = D / 32, NJ = KT / 32;
@@ -609,7 +610,8 @@ __global__ void __launch_bounds__(256, 2) attn_dq_kernel(const AttnArgs a) {
 // TFLOP/s of the four products).
 //
 // With few tiles (few key heads, whose groups make each tile's rows many) the rows
-// of a tile are split over workgroups, which leave fp32 sums to be added.
+// of a tile are split over workgroups, which leave fp32 sums to be added (for 128
+// channels one value a lane goes to memory there).
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(512, 2) attn_dkv_kernel(const AttnArgs a) {
   constexpr int NT = 256, BN = 128, RT = 32, ND = D / 16, NC = D / 32;
@@ -843,6 +845,10 @@ __global__ void __launch_bounds__(256) attn_sum_kernel(const AttnArgs a, int64_t
 //   behind 4096: 57, without this limit 73).  At most 64 (1 token behind 65535: 45,
 //   with 256 parts 53), of 128 or 256 keys at least (1 token of 8 heads on one key
 //   head behind 8191: 12.7, with 256 16.3; 24 tokens behind 8000: 20.2, with 128 22.4).
+// The host knows the mean of the keys alone, and every sequence gets as many parts.
+// Packed single tokens with very unequal keys wait for the longest: one of 131072
+// keys among 63 of 16 takes 1041 (by itself 104), 8 of 16384 among 56 of 16 148, where
+// 64 of 2064 take 110 and 64 of 1 to 4127 120.
 struct AttnPlan {
   int bm;
   int64_t slots;

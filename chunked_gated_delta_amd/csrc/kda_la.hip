@@ -34,14 +34,16 @@
 // would add errors as large as the output's own rounding; dropping the second
 // parts would save 9 % of the time.
 //
-// What bounds it.  The chain of steps: 2 x 4096 tokens are 64 steps one after
-// another whatever the card's width, and a step of two waves a SIMD (242 registers,
-// 58 KB of LDS) has two barriers.  A prompt of 32768 tokens of 96 heads of 128 takes
-// 0.92 ms in the second pass (3.2 GB: 3.5 TB/s; matrix cores busy 36 % of the
-// cycles, with five other vector instructions for each of theirs, and an eighth of
-// the cycles lost to LDS banks), 0.28 ms in the pass before it
-// that makes the segments' states, 0.01 ms in their join.  What cutting costs
-// is that pass: unsplit there were 192 workgroups for 512 places.
+// What bounds it.  Where chains are few, the steps: 2 x 4096 tokens are 64 steps
+// one after another whatever the card's width, and a step of two waves a SIMD (242
+// registers, 58 KB of LDS) has two barriers.  Where they are many, memory: a prompt
+// of 32768 tokens of 96 heads of 128 takes 0.92 ms in the second pass, in which the
+// L2s fetch 2.8 to 3.5 GB (its arrays are 2.4: the slices of z read the same rows of
+// x and y) and write 0.8: 4.0 to 4.6 TB/s, where a copy reaches 5.1 (matrix cores
+// busy 38 % of the cycles, with five other vector instructions for each of theirs).
+// The pass before it, that makes the segments' states, takes 0.28 ms, their join
+// 0.01.  What cutting costs is that pass: unsplit there were 192 workgroups for 512
+// places.
 
 #include "../../include/kda.h"
 #include "kda_mix.h"
@@ -51,12 +53,13 @@ namespace {
 
 constexpr int LC = 64;  // tokens of a step
 constexpr int LT = 256;  // threads
-// How sweeps are cut.  Measured, us: a prompt of 32768 tokens of 96 heads of 128
-// (forward), and training on 2 x 4096 of 12 (all gradients).
-constexpr int64_t kLaWant = 512;    // workgroups at a time, two per CU: 1291, 304 (256: 1521, 311; 1024: 1270, 342)
-constexpr int64_t kLaMost = 1024;   // workgroups that cutting leads to at most: 1267, 303 (2048: 1291, 304)
+// How sweeps are cut.  Measured, us, heads of 128: forward of 32768 tokens of 96
+// heads, and of 8192 of 32; training, all gradients, on 2 x 4096 tokens of 12, and on
+// 4 x 2048 of 16.  As it is: 1267, 118, 291, 342.
+constexpr int64_t kLaWant = 512;    // workgroups at a time, two per CU (256: 1491, 145, 296, 360; 1024: 1269, 138, 322, 389)
+constexpr int64_t kLaMost = 1024;   // workgroups that cutting leads to at most (512: 1382, 119, 289, 344; 2048: 1291, 120, 301, 345)
 constexpr int64_t kLaMinSteps = 4;  // steps of a segment at least: 2 and 8 took the same time; it bounds the workspace
-constexpr int64_t kLaAround = 3;    // steps that a workgroup's beginning and end cost: 1291, 304 (0: 1297, 358)
+constexpr int64_t kLaAround = 3;    // steps that a workgroup's beginning and end cost (0: 1271, 119, 322, 357; 8: 1266, 119, 291, 346)
 
 // One sweep.  State element (d, c) of sequence n and head h is at
 // (n H + h) K V + d sr + c sc.
@@ -216,6 +219,9 @@ __global__ void __launch_bounds__(LT, DG && OUT ? 1 : 2) la_sweep_kernel(const L
 
   // ---- this workgroup's place.  Ids that agree mod 8 run on one XCD: the
   // slices and passes of an item, which read the same rows, are neighbours there.
+  // Nothing keeps them in step, so that the L2 serves only part of what they share:
+  // two slices fetch 1.2 to 1.4 times their three arrays, the four workgroups of dk
+  // and dv 2.1 times their four (2.5 would be without any sharing).
   const int id = blockIdx.x;
   const int kinds = a.slices * a.passes;
   const int item = id / 8 / kinds * 8 + id % 8;
