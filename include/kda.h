@@ -618,7 +618,7 @@ kda_status_t kda_qk_rope_bwd(const void* q, int64_t q_stride, int64_t q_head_str
  * A workspace belongs to one call at a time: calls (and graphs) that may
  * overlap need their own.
  * A launch has fewer than 2^32 threads.  A call that needs more is refused
- * (KDA_ERR_INVALID) before anything is enqueued; 2^21 sequences times heads, in
+ * (KDA_ERR_INVALID) before anything is enqueued; 2^20 sequences times heads, in
  * attention each with its tiles of 128 rows or keys, always fit.
  */
 
